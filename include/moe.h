@@ -4,6 +4,8 @@
  *
  * Path: router softmax + top-k  ->  token-to-expert alignment  ->
  *       FC1 (gate|up) + SiLU-and-mul  ->  FC2 (down)  ->  top-k weighted combine.
+ * Around it: the norms before and after the block (residual add, shared
+ * expert, combine), the router projection, low-rank adapters of many requests.
  *
  * Sources (web pages; cited by title and section):
  *  - "vLLM support for NVIDIA Vera Rubin NVL72" (Chinese summary), section
@@ -393,6 +395,140 @@ moe_status moe_forward_small_static(const float* logits, const uint16_t* x, cons
                                     int T, int E, int H, int I, int k, int renormalize,
                                     int dtype, unsigned flags, int32_t* topk_ids,
                                     float* topk_weights, uint16_t* out, moe_stream_t stream);
+
+/*
+ * Around the FFN: the norms before and after it, the router projection and
+ * low-rank adapters. These steps are not in the pages; their formulas are
+ * stated here in full. Arithmetic and sums are fp32; each output is rounded
+ * once (RNE) from the fp32 value.
+ */
+
+/*
+ * Norm before the block, with the residual add in front of it:
+ *   s[t]   = residual[t] + alpha * x[t]        (alpha * x[t] without residual)
+ *   out[t] = s[t] / sqrt(mean_c(s[t]^2) + eps) * weight
+ *   residual_out[t] = s[t]
+ * The norm takes the unrounded s.
+ *
+ *  x, residual, residual_out, out   [T, H] of `dtype` (MOE_DTYPE_BF16 or
+ *                MOE_DTYPE_F32); residual and residual_out may be NULL.
+ *                out or residual_out may be the buffer of x or of residual
+ *                (each element is read before it is written), not each other's.
+ *  weight        [H] float32.
+ *  Limits: 0 <= T < 2^24, H a multiple of 8 (MOE_DTYPE_F32: 4) and at most
+ *  MOE_NORM_MAX_H, eps finite and >= 0 (MOE_ERR_UNSUPPORTED otherwise; with
+ *  eps = 0 a zero row gives NaN); all pointers 16-byte aligned. A row whose
+ *  sum of squares leaves the fp32 range is outside the contract.
+ */
+#define MOE_NORM_MAX_H 16384
+moe_status moe_norm_in(const void* x, const void* residual, const float* weight, float alpha,
+                       float eps, int T, int H, int dtype, void* residual_out, void* out,
+                       moe_stream_t stream);
+
+/*
+ * Norm after the block, with the combine in front of it and the residual add
+ * and the next block's norm behind it, in one pass over the experts' outputs
+ * (it takes the place of MOE_FFN_STAGE_COMBINE):
+ *   v[t] = sum_j topk_weights[t,j] * y[t*k+j]  + sigmoid(gate[t]) * shared[t]
+ *   n[t] = weight ? v[t] / sqrt(mean_c(v[t]^2) + eps) * weight : v[t]
+ *   o[t] = residual[t] + scale * n[t]
+ *   out[t]  = o[t]
+ *   next[t] = o[t] / sqrt(mean_c(o[t]^2) + eps) * next_weight
+ * The sum over j runs in ascending j; nothing is rounded before out and next.
+ *
+ *  y             [T*k, H] of y_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32): for
+ *                instance the y of an FFN workspace after MOE_FFN_STAGE_FC2
+ *                (moe_ffn_intermediates).
+ *  topk_weights  [T, k] float32; NULL for k = 1: weight 1.
+ *  topk_ids      [T, k] int32 or NULL. A slot whose id is outside [0, E) is
+ *                served by another shard: it adds nothing and its row of y is
+ *                not read. NULL: every slot counts and E is ignored.
+ *  shared        [T, H] or NULL: the output of an expert every token takes;
+ *  gate          [T] float32 or NULL (factor 1): its gate, before the sigmoid
+ *                (MOE_ERR_NULL for a gate without shared).
+ *  residual      [T, H] or NULL (0).
+ *  weight        [H] float32 or NULL: no norm of v.
+ *  next_weight   [H] float32 and next [T, H], both given or both NULL.
+ *  out           [T, H], written.
+ *  shared, residual, out and next are of `dtype` (MOE_DTYPE_BF16 or _F32).
+ *  out or next may be the buffer of residual or of shared, not each other's,
+ *  and do not overlap y.
+ *  Limits: k >= 1, 0 <= T, T * k < 2^24, 1 <= E when topk_ids is given (k may
+ *  exceed E: a small shard), H, eps and alignment as moe_norm_in (H a multiple
+ *  of 4 only when y_dtype and dtype are both MOE_DTYPE_F32); topk_weights,
+ *  topk_ids and gate 4-byte aligned.
+ */
+moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
+                        const float* topk_weights, const void* shared, const float* gate,
+                        const void* residual, const float* weight, const float* next_weight,
+                        float scale, float eps, int T, int E, int H, int k, int dtype, void* out,
+                        void* next, moe_stream_t stream);
+
+/*
+ * Router projection: logits[t, e] = sum_c x[t, c] * w[e, c] + bias[e], in
+ * fp32 from the operands' own values: what moe_route_topk takes.
+ *
+ *  x             [T, H] of x_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *  w             [E, H] of w_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32; fp32 when
+ *                x is fp32, MOE_ERR_UNSUPPORTED otherwise).
+ *  bias          [E] float32 or NULL.
+ *  logits        [T, E] float32, written.
+ *  Limits: 0 <= T, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8; x and w
+ *  16-byte, bias and logits 4-byte aligned. The result is deterministic.
+ *  Infinities and NaN in x or w make the logits that read them non-finite.
+ */
+moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
+                             const float* bias, int T, int E, int H, float* logits,
+                             moe_stream_t stream);
+
+/*
+ * Low-rank adapters of many requests beside a projection they share:
+ *   out[s] = y[s] + scale[g] * b[g] (a[g] x[s])   for every row s of adapter g;
+ * rows without an adapter are neither read nor written. y is what the shared
+ * projection gave, for instance any dense projection of S tokens (k = 1
+ * alignment of the tokens' adapter ids), or the experts' down projection
+ * inside an FFN workspace between MOE_FFN_STAGE_FC2 and the combine (x = h,
+ * ids = adapter * E + expert of every slot; moe_ffn_intermediates).
+ *
+ *  x             [S, K] of x_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row
+ *                stride ldx elements.
+ *  a             [n, r, K] bf16; b [n, N, r] bf16; scale [n] float32 or NULL
+ *                (1). Adapters of lower rank are padded with zeros to r.
+ *  sorted_ids, block_adapter, num_padded   from moe_align_block on the rows'
+ *                adapter ids with E = n and the same block_m; an id outside
+ *                [0, n) marks a row without an adapter. One alignment serves
+ *                every projection of a step.
+ *  y             [S, N] of y_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row
+ *                stride ldy elements; out likewise with stride ldo; out = y
+ *                with equal strides updates in place; otherwise they do not
+ *                overlap.
+ *  workspace     moe_lora_workspace_bytes(S, n, K, r, block_m) bytes (or
+ *                more), 256-byte aligned, no initialisation needed.
+ *  The rank-r intermediate is kept in fp32; products of bf16 factors are
+ *  exact and summed in fp32. The result is deterministic.
+ *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8, r a multiple
+ *  of 8 in [8, 256], block_m a power of two in [1, 256]; ldx >= K, ldy and
+ *  ldo >= N, each a multiple of 8 (of 4 for fp32); x, a, b, y and out 16-byte
+ *  aligned, scale and the lists 4-byte. S == 0 launches nothing.
+ */
+size_t moe_lora_workspace_bytes(int S, int n, int K, int r, int block_m);
+moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const uint16_t* a,
+                        const uint16_t* b, const float* scale, const int32_t* sorted_ids,
+                        const int32_t* block_adapter, const int32_t* num_padded, int S, int n,
+                        int K, int N, int r, int block_m, void* workspace,
+                        size_t workspace_bytes, const void* y, int y_dtype, size_t ldy, void* out,
+                        size_t ldo, moe_stream_t stream);
+
+/*
+ * Where an FFN workspace keeps h [T*k, I] and y [T*k, H] (both indexed by flat
+ * slot) and in which type (MOE_DTYPE_BF16 or MOE_DTYPE_F32), for the FFN call
+ * of that dtype and block_m: byte offsets from the workspace's base. h holds
+ * after MOE_FFN_STAGE_FC1, y after MOE_FFN_STAGE_FC2 (rows of slots whose id
+ * lies outside [0, E) are not written). Returns MOE_ERR_SHAPE or
+ * MOE_ERR_UNSUPPORTED where that FFN call would.
+ */
+moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, int block_m, int dtype,
+                                 size_t* h_offset, int* h_dtype, size_t* y_offset, int* y_dtype);
 
 #ifdef __cplusplus
 }

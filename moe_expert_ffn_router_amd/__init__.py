@@ -17,6 +17,11 @@ The names mirror the C ABI in include/moe.h:
     forward(x, logits, w1, w2, k, ...)   convenience chaining of the three calls
     forward_small(logits, x, w1, w2, k, ...) -> (out, topk_ids, topk_weights)   one launch, T <= 16
     forward_small_static(logits, x, w1, w2, k, ...)   the same without a workspace (allocates nothing)
+    norm_in(x, weight, residual=None, ...) -> (out, residual_out)      residual add + norm before the block
+    router_logits(x, w, bias=None, ...)    -> logits                   router projection
+    lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m, ...) -> out   adapters of many requests
+    norm_out(y, topk_weights, ...)         -> (out, next)              combine + shared expert + norms + residual
+    ffn_intermediates(workspace, ...)      -> (h, y)                   an FFN workspace's tensors, for the two above
 """
 from __future__ import annotations
 
@@ -42,7 +47,9 @@ EXPORTS = ("moe_status_str", "moe_abi_version", "moe_route_topk", "moe_align_cap
            "moe_align_block", "moe_route_align", "moe_default_block_m",
            "moe_ffn_workspace_bytes", "moe_ffn_bf16", "moe_ffn_fp8", "moe_ffn_w8a16",
            "moe_ffn_fp8_block", "moe_ffn_f32", "moe_small_max_tokens",
-           "moe_forward_small_workspace_bytes", "moe_forward_small", "moe_forward_small_static")
+           "moe_forward_small_workspace_bytes", "moe_forward_small", "moe_forward_small_static",
+           "moe_norm_in", "moe_norm_out", "moe_router_logits", "moe_lora_workspace_bytes",
+           "moe_lora_add", "moe_ffn_intermediates")
 STATIC_SCRATCH_BYTES = 32 << 20  # MOE_STATIC_SCRATCH_BYTES
 
 
@@ -59,7 +66,8 @@ def _load() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() "
                           "(or python moe_expert_ffn_router_amd/build.py)")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I, U, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+    P, I, U, Z, F = (ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t,
+                     ctypes.c_float)
     lib.moe_status_str.restype = ctypes.c_char_p
     lib.moe_status_str.argtypes = [I]
     lib.moe_abi_version.restype = I
@@ -95,6 +103,19 @@ def _load() -> ctypes.CDLL:
     lib.moe_forward_small.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, U, P, P, P, Z, P, P]
     lib.moe_forward_small_static.restype = I
     lib.moe_forward_small_static.argtypes = [P, P, P, P, P, P, I, I, I, I, I, I, I, U, P, P, P, P]
+    lib.moe_norm_in.restype = I
+    lib.moe_norm_in.argtypes = [P, P, P, F, F, I, I, I, P, P, P]
+    lib.moe_norm_out.restype = I
+    lib.moe_norm_out.argtypes = [P, I, P, P, P, P, P, P, P, F, F, I, I, I, I, I, P, P, P]
+    lib.moe_router_logits.restype = I
+    lib.moe_router_logits.argtypes = [P, I, P, I, P, I, I, I, P, P]
+    lib.moe_lora_workspace_bytes.restype = Z
+    lib.moe_lora_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.moe_lora_add.restype = I
+    lib.moe_lora_add.argtypes = [P, I, Z, P, P, P, P, P, P, I, I, I, I, I, I, P, Z, P, I, Z, P, Z,
+                                 P]
+    lib.moe_ffn_intermediates.restype = I
+    lib.moe_ffn_intermediates.argtypes = [I, I, I, I, I, I, I, P, P, P, P]
     if lib.moe_abi_version() != ABI_VERSION:
         raise ImportError(f"libmoe ABI {lib.moe_abi_version()} != binding ABI {ABI_VERSION}")
     return lib
@@ -514,3 +535,225 @@ def forward_small_static(logits, x, w1, w2, k: int, renormalize: bool = False, w
         _ptr(w2_scale) if fp8 else None, T, E, H, I, k, 1 if renormalize else 0, dtype, flags,
         _ptr(topk_ids), _ptr(topk_weights), _ptr(out), _stream(stream)))
     return out, topk_ids, topk_weights
+
+
+# ------------------------------------------------------- around the FFN ---
+
+_ACT = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+
+
+def _act(t: torch.Tensor, name: str) -> int:
+    """The library's dtype code of an activation tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _ACT.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(_ACT)}")
+    return code
+
+
+def _launch_stream(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+    """The stream a call on tensors of ``dev`` runs on. The library launches on
+    the current device, so its tensors (and a stream that is passed) are there."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors are on {dev}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype, dev, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor for a call on ``stream``, allocated there: memory that
+    another stream still uses cannot be handed to it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _need_rows(t: torch.Tensor, name: str, dtypes, device=None, shape=None) -> int:
+    """Check a matrix of contiguous rows that may lie apart (a slice of columns
+    of a wider one): a device tensor of one of ``dtypes`` with stride 1 along the
+    rows. Returns its row stride in elements."""
+    rows, cols = _dims(t, name, 2)
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device (cuda/hip) tensor, got {t.device}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} has shape {(rows, cols)}, expected {shape}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+    if rows <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} overlap: strides {t.stride()}")
+    return t.stride(0)
+
+
+def norm_in(x, weight, residual=None, alpha: float = 1.0, eps: float = 1e-6, out=None,
+            residual_out=None, stream=None, prepare: bool = False):
+    """moe_norm_in: s = residual + alpha * x; out = RMS norm of s times ``weight``;
+    residual_out = s. x, residual [T, H] bfloat16 or float32, weight [H] float32.
+    Returns (out, residual_out); residual_out is None (and s not stored) without
+    a residual unless a buffer is given. out or residual_out may be x or
+    residual itself."""
+    T, H = _dims(x, "x", 2)
+    code = _act(x, "x")
+    dev, like = x.device, (x.dtype,)
+    _need(x, "x", like)
+    _need(weight, "weight", (torch.float32,), dev, (H,))
+    if residual is not None:
+        _need(residual, "residual", like, dev, (T, H))
+    raw = _launch_stream(dev, stream)
+    if residual_out is not None:
+        _need(residual_out, "residual_out", like, dev, (T, H))
+    elif residual is not None:
+        residual_out = _empty((T, H), x.dtype, dev, stream)
+    if out is None:
+        out = _empty((T, H), x.dtype, dev, stream)
+    else:
+        _need(out, "out", like, dev, (T, H))
+    keep = (x, weight, residual, out, residual_out)
+    args = (_ptr(x), _ptr(residual), _ptr(weight), alpha, eps, T, H, code, _ptr(residual_out),
+            _ptr(out), raw)
+    return _run(lib.moe_norm_in, args, keep, prepare, (out, residual_out))
+
+
+def norm_out(y, topk_weights=None, topk_ids=None, num_experts: Optional[int] = None, shared=None,
+             gate=None, residual=None, weight=None, next_weight=None, scale: float = 1.0,
+             eps: float = 1e-6, dtype=None, out=None, next_out=None, stream=None,
+             prepare: bool = False):
+    """moe_norm_out: v = sum_j topk_weights[t, j] * y[t*k+j] + sigmoid(gate) * shared;
+    out = residual + scale * (RMS norm of v times ``weight``, or v without it);
+    next = RMS norm of the unrounded out times ``next_weight``.
+
+    y [T*k, H] (or [T, k, H]) bfloat16 or float32; topk_weights, topk_ids [T, k]
+    (k = 1 and weight 1 without topk_weights); slots with an id outside
+    [0, num_experts) add nothing. shared, residual [T, H] of one type (``dtype``,
+    by default theirs, else y's), gate [T], weight, next_weight [H] float32.
+    Returns (out, next); next is None without next_weight."""
+    code_y = _act(y, "y")
+    _need(y, "y", (y.dtype,))
+    dev, H = y.device, y.shape[-1]
+    if topk_weights is None:
+        T, k = y.numel() // H if H else 0, 1
+    else:
+        T, k = _dims(topk_weights, "topk_weights", 2)
+        _need(topk_weights, "topk_weights", (torch.float32,), dev, (T, k))
+    if tuple(y.shape) != (T * k, H) and tuple(y.shape) != (T, k, H):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected {(T * k, H)} or {(T, k, H)}")
+    if topk_ids is not None:
+        _need(topk_ids, "topk_ids", (torch.int32,), dev, (T, k))
+        if num_experts is None:
+            raise ValueError("topk_ids needs num_experts")
+    if dtype is None:
+        dtype = next((t.dtype for t in (residual, shared, out) if t is not None), y.dtype)
+    if dtype not in _ACT:
+        raise TypeError(f"dtype is {dtype}, expected one of {tuple(_ACT)}")
+    for name, t in (("shared", shared), ("residual", residual), ("out", out),
+                    ("next_out", next_out)):
+        if t is not None:
+            _need(t, name, (dtype,), dev, (T, H))
+    if gate is not None:
+        _need(gate, "gate", (torch.float32,), dev, (T,))
+    for name, t in (("weight", weight), ("next_weight", next_weight)):
+        if t is not None:
+            _need(t, name, (torch.float32,), dev, (H,))
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out = _empty((T, H), dtype, dev, stream)
+    if next_out is None and next_weight is not None:
+        next_out = _empty((T, H), dtype, dev, stream)
+    keep = (y, topk_ids, topk_weights, shared, gate, residual, weight, next_weight, out, next_out)
+    args = (_ptr(y), code_y, _ptr(topk_ids), _ptr(topk_weights), _ptr(shared), _ptr(gate),
+            _ptr(residual), _ptr(weight), _ptr(next_weight), scale, eps, T, num_experts or 0, H,
+            k, _ACT[dtype], _ptr(out), _ptr(next_out), raw)
+    return _run(lib.moe_norm_out, args, keep, prepare, (out, next_out))
+
+
+def router_logits(x, w, bias=None, out=None, stream=None, prepare: bool = False):
+    """moe_router_logits: logits [T, E] float32 = x [T, H] @ w [E, H]^T + bias [E].
+    x bfloat16 with w bfloat16 or float32, or both float32."""
+    T, H = _dims(x, "x", 2)
+    E = _dims(w, "w", 2)[0]
+    code_x, code_w = _act(x, "x"), _act(w, "w")
+    dev = x.device
+    _need(x, "x", (x.dtype,))
+    _need(w, "w", (w.dtype,), dev, (E, H))
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), dev, (E,))
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out = _empty((T, E), torch.float32, dev, stream)
+    else:
+        _need(out, "out", (torch.float32,), dev, (T, E))
+    keep = (x, w, bias, out)
+    args = (_ptr(x), code_x, _ptr(w), code_w, _ptr(bias), T, E, H, _ptr(out), raw)
+    return _run(lib.moe_router_logits, args, keep, prepare, out)
+
+
+def lora_workspace_bytes(S: int, n: int, K: int, r: int, block_m: int) -> int:
+    return int(lib.moe_lora_workspace_bytes(S, n, K, r, block_m))
+
+
+def lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m: int, scale=None,
+             out=None, workspace=None, stream=None, prepare: bool = False):
+    """moe_lora_add: out[s] = y[s] + scale[g] * b[g] (a[g] x[s]) for the rows s of
+    adapter g in the lists (align_block of the rows' adapter ids [S, 1], or of
+    any ids whose flat slots are the rows); the other rows of ``out`` are left as
+    they are. x [S, K], y [S, N] bfloat16 or float32, a [n, r, K], b [n, N, r]
+    bfloat16, scale [n] float32. ``out`` defaults to y (in place). x, y and out
+    may be column slices of wider matrices."""
+    S, K = _dims(x, "x", 2)
+    n, r, _ = _dims(a, "a", 3)
+    N = _dims(y, "y", 2)[1]
+    code_x, code_y = _act(x, "x"), _act(y, "y")
+    dev = x.device
+    ldx = _need_rows(x, "x", (x.dtype,))
+    ldy = _need_rows(y, "y", (y.dtype,), dev, (S, N))
+    _need(a, "a", (torch.bfloat16,), dev, (n, r, K))
+    _need(b, "b", (torch.bfloat16,), dev, (n, N, r))
+    if scale is not None:
+        _need(scale, "scale", (torch.float32,), dev, (n,))
+    _align_outputs((sorted_ids, block_adapter, num_padded), S, 1, n, block_m, dev)
+    if out is None:
+        out, ldo = y, ldy
+    else:
+        ldo = _need_rows(out, "out", (y.dtype,), dev, (S, N))
+    raw = _launch_stream(dev, stream)
+    need = lora_workspace_bytes(S, n, K, r, block_m)
+    if workspace is None:
+        workspace = _empty(max(need, 256), torch.uint8, dev, stream)
+    else:
+        _need(workspace, "workspace", (torch.uint8,), dev, min_numel=need)
+    keep = (y, x, a, b, sorted_ids, block_adapter, num_padded, scale, out, workspace)
+    args = (_ptr(x), code_x, ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(sorted_ids),
+            _ptr(block_adapter), _ptr(num_padded), S, n, K, N, r, block_m, _ptr(workspace),
+            workspace.numel(), _ptr(y), code_y, ldy, _ptr(out), ldo, raw)
+    return _run(lib.moe_lora_add, args, keep, prepare, out)
+
+
+def ffn_intermediates(workspace, T: int, E: int, H: int, I: int, k: int, block_m: int,
+                      dtype: int) -> Tuple[torch.Tensor, torch.Tensor]:
+    """moe_ffn_intermediates: the h [T*k, I] and y [T*k, H] that the FFN call of
+    ``dtype`` (MOE_DTYPE_*) and block_m keeps in ``workspace``, as views of it
+    (bfloat16 or float32)."""
+    h_at, y_at = ctypes.c_size_t(), ctypes.c_size_t()
+    h_dt, y_dt = ctypes.c_int(), ctypes.c_int()
+    _check(lib.moe_ffn_intermediates(T, E, H, I, k, block_m, dtype, ctypes.byref(h_at),
+                                     ctypes.byref(h_dt), ctypes.byref(y_at), ctypes.byref(y_dt)))
+    _need(workspace, "workspace", (torch.uint8,),
+          min_numel=workspace_bytes(T, E, H, I, k, block_m, dtype))
+
+    def view(at, code, cols):
+        t = torch.bfloat16 if code.value == MOE_DTYPE_BF16 else torch.float32
+        size = 2 if code.value == MOE_DTYPE_BF16 else 4
+        return workspace[at.value:at.value + T * k * cols * size].view(t).view(T * k, cols)
+
+    return view(h_at, h_dt, I), view(y_at, y_dt, H)

@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe.so")
-SOURCES = ["moe_api.hip", "moe_route.hip", "moe_align.hip", "moe_ffn.hip", "moe_gemm.hip"]
+SOURCES = ["moe_api.hip", "moe_route.hip", "moe_align.hip", "moe_ffn.hip", "moe_gemm.hip",
+           "moe_norm.hip", "moe_router.hip", "moe_lora.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 CFLAGS = [

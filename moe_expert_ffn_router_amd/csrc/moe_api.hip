@@ -326,3 +326,142 @@ MOE_EXPORT moe_status moe_ffn_f32(const float* x, const float* w1, const float* 
               num_padded, T, E, H, I, k, block_m, flags, workspace, out),
       (hipStream_t)stream));
 }
+
+// ---------------------------------------------------- around the FFN ---
+
+namespace {
+
+bool bf16_or_f32(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F32; }
+size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
+
+// Rows and row length of a norm; mult: what H is a multiple of.
+moe_status check_norm(int T, int H, int mult, float eps) {
+  if (T < 0 || (long)T >= kMaxSlots) return MOE_ERR_SHAPE;
+  if (H < mult || H % mult != 0 || H > MOE_NORM_MAX_H) return MOE_ERR_SHAPE;
+  if (!(eps >= 0.f) || eps > 3.0e38f) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+MOE_EXPORT moe_status moe_norm_in(const void* x, const void* residual, const float* weight,
+                                  float alpha, float eps, int T, int H, int dtype,
+                                  void* residual_out, void* out, moe_stream_t stream) {
+  static_assert(moe::kNormMaxH == MOE_NORM_MAX_H, "row length");
+  if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_norm(T, H, dtype == MOE_DTYPE_F32 ? 4 : 8, eps);
+  if (s != MOE_OK || T == 0) return s;
+  if (!x || !weight || !out) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(residual_out, 16) || !aligned(out, 16))
+    return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_norm_in(
+      moe::NormInProblem{x, residual, weight, alpha, eps, T, H, dtype, residual_out, out},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
+                                   const float* topk_weights, const void* shared,
+                                   const float* gate, const void* residual, const float* weight,
+                                   const float* next_weight, float scale, float eps, int T, int E,
+                                   int H, int k, int dtype, void* out, void* next,
+                                   moe_stream_t stream) {
+  if (!bf16_or_f32(dtype) || !bf16_or_f32(y_dtype)) return MOE_ERR_UNSUPPORTED;
+  const int mult = dtype == MOE_DTYPE_F32 && y_dtype == MOE_DTYPE_F32 ? 4 : 8;
+  moe_status s = check_norm(T, H, mult, eps);
+  if (s != MOE_OK) return s;
+  if (k < 1 || (long)T * k >= kMaxSlots || (topk_ids && E < 1)) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!y || !out || (!topk_weights && k > 1) || (gate && !shared) || !next != !next_weight)
+    return MOE_ERR_NULL;
+  if (!aligned(y, 16) || !aligned(shared, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
+      !aligned(next_weight, 16) || !aligned(out, 16) || !aligned(next, 16) ||
+      !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(gate, 4))
+    return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_norm_out(
+      moe::NormOutProblem{y, y_dtype, topk_ids, topk_weights, shared, gate, residual, weight,
+                          next_weight, scale, eps, T, E, H, k, dtype, out, next},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
+                                        const float* bias, int T, int E, int H, float* logits,
+                                        moe_stream_t stream) {
+  if (!bf16_or_f32(x_dtype) || !bf16_or_f32(w_dtype) ||
+      (x_dtype == MOE_DTYPE_F32 && w_dtype != MOE_DTYPE_F32))
+    return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_common(T, E, 1);
+  if (s != MOE_OK) return s;
+  if (H < 8 || H % 8 != 0) return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !logits) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(logits, 4))
+    return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_router_logits(x, x_dtype, w, w_dtype, bias, T, E, H, logits,
+                                              (hipStream_t)stream));
+}
+
+static moe_status check_lora(int S, int n, int K, int r, int block_m) {
+  if (S < 0 || (long)S >= kMaxSlots || n < 1 || n > kMaxE) return MOE_ERR_SHAPE;
+  if (K < 8 || K % 8 != 0 || r < 8 || r % 8 != 0 || r > 256) return MOE_ERR_SHAPE;
+  if (!is_pow2_le256(block_m)) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+MOE_EXPORT size_t moe_lora_workspace_bytes(int S, int n, int K, int r, int block_m) {
+  if (check_lora(S, n, K, r, block_m) != MOE_OK) return 0;
+  return moe::lora_workspace_bytes(S, n, K, r, block_m);
+}
+
+MOE_EXPORT moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const uint16_t* a,
+                                   const uint16_t* b, const float* scale,
+                                   const int32_t* sorted_ids, const int32_t* block_adapter,
+                                   const int32_t* num_padded, int S, int n, int K, int N, int r,
+                                   int block_m, void* workspace, size_t workspace_bytes,
+                                   const void* y, int y_dtype, size_t ldy, void* out, size_t ldo,
+                                   moe_stream_t stream) {
+  if (!bf16_or_f32(x_dtype) || !bf16_or_f32(y_dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_lora(S, n, K, r, block_m);
+  if (s != MOE_OK) return s;
+  const size_t mx = 16 / elem_bytes(x_dtype), my = 16 / elem_bytes(y_dtype);
+  if (N < 8 || N % 8 != 0) return MOE_ERR_SHAPE;
+  if (ldx < (size_t)K || ldy < (size_t)N || ldo < (size_t)N || ldx % mx != 0 || ldy % my != 0 ||
+      ldo % my != 0)
+    return MOE_ERR_SHAPE;
+  if (S == 0) return MOE_OK;
+  if (!x || !a || !b || !sorted_ids || !block_adapter || !num_padded || !workspace || !y || !out)
+    return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(y, 16) ||
+      !aligned(out, 16) || !aligned(scale, 4) || !aligned(sorted_ids, 4) ||
+      !aligned(block_adapter, 4) || !aligned(num_padded, 4) || !aligned(workspace, 256))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes < moe::lora_workspace_bytes(S, n, K, r, block_m)) return MOE_ERR_WORKSPACE;
+  return hip_status(moe::launch_lora_add(
+      moe::LoraProblem{x, x_dtype, ldx, a, b, scale, sorted_ids, block_adapter, num_padded, S, n,
+                       K, N, r, block_m, workspace, y, y_dtype, ldy, out, ldo},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, int block_m,
+                                            int dtype, size_t* h_offset, int* h_dtype,
+                                            size_t* y_offset, int* y_dtype) {
+  if (!h_offset || !h_dtype || !y_offset || !y_dtype) return MOE_ERR_NULL;
+  int mult = 8;
+  if (dtype == MOE_DTYPE_F32) mult = 4;
+  else if (dtype == MOE_DTYPE_W8A16 || dtype == MOE_DTYPE_FP8_BLOCK) mult = 128;
+  else if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP8) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_common(T, E, k);
+  if (s != MOE_OK) return s;
+  if (H < mult || I < mult || H % mult != 0 || I % mult != 0) return MOE_ERR_SHAPE;
+  if (!is_pow2_le256(block_m)) return MOE_ERR_SHAPE;
+  // W8A16 keeps the bf16 path's intermediates, the W8A8 grouped-GEMM tiles
+  // leave theirs in bf16 in the places of the fp32 ones
+  const int layout = dtype == MOE_DTYPE_W8A16 ? MOE_DTYPE_BF16 : dtype;
+  const bool bf16 = layout == MOE_DTYPE_BF16 ||
+                    (dtype == MOE_DTYPE_FP8 && moe::fp8_dense(H, I, block_m));
+  const moe::FfnWorkspace L = moe::ffn_workspace_layout(T, E, H, I, k, layout);
+  *h_offset = L.h_off;
+  *y_offset = L.y_off;
+  *h_dtype = *y_dtype = bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
+  return MOE_OK;
+}

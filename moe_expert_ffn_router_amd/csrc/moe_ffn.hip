@@ -2990,9 +2990,8 @@ hipError_t launch_ffn_fp8(const FfnProblem& p, hipStream_t stream) {
   float* y = (float*)(ws + L.y_off);
   int* queue = (int*)(ws + L.q_off);    // FC1: [0, 8), FC2: [8, 16)
   const bool hot = p.T > 2 * kColdMax;  // see run_quads
-  // prefill-sized blocks: the grouped-GEMM tiles on fp8 MFMA (two 128-code
-  // chunks of K at least)
-  const bool dense = p.block_m >= 128 && p.H >= 256 && p.I >= 256;
+  // prefill-sized blocks: the grouped-GEMM tiles on fp8 MFMA
+  const bool dense = fp8_dense(p.H, p.I, p.block_m);
   hipError_t err;
   if ((dense || hot) && (st & MOE_FFN_STAGE_PREP)) {  // (FC2 without PREP: finish_queue)
     zero_counters_kernel<<<1, 64, 0, stream>>>(queue, kQueueInts);

@@ -124,4 +124,66 @@ constexpr size_t kStaticScratchBytes = (size_t)32 << 20;
 hipError_t static_scratch(void** ptr);
 hipError_t launch_ffn_f32(const FfnProblem& p, hipStream_t stream);
 
+// Whether the W8A8 FFN runs its grouped-GEMM tiles (which keep h and y in bf16)
+// for this problem: prefill-sized blocks and two 128-code chunks of K at least.
+inline bool fp8_dense(int H, int I, int block_m) {
+  return H % 128 == 0 && I % 128 == 0 && block_m >= 128 && H >= 256 && I >= 256;
+}
+
+// Norms around the block (moe_norm.hip). DType is MOE_DTYPE_BF16 or _F32.
+constexpr int kNormMaxH = 16384;
+struct NormInProblem {
+  const void* x;
+  const void* residual;  // may be null
+  const float* weight;
+  float alpha, eps;
+  int T, H, dtype;
+  void* residual_out;  // may be null
+  void* out;
+};
+hipError_t launch_norm_in(const NormInProblem& p, hipStream_t stream);
+struct NormOutProblem {
+  const void* y;
+  int y_dtype;
+  const int32_t* topk_ids;   // null: every slot counts
+  const float* topk_weights;  // null: 1 (k = 1)
+  const void* shared;         // may be null
+  const float* gate;          // may be null
+  const void* residual;       // may be null
+  const float* weight;        // null: no norm of the combined rows
+  const float* next_weight;   // null: no next
+  float scale, eps;
+  int T, E, H, k, dtype;
+  void* out;
+  void* next;
+};
+hipError_t launch_norm_out(const NormOutProblem& p, hipStream_t stream);
+
+// Router projection (moe_router.hip).
+hipError_t launch_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
+                                const float* bias, int T, int E, int H, float* logits,
+                                hipStream_t stream);
+
+// Low-rank adapters over aligned rows (moe_lora.hip).
+struct LoraProblem {
+  const void* x;
+  int x_dtype;
+  size_t ldx;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;  // may be null
+  const int32_t* sorted_ids;
+  const int32_t* block_adapter;
+  const int32_t* num_padded;
+  int S, n, K, N, r, block_m;
+  void* workspace;
+  const void* y;
+  int y_dtype;
+  size_t ldy;
+  void* out;
+  size_t ldo;
+};
+size_t lora_workspace_bytes(int S, int n, int K, int r, int block_m);
+hipError_t launch_lora_add(const LoraProblem& p, hipStream_t stream);
+
 }  // namespace moe

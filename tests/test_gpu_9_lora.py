@@ -1,0 +1,185 @@
+"""GPU parity of the adapters of many requests against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import layer_oracle as lo
+from tests.gpu_util import moe, say
+from tests.layer_util import DT, U, close, f64, gen, rand
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(S, n, r, K, N, xdt="bf16", ydt="bf16", seed=0, ids=None):
+    g = gen(seed + S + 31 * n + r + K + N)
+    if ids is None:
+        ids = torch.randint(-1, n, (S,), generator=g)
+    return dict(ids=ids.int().cuda().view(S, 1), x=rand(g, S, K, dtype=xdt),
+                a=rand(g, n, r, K, dtype="bf16", std=K ** -0.5),
+                b=rand(g, n, N, r, dtype="bf16"), scale=rand(g, n),
+                y=rand(g, S, N, dtype=ydt))
+
+
+def _run(d, block_m, out=None, scale=True, **kw):
+    plan = moe().align_block(d["ids"], d["a"].shape[0], block_m)
+    return moe().lora_add(d["y"] if out is None else d["y"], d["x"], d["a"], d["b"], *plan,
+                          block_m, scale=d["scale"] if scale else None, out=out, **kw)
+
+
+def _check(d, got, y, scale=True):
+    ids = d["ids"].view(-1).cpu().numpy()
+    n, r, K = d["a"].shape
+    x, a, b = f64(d["x"]), f64(d["a"]), f64(d["b"])
+    sc = f64(d["scale"]) if scale else None
+    ref = lo.lora_add(f64(y), x, a, b, ids, sc)
+    # z: a sum of K products in fp32 (of fp32 x: kept to 2^-23); the expansion: a sum of r
+    # products, of z to 16 bits for a bf16 output and to 23 for fp32; scale; the last sum
+    zero = np.zeros_like(ref)
+    mag = lo.lora_add(zero, np.abs(x), np.abs(a), np.abs(b), ids,
+                      None if sc is None else np.abs(sc))
+    dt = "bf16" if d["y"].dtype == torch.bfloat16 else "f32"
+    e = (K + r + 8) * U * mag + (2.0 ** -16 * mag if dt == "bf16" else 0) + U * np.abs(f64(y))
+    close(got, ref, e, dt, "out")
+    away = (ids < 0) | (ids >= n)
+    assert torch.equal(got[torch.from_numpy(away).cuda()], y[torch.from_numpy(away).cuda()])
+
+
+CASES = [  # S, n, r, K, N, block_m
+    (1, 1, 8, 8, 8, 1), (1, 1, 16, 4096, 4096, 64), (2, 3, 8, 64, 136, 16), (7, 5, 24, 72, 72, 4),
+    (16, 16, 16, 4096, 1024, 64), (16, 4, 64, 520, 2056, 16), (33, 2, 40, 1032, 264, 2),
+    (64, 64, 128, 256, 512, 64), (64, 1, 256, 264, 520, 64), (65, 3, 32, 2048, 64, 128),
+    (130, 7, 16, 136, 4104, 256), (300, 1, 64, 512, 512, 256), (300, 200, 8, 128, 256, 64),
+    (511, 1024, 16, 256, 264, 64), (1000, 9, 96, 1000, 1000, 64), (520, 8, 128, 64, 2048, 8),
+    (200, 3, 248, 200, 200, 32)]
+
+
+@pytest.mark.parametrize("S,n,r,K,N,block_m", CASES)
+@pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32"),
+                                     ("f32", "bf16")])
+def test_lora_parity(S, n, r, K, N, block_m, xdt, ydt):
+    say(f"lora S={S} n={n} r={r} K={K} N={N} M={block_m} {xdt}->{ydt}")
+    d = _inputs(S, n, r, K, N, xdt, ydt)
+    y = d["y"].clone()
+    out = torch.empty_like(y).copy_(y)
+    assert _run(d, block_m, out=out) is out
+    torch.cuda.synchronize()
+    assert torch.equal(d["y"], y), "y is an input here"
+    _check(d, out, y)
+    got = _run(d, block_m)                                # in place
+    assert got is d["y"] and torch.equal(got, out)        # the same bits
+    d["y"] = y.clone()
+    _check(d, _run(d, block_m, scale=False), y, scale=False)
+
+
+@pytest.mark.parametrize("kind", ["none", "one_row", "all_one", "last", "out_of_range"])
+def test_lora_uneven_batches(kind):
+    say(f"lora ids: {kind}")
+    S, n = 150, 6
+    ids = torch.full((S,), -1)
+    if kind == "one_row":
+        ids[77] = 3
+    elif kind == "all_one":
+        ids[:] = 2
+    elif kind == "last":
+        ids[-3:] = n - 1
+    elif kind == "out_of_range":
+        ids[:] = torch.arange(S) % 9 - 2                   # -2..6: some beyond n - 1
+    d = _inputs(S, n, 16, 264, 392, ids=ids)
+    away = (ids < 0) | (ids >= n)
+    d["x"][away.cuda()] = float("nan")                     # rows without an adapter are not read
+    d["y"][away.cuda()] = 7.0
+    y = d["y"].clone()
+    got = _run(d, 16)
+    d["x"][away.cuda()] = 0
+    _check(d, got, y)
+
+
+@pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32")])
+def test_lora_column_slices(xdt, ydt):
+    # x, y and out as column slices of wider matrices; what lies beside them stays
+    say(f"lora: strided rows {xdt} {ydt}")
+    S, n, r, K, N = 70, 4, 16, 264, 200
+    d = _inputs(S, n, r, K, N, xdt, ydt)
+    ref = torch.empty_like(d["y"]).copy_(d["y"])
+    _run(d, 16, out=ref)
+    wide_x = torch.full((S, K + 24), float("nan"), dtype=DT[xdt], device="cuda")
+    wide_y = torch.full((S, 3 * N), 5.0, dtype=DT[ydt], device="cuda")
+    wide_x[:, 16:16 + K] = d["x"]
+    wide_y[:, N:2 * N] = d["y"]
+    s = {**d, "x": wide_x[:, 16:16 + K], "y": wide_y[:, N:2 * N]}
+    out = torch.full((S, N + 40), 6.0, dtype=DT[ydt], device="cuda")
+    view = out[:, 8:8 + N]
+    view.copy_(d["y"])
+    _run(s, 16, out=view)
+    assert torch.equal(view, ref) and bool((out[:, :8] == 6).all() and (out[:, 8 + N:] == 6).all())
+    _run(s, 16)
+    assert torch.equal(wide_y[:, N:2 * N], ref)
+    assert bool((wide_y[:, :N] == 5).all() and (wide_y[:, 2 * N:] == 5).all())
+
+
+def test_lora_non_finite_stay_in_their_rows():
+    say("lora: infinities and NaN")
+    d = _inputs(40, 3, 24, 200, 136)
+    d["ids"] = (torch.arange(40) % 3).int().cuda().view(40, 1)
+    y = d["y"].clone()
+    ref = _run(d, 16, out=torch.empty_like(y)).clone()
+    x = d["x"].clone()
+    d["x"][5, 7] = float("nan")
+    d["x"][9, 100] = float("inf")
+    got = _run(d, 16, out=torch.empty_like(y)).clone()
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[[5, 9]] = False
+    assert torch.equal(got[keep.cuda()], ref[keep.cuda()])
+    assert not bool(torch.isfinite(got[[5, 9]]).any())
+    d["x"] = x
+    d["a"][1, 3, 20] = float("inf")                        # an adapter that overflowed
+    got = _run(d, 16, out=torch.empty_like(y))
+    assert torch.equal(got[0::3], ref[0::3]) and torch.equal(got[2::3], ref[2::3])
+    assert not bool(torch.isfinite(got[1::3]).any())
+
+
+def test_lora_empty_and_checks():
+    say("lora: S=0, binding checks")
+    m = moe()
+    d = _inputs(20, 3, 16, 64, 128)
+    plan = m.align_block(d["ids"], 3, 16)
+    e = m.lora_add(d["y"][:0], d["x"][:0], d["a"], d["b"], *plan, 16)
+    assert e.shape == (0, 128)
+    call = lambda **kw: m.lora_add(**{**dict(  # noqa: E731
+        y=d["y"], x=d["x"], a=d["a"], b=d["b"], sorted_ids=plan[0], block_adapter=plan[1],
+        num_padded=plan[2], block_m=16, scale=d["scale"]), **kw})
+    y = d["y"].clone()
+    for kw in (dict(y=d["y"][:19]), dict(x=d["x"][:, :56]), dict(b=d["b"][:2]),
+               dict(b=d["b"][:, :120].contiguous()), dict(scale=d["scale"][:2]),
+               dict(x=d["x"].t()), dict(out=y[:, :64]), dict(block_m=64),
+               dict(sorted_ids=plan[0][:8]), dict(y=d["y"].cpu()), dict(x=d["x"][:, ::2]),
+               dict(workspace=torch.empty(64, dtype=torch.uint8, device="cuda")),
+               dict(y=d["y"][0].expand(20, 128))):
+        with pytest.raises(ValueError):
+            call(**kw)
+    for kw in (dict(a=d["a"].float()), dict(b=d["b"].half()), dict(scale=d["scale"].bfloat16()),
+               dict(out=y.float()), dict(y=d["y"].half())):
+        with pytest.raises(TypeError):
+            call(**kw)
+    with pytest.raises(m.MoEError):
+        call(x=torch.zeros((20, 72), dtype=torch.bfloat16, device="cuda")[:, 4:68])  # 8 bytes off
+    torch.cuda.synchronize()
+    assert torch.equal(d["y"], y)
+
+
+def test_lora_rows_past_32_bit_offsets():
+    # slices of a matrix of more than 2^31 elements
+    S, n, K, N, wide = 40000, 2, 64, 64, 65536
+    say(f"lora S={S} in rows of {wide}")
+    d = _inputs(S, n, 8, K, N)
+    d["ids"][1:-5] = -1
+    d["ids"][-5:] = 1
+    big = torch.zeros((S, wide), dtype=torch.bfloat16, device="cuda")
+    assert big.numel() > 2 ** 31
+    big[:, wide - N:] = d["y"]
+    y = d["y"].clone()
+    d["y"] = big[:, wide - N:]
+    got = _run(d, 64)
+    torch.cuda.synchronize()
+    _check({**d, "y": y}, got.contiguous(), y)
+    assert not bool(big[-8:, :wide - N].any())
