@@ -138,6 +138,20 @@ def test_lora_non_finite_stay_in_their_rows():
     assert not bool(torch.isfinite(got[1::3]).any())
 
 
+@pytest.mark.parametrize("r", [8, 16, 24, 64])
+def test_lora_non_finite_factor_columns(r):
+    # an infinity in b belongs to its own output column of its adapter's rows
+    say(f"lora: an infinity in b, r={r}")
+    d = _inputs(20, 2, r, 72, 264, ids=torch.arange(20) % 2)
+    y = d["y"].clone()
+    ref = _run(d, 16, out=torch.empty_like(y)).clone()
+    d["b"][1, 77, 3] = float("inf")
+    got = _run(d, 16, out=torch.empty_like(y))
+    assert not bool(torch.isfinite(got[1::2, 77]).any())
+    got[1::2, 77] = ref[1::2, 77]
+    assert torch.equal(got, ref)
+
+
 def test_lora_empty_and_checks():
     say("lora: S=0, binding checks")
     m = moe()
