@@ -18,9 +18,11 @@ using skinny::kChunk;
 // How a problem is cut: decided on the host from its sizes alone.
 struct Plan {
   int log2m;
-  int slices;  // of K
-  int rows;    // of a group: consecutive positions of a block, at most 64
-  int groups;  // of all blocks
+  bool many;   // rows of an adapter on average: 32 or more
+  bool tiles;  // 4 or more: the expansion shares b between rows
+  int slices;  // of K, a power of two
+  int rows;    // of a group of the expansion: consecutive positions of a block
+  int rows_a;  // of a group of the shrink
 };
 
 // A group: its adapter, first position and this lane's row (lane l: position
@@ -29,16 +31,16 @@ struct Plan {
 struct Group {
   int adapter, count, row;
 };
-__device__ __forceinline__ Group group_at(const LoraProblem& p, const Plan& c, long g) {
-  const long pos = g * c.rows;
+__device__ __forceinline__ Group group_at(const LoraProblem& p, const Plan& c, long g, int rows) {
+  const long pos = g * rows;
   const int lane = threadIdx.x & 63;
   // the loads do not wait for each other: past *num_padded the lists still
   // hold what the alignment wrote there
   const int padded = p.num_padded[0];
   Group r;
   r.adapter = p.block_adapter[pos >> c.log2m];
-  r.row = p.sorted_ids[pos + min(lane, c.rows - 1)];
-  if (lane >= c.rows || (unsigned)r.row >= (unsigned)p.S || pos >= padded ||
+  r.row = p.sorted_ids[pos + min(lane, rows - 1)];
+  if (lane >= rows || (unsigned)r.row >= (unsigned)p.S || pos >= padded ||
       (unsigned)r.adapter >= (unsigned)p.n)
     r.row = -1;
   r.count = __builtin_popcountll(__ballot(r.row >= 0));
@@ -56,7 +58,7 @@ constexpr int kShrinkWaves = 8;
 
 template <int MT, int NT, typename XT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p, Plan c,
-                                                                   int rank_tiles) {
+                                                                   int rank_tiles, int groups) {
   constexpr int NW = kShrinkWaves;
   __shared__ __align__(16) char lds[skinny::lds_bytes<MT, NT, NW, XT, uint16_t>()];
   const int slice = blockIdx.x / rank_tiles, q0 = blockIdx.x % rank_tiles * NT * 16;
@@ -65,8 +67,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
   const int first = (int)((long)chunks * slice / c.slices);
   const int end = (int)((long)chunks * (slice + 1) / c.slices);
   float* z = (float*)p.workspace + (size_t)slice * p.S * p.r;
-  for (int gi = blockIdx.y; gi < c.groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi);
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows_a);
     const uint16_t* a = p.a + (size_t)g.adapter * p.r * p.K;
     for (int t = 0; t < g.count; t += 16 * MT) {  // the whole workgroup
       skinny::Product<MT, NT, XT, uint16_t> m;
@@ -88,153 +90,303 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
 }
 
 // ---------------------------------------------------------------- expand ---
-// A wave: 16 J columns of a group, 16 rows at a time with the next ones' y and z
-// loaded ahead. D = z (rows) x b (columns) with column 16 J u + J cc + j in
-// column cc of tile j: a lane then holds J consecutive columns of 4 rows, 16
-// bytes of y, and 16 lanes 256 bytes of a row.
-// STEPS: MFMAs over the rank, 32 of it each. A rank of 8 or 16 fills only one or
-// two of an MFMA's four k-groups: there one load brings PACK = 4 or 2 tiles of
-// b, a tile to a k-group (or two), and a tile's fragment is the load with the
-// others' groups zero (z is the same in every group).
-template <int J, int STEPS, typename YT>
-struct Rows16 {
-  static constexpr int kWords = J * (int)sizeof(YT) / 4;  // 32-bit words of y, lane and row
-  float z[STEPS][8];
-  uint32_t y[4][kWords];
+// D = z (rows) x b (columns), 16 rows and 16 J columns at a time, with column
+// J cc + j in column cc of tile j: a lane then holds J consecutive columns of 4
+// rows, 16 bytes of y, and 16 lanes 256 bytes of a row.
+// STEPS: MFMAs over the rank, 32 of it each.
 
-  // rows 16 t .. of the group; zq: this lane's first rank, n: its first column
+// z of rows 16 t .. of a group: 8 ranks from q of row lane & 15 in each step (any
+// values past the rank, where b is zero).
+template <int STEPS>
+struct Z16 {
+  float v[STEPS][8];
+
   __device__ __forceinline__ void load(const LoraProblem& p, const Plan& c, const Group& g, int t,
-                                       int zq, int n) {
-    const int lane = threadIdx.x & 63;
-    const float* zp = (const float*)p.workspace + (size_t)row_at(g, t * 16 + (lane & 15)) * p.r;
+                                       int q) {
+    const int at = t * 16 + (threadIdx.x & 15), row = row_at(g, at);
+    const size_t slice = (size_t)p.S * p.r;
+    const float* zp = (const float*)p.workspace + (size_t)row * p.r;
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) {
-      // past the rank: any values, b is zero there (clamped to stay in the row)
-      const f32x4* q = (const f32x4*)(zp + min(s * 32 + zq, p.r - 8));
+    for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        z[s][e] = q[0][e];
-        z[s][4 + e] = q[1][e];
-      }
+      for (int e = 0; e < 8; ++e) v[s][e] = 0.f;
+    if (at >= g.count) return;
+    constexpr int kTogether = STEPS < 4 ? 4 / STEPS : 1;  // slices whose loads are in flight
+    if (c.slices < kTogether) {
+      for (int k = 0; k < c.slices; ++k) add<1>(zp + k * slice, 0, q, p.r);
+    } else {  // powers of two both
+      for (int k = 0; k < c.slices; k += kTogether) add<kTogether>(zp + k * slice, slice, q, p.r);
     }
+  }
+  // N slices, their loads together
+  template <int N>
+  __device__ __forceinline__ void add(const float* zp, size_t slice, int q, int r) {
+    f32x4 w[N][STEPS][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const YT* yp = (const YT*)p.y + (size_t)row_at(g, t * 16 + (lane >> 4) * 4 + i) * p.ldy + n;
-      if constexpr (kWords == 2) {
-        const u32x2 v = *(const u32x2*)yp;
-        y[i][0] = v[0];
-        y[i][1] = v[1];
-      } else {
-#pragma unroll
-        for (int q = 0; q < kWords; q += 4) {
-          const u32x4 v = ((const u32x4*)yp)[q / 4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[i][q + e] = v[e];
-        }
-      }
-    }
-    for (int k = 1; k < c.slices; ++k) {
-      zp += (size_t)p.S * p.r;
+    for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        const f32x4* q = (const f32x4*)(zp + min(s * 32 + zq, p.r - 8));
+        const f32x4* from = (const f32x4*)(zp + k * slice + min(s * 32 + q, r - 8));
+        w[k][s][0] = from[0];
+        w[k][s][1] = from[1];
+      }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[s][e] += q[0][e];
-          z[s][4 + e] += q[1][e];
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[s][e] += w[k][s][e >> 2][e & 3];
+  }
+};
+
+// J columns from n of rows 16 t + 4 (lane >> 4) .. + 3 of a group, of y.
+template <int J, typename YT>
+struct Y4 {
+  static constexpr int kWords = J * (int)sizeof(YT) / 4;  // 32-bit words of a row
+  uint32_t w[4][kWords];
+
+  __device__ __forceinline__ void load(const LoraProblem& p, const Group& g, int t, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
+      const YT* yp = (const YT*)p.y + (size_t)row * p.ldy + n;
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) w[i][q] = 0;
+      if (at < g.count && n < p.N) {
+        if constexpr (kWords == 2) {
+          const u32x2 v = *(const u32x2*)yp;
+          w[i][0] = v[0];
+          w[i][1] = v[1];
+        } else {
+#pragma unroll
+          for (int q = 0; q < kWords; q += 4) {
+            const u32x4 v = ((const u32x4*)yp)[q / 4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[i][q + e] = v[e];
+          }
         }
       }
     }
   }
 };
 
-template <int J, int STEPS, int PACK, typename YT>
-__global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c) {
+// out = y + scale * z b for those rows and columns; frag(s, j): b's fragments.
+template <int J, int STEPS, typename YT, typename F>
+__device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, int t,
+                                         const Z16<STEPS>& z, const Y4<J, YT>& y, float scale,
+                                         int n, F frag) {
   // z enters as bf16 planes: exactly (3) for fp32 rows, to 2^-16 (2) for bf16
   // rows, whose own rounding is 2^-8
   constexpr int kPlanes = sizeof(YT) == 2 ? 2 : 3;
-  constexpr int kWords = Rows16<J, STEPS, YT>::kWords;
-  const int lane = threadIdx.x & 63, cc = lane & 15, g4 = lane >> 4;
+  constexpr int kWords = Y4<J, YT>::kWords;
+  f32x4 acc[J];
+#pragma unroll
+  for (int j = 0; j < J; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    bf16x8 zf[kPlanes];
+    skinny::split8<kPlanes>(z.v[s], zf);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const bf16x8 bf = frag(s, j);
+#pragma unroll
+      for (int q = kPlanes - 1; q >= 0; --q) acc[j] = mfma_bf16(zf[q], bf, acc[j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
+    if (at < g.count && n < p.N) {
+      uint32_t o[kWords];
+#pragma unroll
+      for (int q = 0; q < kWords; ++q) {
+        const uint32_t w = y.w[i][q];
+        if constexpr (sizeof(YT) == 2) {
+          const float lo = bf16_bits_to_f32(w & 0xffffu) + scale * acc[2 * q][i];
+          const float hi = __uint_as_float(w & 0xffff0000u) + scale * acc[2 * q + 1][i];
+          o[q] = f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
+        } else {
+          o[q] = __float_as_uint(__uint_as_float(w) + scale * acc[q][i]);
+        }
+      }
+      YT* op = (YT*)p.out + (size_t)row * p.ldo + n;
+      if constexpr (kWords == 2) {
+        *(u32x2*)op = u32x2{o[0], o[1]};
+      } else {
+#pragma unroll
+        for (int q = 0; q < kWords; q += 4)
+          ((u32x4*)op)[q / 4] = u32x4{o[q], o[q + 1], o[q + 2], o[q + 3]};
+      }
+    }
+  }
+}
+
+// Few rows of an adapter and a rank above 32: b is most of the traffic and each
+// of its rows is used once or little more. A wave keeps the b of 16 J columns in
+// registers and takes the group's rows 16 at a time.
+template <int J, int STEPS, typename YT>
+__global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int groups) {
+  const int g4 = (threadIdx.x >> 4) & 3;
   const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * 16 * J;
   if (n0 >= p.N) return;  // whole waves
-  const int n = n0 + cc * J, n_in = min(n, p.N - J);  // N and J: whole groups of J
-  constexpr int kGroups = 4 / PACK;  // k-groups of a tile
-  const int kq = g4 % kGroups * 8;
-  for (int gi = blockIdx.y; gi < c.groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi);
+  const int n = n0 + (threadIdx.x & 15) * J;
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows);
     if (g.count == 0) continue;
     const float scale = p.scale ? p.scale[g.adapter] : 1.f;
-    const uint16_t* b = p.b + (size_t)g.adapter * p.N * p.r;
+    const uint16_t* b = p.b + ((size_t)g.adapter * p.N + min(n, p.N - J)) * p.r;  // J divides N
     u32x4 bq[STEPS][J];
 #pragma unroll
     for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-      for (int j = 0; j < J; j += PACK) {
-        const int q = s * 32 + kq;
-        const u32x4 v = *(const u32x4*)(b + (size_t)(n_in + j + g4 / kGroups) * p.r +
-                                        min(q, p.r - 8));
+      for (int j = 0; j < J; ++j)
+        bq[s][j] = *(const u32x4*)(b + (size_t)j * p.r + min(s * 32 + g4 * 8, p.r - 8));
+    for (int t = 0; t * 16 < g.count; ++t) {
+      Z16<STEPS> z;
+      Y4<J, YT> y;
+      y.load(p, g, t, n);
+      z.load(p, c, g, t, g4 * 8);
+      add_rows(p, g, t, z, y, scale, n, [&](int s, int j) {
+        return __builtin_bit_cast(bf16x8, s * 32 + g4 * 8 < p.r ? bq[s][j] : u32x4{0, 0, 0, 0});
+      });
+    }
+  }
+}
+
+// Few rows and a rank of at most 32 (PIECES = r / 8 pieces of 16 bytes): a lane
+// takes whole rows of b, one column of the output each, and fp32 FMAs do the
+// little there is to compute; z lies in LDS, read by all lanes alike. A matrix
+// tile would hold one row of 16, and its registers would leave a quarter of the
+// loads in flight that this kernel has (8 KB of b per wave, seven waves per
+// SIMD): 512 slots of 8 adapters x 128 experts, r 8, N 7168 took 21 us so.
+template <int PIECES, typename YT>
+__global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan c, int groups) {
+  constexpr int U = 8 / PIECES;  // columns of a lane, 64 apart
+  constexpr int R = PIECES * 8, RB = 2;  // rank; rows of y in flight
+  __shared__ __align__(16) float zl[64 * R];
+  const int lane = threadIdx.x & 63;
+  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * U * 64 + lane;
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows);
+    if (g.count == 0) continue;  // the whole workgroup
+    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+    const uint16_t* b = p.b + (size_t)g.adapter * p.N * R;
+    u32x4 bq[U][PIECES];
 #pragma unroll
-        for (int pk = 0; pk < PACK; ++pk)
-          bq[s][j + pk] = q < p.r && g4 / kGroups == pk ? v : u32x4{0, 0, 0, 0};
-      }
-    Rows16<J, STEPS, YT> now;
-    auto work = [&](int t) {
-      f32x4 acc[J];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < J; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int q = 0; q < PIECES; ++q)
+        bq[u][q] = ((const u32x4*)(b + (size_t)min(n0 + u * 64, p.N - 1) * R))[q];
+    YT yv[RB][U];
+    auto load_y = [&](int i0) {
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        bf16x8 zf[kPlanes];
-        skinny::split8<kPlanes>(now.z[s], zf);
+      for (int i = 0; i < RB; ++i) {
+        if (i0 + i < g.count) {
+          const YT* yp = (const YT*)p.y + (size_t)row_at(g, i0 + i) * p.ldy;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int q = kPlanes - 1; q >= 0; --q)
-            acc[j] = mfma_bf16(zf[q], __builtin_bit_cast(bf16x8, bq[s][j]), acc[j]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int at = t * 16 + g4 * 4 + i, row = row_at(g, at);
-        uint32_t o[kWords];
-#pragma unroll
-        for (int q = 0; q < kWords; ++q) {
-          const uint32_t w = now.y[i][q];
-          if constexpr (sizeof(YT) == 2) {
-            const float lo = bf16_bits_to_f32(w & 0xffffu) + scale * acc[2 * q][i];
-            const float hi = __uint_as_float(w & 0xffff0000u) + scale * acc[2 * q + 1][i];
-            o[q] = f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
-          } else {
-            o[q] = __float_as_uint(__uint_as_float(w) + scale * acc[q][i]);
-          }
-        }
-        if (at < g.count && n < p.N) {
-          YT* op = (YT*)p.out + (size_t)row * p.ldo + n;
-          if constexpr (kWords == 2) {
-            *(u32x2*)op = u32x2{o[0], o[1]};
-          } else {
-#pragma unroll
-            for (int q = 0; q < kWords; q += 4)
-              ((u32x4*)op)[q / 4] = u32x4{o[q], o[q + 1], o[q + 2], o[q + 3]};
-          }
+          for (int u = 0; u < U; ++u) yv[i][u] = yp[min(n0 + u * 64, p.N - 1)];
         }
       }
     };
-    const int tiles = (g.count + 15) / 16;
-    now.load(p, c, g, 0, kq, n_in);
-    for (int t = 0; t + 1 < tiles; ++t) {
-      Rows16<J, STEPS, YT> next;
-      next.load(p, c, g, t + 1, kq, n_in);
-      work(t);
-      now = next;
+    load_y(0);
+    for (int e0 = 0; e0 < g.count * R; e0 += 256) {
+      const int e = e0 + threadIdx.x;
+      const size_t at = (size_t)row_at(g, e / R) * R + e % R, slice = (size_t)p.S * R;
+      const float* z = (const float*)p.workspace + at;
+      float v = z[0];
+      if (c.slices == 2) v += z[slice];
+      if (c.slices >= 4) {  // a power of two: the loads of four together
+        v = 0.f;
+        for (int k = 0; k < c.slices; k += 4)
+          v += (z[k * slice] + z[(k + 1) * slice]) + (z[(k + 2) * slice] + z[(k + 3) * slice]);
+      }
+      if (e < g.count * R) zl[e] = v;
     }
-    work(tiles - 1);
+    __syncthreads();
+    for (int i0 = 0; i0 < g.count; i0 += RB) {
+      if (i0) load_y(i0);
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        if (i0 + i < g.count) {
+          YT* op = (YT*)p.out + (size_t)row_at(g, i0 + i) * p.ldo;
+          float acc[U] = {};
+#pragma unroll
+          for (int q = 0; q < PIECES; ++q) {
+            const f32x4 lo = *(const f32x4*)(zl + (i0 + i) * R + q * 8);
+            const f32x4 hi = *(const f32x4*)(zl + (i0 + i) * R + q * 8 + 4);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t w = bq[u][q][e];
+                acc[u] += (e < 2 ? lo : hi)[e * 2 & 3] * bf16_bits_to_f32(w & 0xffffu);
+                acc[u] += (e < 2 ? lo : hi)[(e * 2 & 3) + 1] * __uint_as_float(w & 0xffff0000u);
+              }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (n0 + u * 64 < p.N) {
+              if constexpr (sizeof(YT) == 2)
+                op[n0 + u * 64] = (YT)f32_to_bf16_rne(bf16_bits_to_f32(yv[i][u]) + scale * acc[u]);
+              else
+                op[n0 + u * 64] = yv[i][u] + scale * acc[u];
+            }
+          }
+        }
+      }
+    }
+    __syncthreads();  // z is read before the next group's comes in
+  }
+}
+
+// The same for adapters with many rows: a workgroup takes up to 64 rows of an
+// adapter, 16 to a wave, and 16 J columns, whose rows of b it brings into LDS
+// once, 16 bytes per lane along b. b then costs no registers and is read along
+// its lines: five waves per SIMD instead of two keep the rows of y in flight.
+template <int J, int STEPS, typename YT>
+__global__ __launch_bounds__(256) void expand_tiles_kernel(LoraProblem p, Plan c,
+                                                           int groups) {
+  // rows of b at (n % J) * 16 + n / J, so that a tile's are together; 16 bytes
+  // of padding spread a column of them over the banks
+  constexpr int kStride = STEPS * 64 + 16;
+  __shared__ __align__(16) char lds[16 * J * kStride];
+  const int lane = threadIdx.x & 63, g4 = lane >> 4, cc = lane & 15;
+  const int wave = threadIdx.x >> 6;
+  const int n0 = blockIdx.x * 16 * J, n = n0 + cc * J;
+  const int pieces = p.r / 8, rows_b = min(16 * J, p.N - n0);  // 16-byte pieces of a row of b
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows);
+    if (g.count == 0) continue;  // the whole workgroup
+    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+    const u32x4* b = (const u32x4*)(p.b + ((size_t)g.adapter * p.N + n0) * p.r);
+    Z16<STEPS> z;
+    Y4<J, YT> y;
+    const bool mine = wave * 16 < g.count;
+    if (mine) {
+      y.load(p, g, wave, n);
+      z.load(p, c, g, wave, g4 * 8);
+    }
+    for (int u = threadIdx.x; u < rows_b * pieces; u += 256) {
+      const int r = u / pieces, q = u - r * pieces;
+      *(u32x4*)(lds + ((r % J) * 16 + r / J) * kStride + q * 16) = b[u];
+    }
+    __syncthreads();
+    if (mine)
+      add_rows(p, g, wave, z, y, scale, n, [&](int s, int j) {
+        // past the rank and past the last column: zero, and any finite values
+        u32x4 v = {0, 0, 0, 0};
+        if (s * 4 + g4 < pieces && cc * J < rows_b)
+          v = *(const u32x4*)(lds + (j * 16 + cc) * kStride + (s * 4 + g4) * 16);
+        return __builtin_bit_cast(bf16x8, v);
+      });
+    __syncthreads();  // b is read before the next group's comes in
   }
 }
 
 // ------------------------------------------------------------------ host ---
 
-// Rows of a call: up to kSliceRows of z (in slices of K and rows) are kept.
-constexpr long kSliceRows = 8192;
+// Rows of z that the slices of K may add up to, where a call's own are fewer.
+constexpr long kSliceRows = 16384;
 constexpr int kMaxSlices = 16;
 
 static int max_slices(int K) {
@@ -247,53 +399,76 @@ static Plan plan_of(const LoraProblem& p) {
   Plan c{};
   while ((1 << c.log2m) < p.block_m) ++c.log2m;
   c.rows = p.block_m < 64 ? p.block_m : 64;
-  c.groups = (int)(align_capacity(p.S, p.n, p.block_m) / c.rows);
-  // slices of K until some 512 workgroups have work: every adapter in use and
-  // every 16 rows give one
-  const long groups = p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1;
-  const int want = (int)(512 / groups), most = max_slices(p.K);
-  c.slices = want < 1 ? 1 : want > most ? most : want;
+  c.many = p.block_m >= 32 && (long)p.S >= 32L * p.n;
+  c.tiles = (long)p.S >= 4L * p.n;
+  // 16 rows to a group of the shrink until 32 of them are 256 groups
+  c.rows_a = c.many ? (p.S >= 8192 ? 32 : 16) : c.rows;
+  // slices of K until some 256 workgroups (of much-used adapters: the expansion
+  // reads every slice of z once per 128 columns) or 512 have work
+  const long groups = c.many ? p.S / c.rows_a + 1 : p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1;
+  const long most = max_slices(p.K), want = c.many ? 320 : 512;
+  c.slices = 1;
+  while (c.slices * 2 <= most && c.slices * 2 * groups <= want) c.slices *= 2;
   return c;
 }
 
+static int groups_of(const LoraProblem& p, int rows) {
+  return (int)(align_capacity(p.S, p.n, p.block_m) / rows);
+}
+static int grid_y(int groups) { return groups < 65535 ? groups : 65535; }
+
 template <int MT, int NT, typename XT>
 static void shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
-  const int rank_tiles = (p.r + NT * 16 - 1) / (NT * 16);
-  const dim3 grid(c.slices * rank_tiles, c.groups < 65535 ? c.groups : 65535);
-  shrink_kernel<MT, NT, XT><<<grid, kShrinkWaves * 64, 0, stream>>>(p, c, rank_tiles);
+  const int rank_tiles = (p.r + NT * 16 - 1) / (NT * 16), groups = groups_of(p, c.rows_a);
+  shrink_kernel<MT, NT, XT><<<dim3(c.slices * rank_tiles, grid_y(groups)), kShrinkWaves * 64, 0,
+                              stream>>>(p, c, rank_tiles, groups);
 }
 
 template <typename XT>
 static void run_shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
-  const bool pairs = c.rows >= 32 && (long)p.S >= 32L * p.n;  // rows of an adapter on average
+  const bool pairs = c.many && c.rows_a == 32;
   if (p.r > 32) pairs ? shrink<2, 4, XT>(p, c, stream) : shrink<1, 4, XT>(p, c, stream);
   else if (p.r > 16) pairs ? shrink<2, 2, XT>(p, c, stream) : shrink<1, 2, XT>(p, c, stream);
   else pairs ? shrink<2, 1, XT>(p, c, stream) : shrink<1, 1, XT>(p, c, stream);
 }
 
-template <int J, int STEPS, int PACK, typename YT>
+template <int J, int STEPS, typename YT>
 static void expand(const LoraProblem& p, const Plan& c, hipStream_t stream) {
-  const int units = (p.N + 16 * J - 1) / (16 * J);
-  const dim3 grid((units + 3) / 4, c.groups < 65535 ? c.groups : 65535);
-  expand_kernel<J, STEPS, PACK, YT><<<grid, 256, 0, stream>>>(p, c);
+  const int groups = groups_of(p, c.rows), units = (p.N + 16 * J - 1) / (16 * J);
+  if (c.tiles)
+    expand_tiles_kernel<J, STEPS, YT>
+        <<<dim3(units, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
+  else if constexpr (STEPS > 1)
+    expand_kernel<J, STEPS, YT>
+        <<<dim3((units + 3) / 4, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
+}
+
+template <int PIECES, typename YT>
+static void expand_columns(const LoraProblem& p, const Plan& c, hipStream_t stream) {
+  constexpr int kColumns = 4 * 64 * (8 / PIECES);  // of a workgroup
+  const int groups = groups_of(p, c.rows);
+  expand_columns_kernel<PIECES, YT>
+      <<<dim3((p.N + kColumns - 1) / kColumns, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
 }
 
 template <typename YT>
 static void run_expand(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   constexpr int J = 16 / sizeof(YT);  // 16 bytes of a row per lane
-  if (p.r == 8) expand<J, 1, 4, YT>(p, c, stream);
-  else if (p.r == 16) expand<J, 1, 2, YT>(p, c, stream);
-  else if (p.r <= 32) expand<J, 1, 1, YT>(p, c, stream);
-  else if (p.r <= 64) expand<J, 2, 1, YT>(p, c, stream);
-  else if (p.r <= 128) expand<4, 4, 1, YT>(p, c, stream);
-  else expand<4, 8, 1, YT>(p, c, stream);
+  if (!c.tiles && p.r == 8) expand_columns<1, YT>(p, c, stream);
+  else if (!c.tiles && p.r == 16) expand_columns<2, YT>(p, c, stream);
+  else if (!c.tiles && p.r == 24) expand_columns<3, YT>(p, c, stream);
+  else if (!c.tiles && p.r == 32) expand_columns<4, YT>(p, c, stream);
+  else if (p.r <= 32) expand<J, 1, YT>(p, c, stream);
+  else if (p.r <= 64) expand<J, 2, YT>(p, c, stream);
+  else if (p.r <= 128) expand<4, 4, YT>(p, c, stream);
+  else expand<4, 8, YT>(p, c, stream);
 }
 
 }  // namespace lora
 
 size_t lora_workspace_bytes(int S, int n, int K, int r, int block_m) {
   (void)n, (void)block_m;
-  // slices * S <= max(S, kSliceRows): 512 / (S / 16) slices at most. Stated so
+  // slices * S <= max(S, kSliceRows): 512 / (S / 32) slices at most. Stated so
   // that a workspace for some batch holds for every smaller one.
   const long few = (long)S * lora::max_slices(K);
   const long rows = few < lora::kSliceRows ? few : S > lora::kSliceRows ? S : lora::kSliceRows;
