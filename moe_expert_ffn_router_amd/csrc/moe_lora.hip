@@ -95,32 +95,39 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
 // rows, 16 bytes of y, and 16 lanes 256 bytes of a row.
 // STEPS: MFMAs over the rank, 32 of it each.
 
+// z enters the matrix cores as bf16 planes: exactly (3) for fp32 rows of y, to
+// 2^-16 (2) for bf16 rows, whose own rounding is 2^-8.
+template <typename YT>
+constexpr int z_planes() {
+  return sizeof(YT) == 2 ? 2 : 3;
+}
+
 // z of rows 16 t .. of a group: 8 ranks from q of row lane & 15 in each step (any
 // values past the rank, where b is zero).
-template <int STEPS>
+template <int STEPS, typename YT>
 struct Z16 {
-  float v[STEPS][8];
+  bf16x8 f[STEPS][z_planes<YT>()];
 
   __device__ __forceinline__ void load(const LoraProblem& p, const Plan& c, const Group& g, int t,
                                        int q) {
-    const int at = t * 16 + (threadIdx.x & 15), row = row_at(g, at);
     const size_t slice = (size_t)p.S * p.r;
-    const float* zp = (const float*)p.workspace + (size_t)row * p.r;
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[s][e] = 0.f;
-    if (at >= g.count) return;
+    const float* zp =
+        (const float*)p.workspace + (size_t)row_at(g, t * 16 + (threadIdx.x & 15)) * p.r;
+    float v[STEPS][8] = {};
     constexpr int kTogether = STEPS < 4 ? 4 / STEPS : 1;  // slices whose loads are in flight
     if (c.slices < kTogether) {
-      for (int k = 0; k < c.slices; ++k) add<1>(zp + k * slice, 0, q, p.r);
+      for (int k = 0; k < c.slices; ++k) add<1>(v, zp + k * slice, 0, q, p.r);
     } else {  // powers of two both
-      for (int k = 0; k < c.slices; k += kTogether) add<kTogether>(zp + k * slice, slice, q, p.r);
+      for (int k = 0; k < c.slices; k += kTogether)
+        add<kTogether>(v, zp + k * slice, slice, q, p.r);
     }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) skinny::split8<z_planes<YT>()>(v[s], f[s]);
   }
   // N slices, their loads together
   template <int N>
-  __device__ __forceinline__ void add(const float* zp, size_t slice, int q, int r) {
+  __device__ __forceinline__ static void add(float (&v)[STEPS][8], const float* zp, size_t slice,
+                                             int q, int r) {
     f32x4 w[N][STEPS][2];
 #pragma unroll
     for (int k = 0; k < N; ++k)
@@ -173,26 +180,20 @@ struct Y4 {
 // out = y + scale * z b for those rows and columns; frag(s, j): b's fragments.
 template <int J, int STEPS, typename YT, typename F>
 __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, int t,
-                                         const Z16<STEPS>& z, const Y4<J, YT>& y, float scale,
-                                         int n, F frag) {
-  // z enters as bf16 planes: exactly (3) for fp32 rows, to 2^-16 (2) for bf16
-  // rows, whose own rounding is 2^-8
-  constexpr int kPlanes = sizeof(YT) == 2 ? 2 : 3;
+                                         const Z16<STEPS, YT>& z, const Y4<J, YT>& y,
+                                         float scale, int n, F frag) {
   constexpr int kWords = Y4<J, YT>::kWords;
   f32x4 acc[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    bf16x8 zf[kPlanes];
-    skinny::split8<kPlanes>(z.v[s], zf);
+  for (int s = 0; s < STEPS; ++s)
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const bf16x8 bf = frag(s, j);
 #pragma unroll
-      for (int q = kPlanes - 1; q >= 0; --q) acc[j] = mfma_bf16(zf[q], bf, acc[j]);
+      for (int q = z_planes<YT>() - 1; q >= 0; --q) acc[j] = mfma_bf16(z.f[s][q], bf, acc[j]);
     }
-  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
@@ -204,7 +205,7 @@ __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, i
         if constexpr (sizeof(YT) == 2) {
           const float lo = bf16_bits_to_f32(w & 0xffffu) + scale * acc[2 * q][i];
           const float hi = __uint_as_float(w & 0xffff0000u) + scale * acc[2 * q + 1][i];
-          o[q] = f32_to_bf16_rne(lo) | (f32_to_bf16_rne(hi) << 16);
+          o[q] = pack_bf16(lo, hi);
         } else {
           o[q] = __float_as_uint(__uint_as_float(w) + scale * acc[q][i]);
         }
@@ -242,7 +243,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int 
       for (int j = 0; j < J; ++j)
         bq[s][j] = *(const u32x4*)(b + (size_t)j * p.r + min(s * 32 + g4 * 8, p.r - 8));
     for (int t = 0; t * 16 < g.count; ++t) {
-      Z16<STEPS> z;
+      Z16<STEPS, YT> z;
       Y4<J, YT> y;
       y.load(p, g, t, n);
       z.load(p, c, g, t, g4 * 8);
@@ -327,7 +328,7 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
           for (int u = 0; u < U; ++u) {
             if (n0 + u * 64 < p.N) {
               if constexpr (sizeof(YT) == 2)
-                op[n0 + u * 64] = (YT)f32_to_bf16_rne(bf16_bits_to_f32(yv[i][u]) + scale * acc[u]);
+                op[n0 + u * 64] = (YT)pack_bf16(bf16_bits_to_f32(yv[i][u]) + scale * acc[u], 0.f);
               else
                 op[n0 + u * 64] = yv[i][u] + scale * acc[u];
             }
@@ -339,47 +340,73 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
   }
 }
 
-// The same for adapters with many rows: a workgroup takes up to 64 rows of an
-// adapter, 16 to a wave, and 16 J columns, whose rows of b it brings into LDS
-// once, 16 bytes per lane along b. b then costs no registers and is read along
-// its lines: five waves per SIMD instead of two keep the rows of y in flight.
+// More rows of an adapter: a workgroup takes up to 64 rows of it, 16 to a wave,
+// and every stride-th 16 J columns, whose rows of b it brings into LDS once for
+// all its rows, 16 bytes per lane along b. z stays in registers from one set of
+// columns to the next (it is as large as y's columns from a rank of 64 on), and
+// the next ones' b and y are in flight while these are worked on.
 template <int J, int STEPS, typename YT>
-__global__ __launch_bounds__(256) void expand_tiles_kernel(LoraProblem p, Plan c,
-                                                           int groups) {
+__global__ __launch_bounds__(256) void expand_tiles_kernel(LoraProblem p, Plan c, int groups) {
   // rows of b at (n % J) * 16 + n / J, so that a tile's are together; 16 bytes
   // of padding spread a column of them over the banks
   constexpr int kStride = STEPS * 64 + 16;
+  constexpr int kLoads = J * STEPS / 4;  // of a thread: 16 J rows of 64 STEPS bytes at most
   __shared__ __align__(16) char lds[16 * J * kStride];
-  const int lane = threadIdx.x & 63, g4 = lane >> 4, cc = lane & 15;
-  const int wave = threadIdx.x >> 6;
-  const int n0 = blockIdx.x * 16 * J, n = n0 + cc * J;
-  const int pieces = p.r / 8, rows_b = min(16 * J, p.N - n0);  // 16-byte pieces of a row of b
+  const int g4 = (threadIdx.x >> 4) & 3, cc = threadIdx.x & 15, wave = threadIdx.x >> 6;
+  const int units = (p.N + 16 * J - 1) / (16 * J), stride = gridDim.x;
+  const int pieces = p.r / 8;  // 16-byte pieces of a row of b
+  int to[kLoads];              // where this thread's pieces go
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int e = threadIdx.x + i * 256, row = e / pieces;
+    to[i] = ((row % J) * 16 + row / J) * kStride + (e - row * pieces) * 16;
+  }
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
     const Group g = group_at(p, c, gi, c.rows);
     if (g.count == 0) continue;  // the whole workgroup
     const float scale = p.scale ? p.scale[g.adapter] : 1.f;
-    const u32x4* b = (const u32x4*)(p.b + ((size_t)g.adapter * p.N + n0) * p.r);
-    Z16<STEPS> z;
-    Y4<J, YT> y;
+    const u32x4* b = (const u32x4*)(p.b + (size_t)g.adapter * p.N * p.r);
+    auto column = [&](int u) { return (u * 16 + cc) * J; };
+    auto pieces_of = [&](int u) { return min(16 * J, p.N - u * 16 * J) * pieces; };
+    u32x4 bq[kLoads];
+    auto load_b = [&](int u) {
+      const u32x4* from = b + (size_t)u * 16 * J * pieces;
+      const int last = pieces_of(u) - 1;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) bq[i] = from[min((int)threadIdx.x + i * 256, last)];
+    };
     const bool mine = wave * 16 < g.count;
+    Z16<STEPS, YT> z;
+    Y4<J, YT> even, odd;
+    load_b(blockIdx.x);
     if (mine) {
-      y.load(p, g, wave, n);
+      even.load(p, g, wave, column(blockIdx.x));
       z.load(p, c, g, wave, g4 * 8);
     }
-    for (int u = threadIdx.x; u < rows_b * pieces; u += 256) {
-      const int r = u / pieces, q = u - r * pieces;
-      *(u32x4*)(lds + ((r % J) * 16 + r / J) * kStride + q * 16) = b[u];
+    auto step = [&](int u, const Y4<J, YT>& now, Y4<J, YT>& next) {
+      const int rows_b = min(16 * J, p.N - u * 16 * J);
+      __syncthreads();  // the previous columns' b is read
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        if ((int)threadIdx.x + i * 256 < rows_b * pieces) *(u32x4*)(lds + to[i]) = bq[i];
+      __syncthreads();
+      if (u + stride < units) {
+        load_b(u + stride);
+        if (mine) next.load(p, g, wave, column(u + stride));
+      }
+      if (mine)
+        add_rows(p, g, wave, z, now, scale, column(u), [&](int s, int j) {
+          // zero past the rank and past the last column
+          u32x4 v = {0, 0, 0, 0};
+          if (s * 4 + g4 < pieces && cc * J < rows_b)
+            v = *(const u32x4*)(lds + (j * 16 + cc) * kStride + (s * 4 + g4) * 16);
+          return __builtin_bit_cast(bf16x8, v);
+        });
+    };
+    for (int u = blockIdx.x; u < units; u += 2 * stride) {
+      step(u, even, odd);  // two sets of registers in turn: a copy would wait for the loads
+      if (u + stride < units) step(u + stride, odd, even);
     }
-    __syncthreads();
-    if (mine)
-      add_rows(p, g, wave, z, y, scale, n, [&](int s, int j) {
-        // past the rank and past the last column: zero, and any finite values
-        u32x4 v = {0, 0, 0, 0};
-        if (s * 4 + g4 < pieces && cc * J < rows_b)
-          v = *(const u32x4*)(lds + (j * 16 + cc) * kStride + (s * 4 + g4) * 16);
-        return __builtin_bit_cast(bf16x8, v);
-      });
-    __syncthreads();  // b is read before the next group's comes in
   }
 }
 
@@ -402,7 +429,7 @@ static Plan plan_of(const LoraProblem& p) {
   c.many = p.block_m >= 32 && (long)p.S >= 32L * p.n;
   c.tiles = (long)p.S >= 4L * p.n;
   // 16 rows to a group of the shrink until 32 of them are 256 groups
-  c.rows_a = c.many ? (p.S >= 8192 ? 32 : 16) : c.rows;
+  c.rows_a = c.many ? (p.S >= 4096 ? 32 : 16) : c.rows;
   // slices of K until some 256 workgroups (of much-used adapters: the expansion
   // reads every slice of z once per 128 columns) or 512 have work
   const long groups = c.many ? p.S / c.rows_a + 1 : p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1;
@@ -435,9 +462,13 @@ static void run_shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) 
 template <int J, int STEPS, typename YT>
 static void expand(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   const int groups = groups_of(p, c.rows), units = (p.N + 16 * J - 1) / (16 * J);
+  // some 1024 workgroups at work; beyond, one takes several sets of columns, all
+  // of them as many (4096 rows r 128: 43 us; 2048 workgroups 46, 4096 54)
+  const long live = p.S / c.rows + (p.n < p.S ? p.n : p.S) / 2 + 1;
+  const int want = (int)((1024 + live - 1) / live), each = units > want ? units / want : 1;
   if (c.tiles)
     expand_tiles_kernel<J, STEPS, YT>
-        <<<dim3(units, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
+        <<<dim3((units + each - 1) / each, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
   else if constexpr (STEPS > 1)
     expand_kernel<J, STEPS, YT>
         <<<dim3((units + 3) / 4, grid_y(groups)), 256, 0, stream>>>(p, c, groups);

@@ -61,7 +61,7 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     if constexpr (sizeof(T) == 2)
-      o[i] = f32_to_bf16_rne(v[2 * i]) | (f32_to_bf16_rne(v[2 * i + 1]) << 16);
+      o[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     else
       o[i] = __float_as_uint(v[i]);
   }
