@@ -539,7 +539,13 @@ def forward_small_static(logits, x, w1, w2, k: int, renormalize: bool = False, w
 
 # ------------------------------------------------------- around the FFN ---
 
+# These calls are microseconds of kernel each, so their checks are kept short: a
+# tensor that is as expected costs one comparison of each property; for any
+# other _need finds the words.
+
 _ACT = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32}
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _act(t: torch.Tensor, name: str) -> int:
@@ -552,48 +558,60 @@ def _act(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _launch_stream(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
-    """The stream a call on tensors of ``dev`` runs on. The library launches on
-    the current device, so its tensors (and a stream that is passed) are there."""
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is "
+def _same(t, name: str, dtypes, dev: int, shape: tuple) -> None:
+    """_need for a tensor of exactly ``shape`` on the device of index ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.get_device() == dev >= 0
+            and t.shape == shape and t.is_contiguous()):
+        return
+    _need(t, name, dtypes, None if dev < 0 else torch.device("cuda", dev), shape)
+
+
+def _launch_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """The stream a call on tensors of device ``dev`` runs on. The library
+    launches on the current device, so its tensors (and a stream that is passed)
+    are there."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, tensors are on {dev}")
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    if stream.device.index != dev:
+        raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{dev}")
     return stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A new tensor for a call on ``stream``, allocated there: memory that
-    another stream still uses cannot be handed to it."""
+def _empty(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new tensor on ``like``'s device for a call on ``stream``, allocated
+    there: memory that another stream still uses cannot be handed to it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        if like.dtype is dtype and like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _need_rows(t: torch.Tensor, name: str, dtypes, device=None, shape=None) -> int:
+def _need_rows(t: torch.Tensor, name: str, dtypes, dev: Optional[int] = None, shape=None) -> int:
     """Check a matrix of contiguous rows that may lie apart (a slice of columns
     of a wider one): a device tensor of one of ``dtypes`` with stride 1 along the
     rows. Returns its row stride in elements."""
     rows, cols = _dims(t, name, 2)
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor, got {t.device}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if shape is not None and (rows, cols) != shape:
         raise ValueError(f"{name} has shape {(rows, cols)}, expected {shape}")
-    if cols > 1 and t.stride(1) != 1:
+    step, one = t.stride()
+    if cols > 1 and one != 1:
         raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
     if rows <= 1:
         return cols
-    if t.stride(0) < cols:
+    if step < cols:
         raise ValueError(f"the rows of {name} overlap: strides {t.stride()}")
-    return t.stride(0)
+    return step
 
 
 def norm_in(x, weight, residual=None, alpha: float = 1.0, eps: float = 1e-6, out=None,
@@ -603,25 +621,25 @@ def norm_in(x, weight, residual=None, alpha: float = 1.0, eps: float = 1e-6, out
     Returns (out, residual_out); residual_out is None (and s not stored) without
     a residual unless a buffer is given. out or residual_out may be x or
     residual itself."""
-    T, H = _dims(x, "x", 2)
+    T, H = shape = _dims(x, "x", 2)
     code = _act(x, "x")
-    dev, like = x.device, (x.dtype,)
-    _need(x, "x", like)
-    _need(weight, "weight", (torch.float32,), dev, (H,))
+    dev, like = x.get_device(), (x.dtype,)
+    _same(x, "x", like, dev, shape)
+    _same(weight, "weight", _F32, dev, (H,))
     if residual is not None:
-        _need(residual, "residual", like, dev, (T, H))
+        _same(residual, "residual", like, dev, shape)
     raw = _launch_stream(dev, stream)
     if residual_out is not None:
-        _need(residual_out, "residual_out", like, dev, (T, H))
+        _same(residual_out, "residual_out", like, dev, shape)
     elif residual is not None:
-        residual_out = _empty((T, H), x.dtype, dev, stream)
+        residual_out = _empty(x, shape, x.dtype, stream)
     if out is None:
-        out = _empty((T, H), x.dtype, dev, stream)
+        out = _empty(x, shape, x.dtype, stream)
     else:
-        _need(out, "out", like, dev, (T, H))
+        _same(out, "out", like, dev, shape)
     keep = (x, weight, residual, out, residual_out)
-    args = (_ptr(x), _ptr(residual), _ptr(weight), alpha, eps, T, H, code, _ptr(residual_out),
-            _ptr(out), raw)
+    args = (x.data_ptr(), _ptr(residual), weight.data_ptr(), alpha, eps, T, H, code,
+            _ptr(residual_out), out.data_ptr(), raw)
     return _run(lib.moe_norm_in, args, keep, prepare, (out, residual_out))
 
 
@@ -639,41 +657,44 @@ def norm_out(y, topk_weights=None, topk_ids=None, num_experts: Optional[int] = N
     by default theirs, else y's), gate [T], weight, next_weight [H] float32.
     Returns (out, next); next is None without next_weight."""
     code_y = _act(y, "y")
-    _need(y, "y", (y.dtype,))
-    dev, H = y.device, y.shape[-1]
+    dev, H = y.get_device(), y.shape[-1] if y.dim() else 0
+    _same(y, "y", (y.dtype,), dev, y.shape)
     if topk_weights is None:
         T, k = y.numel() // H if H else 0, 1
     else:
         T, k = _dims(topk_weights, "topk_weights", 2)
-        _need(topk_weights, "topk_weights", (torch.float32,), dev, (T, k))
-    if tuple(y.shape) != (T * k, H) and tuple(y.shape) != (T, k, H):
+        _same(topk_weights, "topk_weights", _F32, dev, (T, k))
+    if y.shape != (T * k, H) and y.shape != (T, k, H):
         raise ValueError(f"y has shape {tuple(y.shape)}, expected {(T * k, H)} or {(T, k, H)}")
     if topk_ids is not None:
-        _need(topk_ids, "topk_ids", (torch.int32,), dev, (T, k))
+        _same(topk_ids, "topk_ids", _I32, dev, (T, k))
         if num_experts is None:
             raise ValueError("topk_ids needs num_experts")
     if dtype is None:
-        dtype = next((t.dtype for t in (residual, shared, out) if t is not None), y.dtype)
+        like = residual if residual is not None else shared if shared is not None else out
+        dtype = y.dtype if like is None else like.dtype
     if dtype not in _ACT:
         raise TypeError(f"dtype is {dtype}, expected one of {tuple(_ACT)}")
     for name, t in (("shared", shared), ("residual", residual), ("out", out),
                     ("next_out", next_out)):
         if t is not None:
-            _need(t, name, (dtype,), dev, (T, H))
+            _same(t, name, (dtype,), dev, (T, H))
     if gate is not None:
-        _need(gate, "gate", (torch.float32,), dev, (T,))
-    for name, t in (("weight", weight), ("next_weight", next_weight)):
-        if t is not None:
-            _need(t, name, (torch.float32,), dev, (H,))
+        _same(gate, "gate", _F32, dev, (T,))
+    if weight is not None:
+        _same(weight, "weight", _F32, dev, (H,))
+    if next_weight is not None:
+        _same(next_weight, "next_weight", _F32, dev, (H,))
     raw = _launch_stream(dev, stream)
+    like = y if residual is None else residual
     if out is None:
-        out = _empty((T, H), dtype, dev, stream)
+        out = _empty(like, (T, H), dtype, stream)
     if next_out is None and next_weight is not None:
-        next_out = _empty((T, H), dtype, dev, stream)
+        next_out = _empty(like, (T, H), dtype, stream)
     keep = (y, topk_ids, topk_weights, shared, gate, residual, weight, next_weight, out, next_out)
-    args = (_ptr(y), code_y, _ptr(topk_ids), _ptr(topk_weights), _ptr(shared), _ptr(gate),
+    args = (y.data_ptr(), code_y, _ptr(topk_ids), _ptr(topk_weights), _ptr(shared), _ptr(gate),
             _ptr(residual), _ptr(weight), _ptr(next_weight), scale, eps, T, num_experts or 0, H,
-            k, _ACT[dtype], _ptr(out), _ptr(next_out), raw)
+            k, _ACT[dtype], out.data_ptr(), _ptr(next_out), raw)
     return _run(lib.moe_norm_out, args, keep, prepare, (out, next_out))
 
 
@@ -683,19 +704,18 @@ def router_logits(x, w, bias=None, out=None, stream=None, prepare: bool = False)
     T, H = _dims(x, "x", 2)
     E = _dims(w, "w", 2)[0]
     code_x, code_w = _act(x, "x"), _act(w, "w")
-    dev = x.device
-    _need(x, "x", (x.dtype,))
-    _need(w, "w", (w.dtype,), dev, (E, H))
+    dev = x.get_device()
+    _same(x, "x", (x.dtype,), dev, (T, H))
+    _same(w, "w", (w.dtype,), dev, (E, H))
     if bias is not None:
-        _need(bias, "bias", (torch.float32,), dev, (E,))
+        _same(bias, "bias", _F32, dev, (E,))
     raw = _launch_stream(dev, stream)
     if out is None:
-        out = _empty((T, E), torch.float32, dev, stream)
+        out = _empty(x, (T, E), torch.float32, stream)
     else:
-        _need(out, "out", (torch.float32,), dev, (T, E))
-    keep = (x, w, bias, out)
-    args = (_ptr(x), code_x, _ptr(w), code_w, _ptr(bias), T, E, H, _ptr(out), raw)
-    return _run(lib.moe_router_logits, args, keep, prepare, out)
+        _same(out, "out", _F32, dev, (T, E))
+    args = (x.data_ptr(), code_x, w.data_ptr(), code_w, _ptr(bias), T, E, H, out.data_ptr(), raw)
+    return _run(lib.moe_router_logits, args, (x, w, bias, out), prepare, out)
 
 
 def lora_workspace_bytes(S: int, n: int, K: int, r: int, block_m: int) -> int:
@@ -714,14 +734,20 @@ def lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m: int, sc
     n, r, _ = _dims(a, "a", 3)
     N = _dims(y, "y", 2)[1]
     code_x, code_y = _act(x, "x"), _act(y, "y")
-    dev = x.device
+    dev, bf16 = x.get_device(), (torch.bfloat16,)
     ldx = _need_rows(x, "x", (x.dtype,))
     ldy = _need_rows(y, "y", (y.dtype,), dev, (S, N))
-    _need(a, "a", (torch.bfloat16,), dev, (n, r, K))
-    _need(b, "b", (torch.bfloat16,), dev, (n, N, r))
+    _same(a, "a", bf16, dev, (n, r, K))
+    _same(b, "b", bf16, dev, (n, N, r))
     if scale is not None:
-        _need(scale, "scale", (torch.float32,), dev, (n,))
-    _align_outputs((sorted_ids, block_adapter, num_padded), S, 1, n, block_m, dev)
+        _same(scale, "scale", _F32, dev, (n,))
+    cap = align_capacity(S, 1, n, block_m)
+    for name, t, least in (("sorted_ids", sorted_ids, cap),
+                           ("block_adapter", block_adapter, cap // block_m if block_m > 0 else 0),
+                           ("num_padded", num_padded, 1)):
+        if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev
+                and t.numel() >= least and t.is_contiguous()):
+            _need(t, name, _I32, x.device, min_numel=least)
     if out is None:
         out, ldo = y, ldy
     else:
@@ -729,13 +755,14 @@ def lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m: int, sc
     raw = _launch_stream(dev, stream)
     need = lora_workspace_bytes(S, n, K, r, block_m)
     if workspace is None:
-        workspace = _empty(max(need, 256), torch.uint8, dev, stream)
+        workspace = _empty(x, (max(need, 256),), torch.uint8, stream)
     else:
-        _need(workspace, "workspace", (torch.uint8,), dev, min_numel=need)
+        _need(workspace, "workspace", (torch.uint8,), x.device, min_numel=need)
     keep = (y, x, a, b, sorted_ids, block_adapter, num_padded, scale, out, workspace)
-    args = (_ptr(x), code_x, ldx, _ptr(a), _ptr(b), _ptr(scale), _ptr(sorted_ids),
-            _ptr(block_adapter), _ptr(num_padded), S, n, K, N, r, block_m, _ptr(workspace),
-            workspace.numel(), _ptr(y), code_y, ldy, _ptr(out), ldo, raw)
+    args = (x.data_ptr(), code_x, ldx, a.data_ptr(), b.data_ptr(), _ptr(scale),
+            sorted_ids.data_ptr(), block_adapter.data_ptr(), num_padded.data_ptr(), S, n, K, N, r,
+            block_m, workspace.data_ptr(), workspace.numel(), y.data_ptr(), code_y, ldy,
+            out.data_ptr(), ldo, raw)
     return _run(lib.moe_lora_add, args, keep, prepare, out)
 
 
