@@ -52,16 +52,16 @@ __device__ __forceinline__ int row_at(const Group& g, int i) {
 }
 
 // ---------------------------------------------------------------- shrink ---
-// A workgroup: 16 NT ranks of a group's adapter, one slice of K, 16 MT rows at a
+// A workgroup: R NT ranks of a group's adapter, one slice of K, R MT rows at a
 // time.
 constexpr int kShrinkWaves = 8;
 
-template <int MT, int NT, typename XT>
+template <int MT, int NT, int R, typename XT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p, Plan c,
                                                                    int rank_tiles, int groups) {
   constexpr int NW = kShrinkWaves;
-  __shared__ __align__(16) char lds[skinny::lds_bytes<MT, NT, NW, XT, uint16_t>()];
-  const int slice = blockIdx.x / rank_tiles, q0 = blockIdx.x % rank_tiles * NT * 16;
+  __shared__ __align__(16) char lds[skinny::lds_bytes<MT, NT, R, NW, XT, uint16_t>()];
+  const int slice = blockIdx.x / rank_tiles, q0 = blockIdx.x % rank_tiles * NT * R;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int chunks = (p.K + kChunk - 1) / kChunk;
   const int first = (int)((long)chunks * slice / c.slices);
@@ -70,8 +70,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
     const Group g = group_at(p, c, gi, c.rows_a);
     const uint16_t* a = p.a + (size_t)g.adapter * p.r * p.K;
-    for (int t = 0; t < g.count; t += 16 * MT) {  // the whole workgroup
-      skinny::Product<MT, NT, XT, uint16_t> m;
+    for (int t = 0; t < g.count; t += R * MT) {  // the whole workgroup
+      skinny::Product<MT, NT, R, XT, uint16_t> m;
       m.lds = lds + wave * m.kLdsBytes;
       m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, t + i) * p.ldx; });
       m.w.set([&](int i) { return a + (size_t)min(q0 + i, p.r - 1) * p.K; });
@@ -79,10 +79,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
       // two chunks in flight where their registers allow it
       constexpr int D = MT * (int)sizeof(XT) / 2 + NT <= 5 ? 2 : 1;
       m.template accumulate<D>(p.K, first + wave, end, NW);
-      skinny::reduce_waves<MT, NT, NW>(m.acc, lds, [&](int j, int i, int lane, f32x4 s) {
-        const int at = t + i * 16 + (lane & 15), q = q0 + j * 16 + (lane >> 4) * 4;
-        const int row = row_at(g, at);
-        if (at < g.count && q < p.r) *(f32x4*)(z + (size_t)row * p.r + q) = s;
+      skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, float s) {
+        // (not row_at: the lanes that hold the rows need not be here)
+        const int q = q0 + wr;
+        if (t + xr < g.count && q < p.r)
+          z[(size_t)p.sorted_ids[(long)gi * c.rows_a + t + xr] * p.r + q] = s;
       });
       __syncthreads();  // the sums are read before the next rows' chunks
     }
@@ -444,19 +445,22 @@ static int groups_of(const LoraProblem& p, int rows) {
 }
 static int grid_y(int groups) { return groups < 65535 ? groups : 65535; }
 
-template <int MT, int NT, typename XT>
+template <int MT, int NT, int R, typename XT>
 static void shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
-  const int rank_tiles = (p.r + NT * 16 - 1) / (NT * 16), groups = groups_of(p, c.rows_a);
-  shrink_kernel<MT, NT, XT><<<dim3(c.slices * rank_tiles, grid_y(groups)), kShrinkWaves * 64, 0,
+  const int rank_tiles = (p.r + NT * R - 1) / (NT * R), groups = groups_of(p, c.rows_a);
+  shrink_kernel<MT, NT, R, XT><<<dim3(c.slices * rank_tiles, grid_y(groups)), kShrinkWaves * 64, 0,
                               stream>>>(p, c, rank_tiles, groups);
 }
 
 template <typename XT>
 static void run_shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   const bool pairs = c.many && c.rows_a == 32;
-  if (p.r > 32) pairs ? shrink<2, 4, XT>(p, c, stream) : shrink<1, 4, XT>(p, c, stream);
-  else if (p.r > 16) pairs ? shrink<2, 2, XT>(p, c, stream) : shrink<1, 2, XT>(p, c, stream);
-  else pairs ? shrink<2, 1, XT>(p, c, stream) : shrink<1, 1, XT>(p, c, stream);
+  if (p.r > 32) pairs ? shrink<2, 4, 16, XT>(p, c, stream) : shrink<1, 4, 16, XT>(p, c, stream);
+  else if (p.r > 16) pairs ? shrink<2, 2, 16, XT>(p, c, stream) : shrink<1, 2, 16, XT>(p, c, stream);
+  else if (pairs) shrink<2, 1, 16, XT>(p, c, stream);
+  else if (c.tiles) shrink<1, 1, 16, XT>(p, c, stream);
+  else if (p.r > 8) shrink<1, 2, 8, XT>(p, c, stream);
+  else shrink<1, 1, 8, XT>(p, c, stream);
 }
 
 template <int J, int STEPS, typename YT>

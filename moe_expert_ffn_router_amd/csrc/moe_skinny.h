@@ -28,30 +28,39 @@ constexpr int kChunk = 64;  // k per step of a wave
 // 2 planes: to 2^-16).
 template <int PLANES>
 __device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&out)[PLANES]) {
+  u32x4 w[PLANES];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float rest = v[i];
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i], b = v[2 * i + 1];
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
-      const __bf16 b = (__bf16)rest;
-      out[p][i] = b;
-      if (p + 1 < PLANES) rest -= (float)b;
+      const uint32_t u = pack_bf16(a, b);
+      w[p][i] = u;
+      a -= __uint_as_float(u << 16);
+      b -= __uint_as_float(u & 0xffff0000u);
     }
   }
+#pragma unroll
+  for (int p = 0; p < PLANES; ++p) out[p] = __builtin_bit_cast(bf16x8, w[p]);
 }
 
-// A tile of 16 rows, one chunk wide: as loaded (kLoads 16-byte words per lane,
+// A tile of R rows, one chunk wide: as loaded (kLoads 16-byte words per lane,
 // load i covering rows i * kRows ..) and in LDS, where column c (16 bytes) of
 // row r is kept at column c ^ (r % kCols), so that the 8 rows a fragment read
 // meets at a time lie in different banks.
-template <typename T>
+// R = 16: the two halves of a chunk are an MFMA each. R = 8: one MFMA takes both,
+// the first half in rows 0 .. 7 of its operands and the second in rows 8 .. 15;
+// of its output the quarters row, column < 8 and row, column >= 8 are the two
+// halves' sums, the others mean nothing.
+template <typename T, int R>
 struct Tile {
   static constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
   static constexpr int kRowBytes = kChunk * sizeof(T);
   static constexpr int kCols = kRowBytes / 16;   // lanes along a row
   static constexpr int kRows = 64 / kCols;       // rows per load
-  static constexpr int kLoads = 16 / kRows;
-  static constexpr int kBytes = 16 * kRowBytes;
+  static constexpr int kLoads = R / kRows;
+  static constexpr int kBytes = R * kRowBytes;
+  static constexpr int kSteps = R / 8;           // MFMAs of a chunk
 
   __device__ __forceinline__ static int col() { return (threadIdx.x & 63) % kCols; }
   __device__ __forceinline__ static int row(int i) { return i * kRows + (threadIdx.x & 63) / kCols; }
@@ -63,9 +72,11 @@ struct Tile {
     for (int i = 0; i < kLoads; ++i)
       *(u32x4*)(lds + row(i) * kRowBytes + ((col() ^ (row(i) % kCols)) << 4)) = v[i];
   }
-  // this lane's fragment of a half: 8 elements of row l & 15 at k-group l >> 4
-  __device__ __forceinline__ static void frag(const char* lds, int half, bf16x8 (&out)[kPlanes]) {
-    const int r = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+  // this lane's fragment of a step: 8 elements of its row at k-group l >> 4
+  __device__ __forceinline__ static void frag(const char* lds, int step,
+                                              bf16x8 (&out)[kPlanes]) {
+    const int l = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const int r = l % R, half = R == 16 ? step : l / 8;
     const char* base = lds + r * kRowBytes;
     if constexpr (sizeof(T) == 2) {
       out[0] = *(const bf16x8*)(base + (((half * 4 + g) ^ (r % kCols)) << 4));
@@ -79,56 +90,58 @@ struct Tile {
   }
 };
 
-// The rows of one operand: N tiles of 16, as per-lane pointers at k = at().
-template <typename T, int N>
+// The rows of one operand: N tiles, as per-lane pointers at k = at().
+template <typename T, int N, int R>
 struct Rows {
-  const T* p[N][Tile<T>::kLoads];
+  const T* p[N][Tile<T, R>::kLoads];
 
-  // row(i): the address of row i of the 16 N, i < 16 N
+  // row(i): the address of row i of the R N
   template <typename F>
   __device__ __forceinline__ void set(F row) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < Tile<T>::kLoads; ++i)
-        p[n][i] = row(n * 16 + Tile<T>::row(i)) + Tile<T>::at();
+      for (int i = 0; i < Tile<T, R>::kLoads; ++i)
+        p[n][i] = row(n * R + Tile<T, R>::row(i)) + Tile<T, R>::at();
   }
 };
 
-template <typename T, int N>
+template <typename T, int N, int R>
 struct Chunk {
-  u32x4 v[N][Tile<T>::kLoads];
+  u32x4 v[N][Tile<T, R>::kLoads];
 
-  __device__ __forceinline__ void load(const Rows<T, N>& rows, int k) {
+  __device__ __forceinline__ void load(const Rows<T, N, R>& rows, int k) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < Tile<T>::kLoads; ++i) v[n][i] = *(const u32x4*)(rows.p[n][i] + k);
+      for (int i = 0; i < Tile<T, R>::kLoads; ++i) v[n][i] = *(const u32x4*)(rows.p[n][i] + k);
   }
   // the partial chunk at the end of K: zeros from there on (K a multiple of 8,
   // so a load lies inside or outside as a whole)
-  __device__ __forceinline__ void load_tail(const Rows<T, N>& rows, int k, int K) {
-    const bool in = k + Tile<T>::at() < K;
+  __device__ __forceinline__ void load_tail(const Rows<T, N, R>& rows, int k, int K) {
+    const bool in = k + Tile<T, R>::at() < K;
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int i = 0; i < Tile<T>::kLoads; ++i) {
+      for (int i = 0; i < Tile<T, R>::kLoads; ++i) {
         v[n][i] = u32x4{0, 0, 0, 0};
         if (in) v[n][i] = *(const u32x4*)(rows.p[n][i] + k);
       }
   }
   __device__ __forceinline__ void put(char* lds) const {
 #pragma unroll
-    for (int n = 0; n < N; ++n) Tile<T>::put(lds + n * Tile<T>::kBytes, v[n]);
+    for (int n = 0; n < N; ++n) Tile<T, R>::put(lds + n * Tile<T, R>::kBytes, v[n]);
   }
 };
 
-template <int MT, int NT, typename XT, typename WT>
+template <int MT, int NT, int R, typename XT, typename WT>
 struct Product {
-  static constexpr int kLdsBytes = MT * Tile<XT>::kBytes + NT * Tile<WT>::kBytes;  // per wave
+  typedef Tile<XT, R> XTile;
+  typedef Tile<WT, R> WTile;
+  static constexpr int kLdsBytes = MT * XTile::kBytes + NT * WTile::kBytes;  // per wave
 
-  Rows<XT, MT> x;
-  Rows<WT, NT> w;
+  Rows<XT, MT, R> x;
+  Rows<WT, NT, R> w;
   f32x4 acc[NT][MT];
   char* lds;  // this wave's kLdsBytes
 
@@ -141,8 +154,8 @@ struct Product {
 
   template <int D>
   struct Group {
-    Chunk<XT, MT> x[D];
-    Chunk<WT, NT> w[D];
+    Chunk<XT, MT, R> x[D];
+    Chunk<WT, NT, R> w[D];
   };
 
   template <int D>
@@ -155,26 +168,26 @@ struct Product {
   }
   // Passes chunk d of the group through LDS into acc. The LDS accesses of a
   // wave are performed in order, so one piece of LDS serves every chunk.
-  __device__ __forceinline__ void put(const Chunk<XT, MT>& cx, const Chunk<WT, NT>& cw) {
+  __device__ __forceinline__ void put(const Chunk<XT, MT, R>& cx, const Chunk<WT, NT, R>& cw) {
     cx.put(lds);
-    cw.put(lds + MT * Tile<XT>::kBytes);
+    cw.put(lds + MT * XTile::kBytes);
   }
   __device__ __forceinline__ void multiply() {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      bf16x8 xf[MT][Tile<XT>::kPlanes];
+    for (int step = 0; step < XTile::kSteps; ++step) {
+      bf16x8 xf[MT][XTile::kPlanes];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) Tile<XT>::frag(lds + i * Tile<XT>::kBytes, half, xf[i]);
+      for (int i = 0; i < MT; ++i) XTile::frag(lds + i * XTile::kBytes, step, xf[i]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        bf16x8 wf[Tile<WT>::kPlanes];
-        Tile<WT>::frag(lds + MT * Tile<XT>::kBytes + j * Tile<WT>::kBytes, half, wf);
+        bf16x8 wf[WTile::kPlanes];
+        WTile::frag(lds + MT * XTile::kBytes + j * WTile::kBytes, step, wf);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int p = Tile<WT>::kPlanes - 1; p >= 0; --p)
+          for (int p = WTile::kPlanes - 1; p >= 0; --p)
 #pragma unroll
-            for (int q = Tile<XT>::kPlanes - 1; q >= 0; --q)
+            for (int q = XTile::kPlanes - 1; q >= 0; --q)
               if (p + q <= 2) acc[j][i] = mfma_bf16(wf[p], xf[i][q], acc[j][i]);
       }
     }
@@ -217,8 +230,8 @@ struct Product {
     whole<D>(first, step, first < full ? (full - first + step - 1) / step : 0);
     // the partial last chunk, by the wave whose turn it is
     if (full < end && full >= first && (full - first) % step == 0) {
-      Chunk<XT, MT> cx;
-      Chunk<WT, NT> cw;
+      Chunk<XT, MT, R> cx;
+      Chunk<WT, NT, R> cw;
       cx.load_tail(x, full * kChunk, K);
       cw.load_tail(w, full * kChunk, K);
       put(cx, cw);
@@ -228,33 +241,49 @@ struct Product {
 };
 
 // LDS of a workgroup of NW waves: their pieces, then (in the same place) their sums.
-template <int MT, int NT, int NW, typename XT, typename WT>
+template <int MT, int NT, int R, int NW, typename XT, typename WT>
 constexpr int lds_bytes() {
-  constexpr int stage = NW * Product<MT, NT, XT, WT>::kLdsBytes;
+  constexpr int stage = NW * Product<MT, NT, R, XT, WT>::kLdsBytes;
   constexpr int sums = NW * NT * MT * 1024;
   return stage > sums ? stage : sums;
 }
 
 // Sums the accumulators of the NW waves of a workgroup in wave order and calls
-// store(nt, mt, lane, sum) for every tile and lane; sum holds w rows
-// 16 nt + 4 (lane >> 4) .. + 3 of x row 16 mt + (lane & 15).
-template <int MT, int NT, int NW, typename F>
+// store(w row, x row, sum) for every row of the R MT of x and the R NT of w; a
+// thread adds up single values, so that a small tile has many threads at it.
+template <int MT, int NT, int R, int NW, typename F>
 __device__ __forceinline__ void reduce_waves(const f32x4 (&acc)[NT][MT], char* lds, F store) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  f32x4* part = (f32x4*)lds;
-  constexpr int kOne = NT * MT * 64;
+  float* part = (float*)lds;
+  constexpr int kOne = NT * MT * 256;  // values of a wave
   __syncthreads();  // the pieces of all waves are done with
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < MT; ++i) part[wave * kOne + (j * MT + i) * 64 + lane] = acc[j][i];
+    for (int i = 0; i < MT; ++i)
+      ((f32x4*)part)[wave * (kOne / 4) + (j * MT + i) * 64 + lane] = acc[j][i];
   __syncthreads();
-  for (int u = threadIdx.x; u < kOne; u += NW * 64) {
-    f32x4 s = part[u];
+  if constexpr (R == 16) {
+    for (int u = threadIdx.x; u < kOne; u += NW * 64) {
+      float s = 0.f;
 #pragma unroll
-    for (int w = 1; w < NW; ++w) s += part[w * kOne + u];
-    const int tile = u >> 6;
-    store(tile / MT, tile % MT, u & 63, s);
+      for (int w = 0; w < NW; ++w) s += part[w * kOne + u];
+      const int tile = u >> 8, l = (u >> 2) & 63;
+      store(tile / MT * R + (l >> 4) * 4 + (u & 3), tile % MT * R + (l & 15), s);
+    }
+  } else {
+    // the 8 x 8 values of a tile in a wave's lanes 0 .. 31 and in the next
+    // iteration's; lanes 32 .. 63 add up the other half of K: rows and columns 8 on
+    for (int u = threadIdx.x; u < NT * MT * 128; u += NW * 64) {
+      const int tile = u >> 7, v = (u >> 6 & 1) * 32 + (u & 31), half = u >> 5 & 1;
+      const int wr = v & 7, xr = v >> 3;
+      const int at = tile * 256 + (half * 32 + (wr >> 2) * 16 + half * 8 + xr) * 4 + (wr & 3);
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) s += part[w * kOne + at];
+      s += __shfl_xor(s, 32);
+      if (half == 0) store(tile / MT * R + wr, tile % MT * R + xr, s);
+    }
   }
 }
 
