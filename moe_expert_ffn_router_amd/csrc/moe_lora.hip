@@ -346,8 +346,10 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
 // all its rows, 16 bytes per lane along b. z stays in registers from one set of
 // columns to the next (it is as large as y's columns from a rank of 64 on), and
 // the next ones' b and y are in flight while these are worked on.
+// (Held to 128 registers a rank of 16 took 26.8 us instead of 29.0, 4096 rows of
+// 64 adapters; from a rank of 64 on the registers are needed: 39 instead of 27.)
 template <int J, int STEPS, typename YT>
-__global__ __launch_bounds__(256) void expand_tiles_kernel(LoraProblem p, Plan c, int groups) {
+__global__ __launch_bounds__(256, STEPS == 1 ? 4 : 1) void expand_tiles_kernel(LoraProblem p, Plan c, int groups) {
   // rows of b at (n % J) * 16 + n / J, so that a tile's are together; 16 bytes
   // of padding spread a column of them over the banks
   constexpr int kStride = STEPS * 64 + 16;
