@@ -473,9 +473,10 @@ moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
  *                x is fp32, MOE_ERR_UNSUPPORTED otherwise).
  *  bias          [E] float32 or NULL.
  *  logits        [T, E] float32, written.
- *  Limits: 0 <= T, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8; x and w
- *  16-byte, bias and logits 4-byte aligned. The result is deterministic.
- *  Infinities and NaN in x or w make the logits that read them non-finite.
+ *  Limits: 0 <= T < 2^24, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8 below
+ *  2^24; x and w 16-byte, bias and logits 4-byte aligned. The result is
+ *  deterministic. Infinities and NaN in x or w make the logits that read them
+ *  non-finite, and no others.
  */
 moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
                              const float* bias, int T, int E, int H, float* logits,
@@ -504,12 +505,16 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                overlap.
  *  workspace     moe_lora_workspace_bytes(S, n, K, r, block_m) bytes (or
  *                more), 256-byte aligned, no initialisation needed.
- *  The rank-r intermediate is kept in fp32; products of bf16 factors are
- *  exact and summed in fp32. The result is deterministic.
- *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8, r a multiple
- *  of 8 in [8, 256], block_m a power of two in [1, 256]; ldx >= K, ldy and
- *  ldo >= N, each a multiple of 8 (of 4 for fp32); x, a, b, y and out 16-byte
- *  aligned, scale and the lists 4-byte. S == 0 launches nothing.
+ *                It holds for every smaller S too. Calls that share one must
+ *                not overlap in time (two graphs captured with it included).
+ *  The rank-r intermediate is kept in fp32 and enters the second product
+ *  exactly for fp32 y, to 2^-16 of its values for bf16 y (whose own rounding
+ *  is 2^-8); products are summed in fp32. The result is deterministic, and a
+ *  row's depends on its own x, y and adapter alone.
+ *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8 below 2^24, r a
+ *  multiple of 8 in [8, 256], block_m a power of two in [1, 256]; ldx >= K, ldy
+ *  and ldo >= N, each a multiple of 8 (of 4 for fp32); x, a, b, y and out
+ *  16-byte aligned, scale and the lists 4-byte. S == 0 launches nothing.
  */
 size_t moe_lora_workspace_bytes(int S, int n, int K, int r, int block_m);
 moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const uint16_t* a,

@@ -745,9 +745,11 @@ def lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m: int, sc
     _same(b, "b", bf16, dev, (n, N, r))
     if scale is not None:
         _same(scale, "scale", _F32, dev, (n,))
-    cap = align_capacity(S, 1, n, block_m)
-    for name, t, least in (("sorted_ids", sorted_ids, cap),
-                           ("block_adapter", block_adapter, cap // block_m if block_m > 0 else 0),
+    # what the lists of S slots hold, however these split into tokens and k
+    m = max(block_m, 1)
+    blocks = (S + min(n, S) * (m - 1) + m - 1) // m
+    for name, t, least in (("sorted_ids", sorted_ids, blocks * m),
+                           ("block_adapter", block_adapter, blocks),
                            ("num_padded", num_padded, 1)):
         if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev
                 and t.numel() >= least and t.is_contiguous()):

@@ -333,6 +333,7 @@ namespace {
 
 bool bf16_or_f32(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_F32; }
 size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
+constexpr int kMaxLength = 1 << 24;  // of a row, where the kernels count in 32 bits
 
 // Rows and row length of a norm; mult: what H is a multiple of.
 moe_status check_norm(int T, int H, int mult, float eps) {
@@ -392,7 +393,7 @@ MOE_EXPORT moe_status moe_router_logits(const void* x, int x_dtype, const void* 
     return MOE_ERR_UNSUPPORTED;
   moe_status s = check_common(T, E, 1);
   if (s != MOE_OK) return s;
-  if (H < 8 || H % 8 != 0) return MOE_ERR_SHAPE;
+  if (H < 8 || H % 8 != 0 || H >= kMaxLength) return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;
   if (!x || !w || !logits) return MOE_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(logits, 4))
@@ -403,7 +404,8 @@ MOE_EXPORT moe_status moe_router_logits(const void* x, int x_dtype, const void* 
 
 static moe_status check_lora(int S, int n, int K, int r, int block_m) {
   if (S < 0 || (long)S >= kMaxSlots || n < 1 || n > kMaxE) return MOE_ERR_SHAPE;
-  if (K < 8 || K % 8 != 0 || r < 8 || r % 8 != 0 || r > 256) return MOE_ERR_SHAPE;
+  if (K < 8 || K % 8 != 0 || K >= kMaxLength || r < 8 || r % 8 != 0 || r > 256)
+    return MOE_ERR_SHAPE;
   if (!is_pow2_le256(block_m)) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
@@ -424,7 +426,7 @@ MOE_EXPORT moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const
   moe_status s = check_lora(S, n, K, r, block_m);
   if (s != MOE_OK) return s;
   const size_t mx = 16 / elem_bytes(x_dtype), my = 16 / elem_bytes(y_dtype);
-  if (N < 8 || N % 8 != 0) return MOE_ERR_SHAPE;
+  if (N < 8 || N % 8 != 0 || N >= kMaxLength) return MOE_ERR_SHAPE;
   if (ldx < (size_t)K || ldy < (size_t)N || ldo < (size_t)N || ldx % mx != 0 || ldy % my != 0 ||
       ldo % my != 0)
     return MOE_ERR_SHAPE;

@@ -50,7 +50,16 @@ CASES = [  # S, n, r, K, N, block_m
     (64, 64, 128, 256, 512, 64), (64, 1, 256, 264, 520, 64), (65, 3, 32, 2048, 64, 128),
     (130, 7, 16, 136, 4104, 256), (300, 1, 64, 512, 512, 256), (300, 200, 8, 128, 256, 64),
     (511, 1024, 16, 256, 264, 64), (1000, 9, 96, 1000, 1000, 64), (520, 8, 128, 64, 2048, 8),
-    (200, 3, 248, 200, 200, 32)]
+    (200, 3, 248, 200, 200, 32),
+    # few rows of an adapter with ranks above 32; many slices of K
+    (7, 5, 64, 72, 520, 16), (6, 4, 256, 136, 264, 64), (9, 9, 40, 1032, 200, 2),
+    (3, 2, 16, 8264, 72, 64), (5, 3, 128, 4096, 136, 64), (2, 1, 64, 8192, 72, 16),
+    # four rows an adapter or fewer, and thirty-two or fewer
+    (12, 3, 32, 136, 264, 64), (11, 3, 32, 136, 264, 64), (96, 3, 8, 520, 136, 64),
+    (95, 3, 8, 520, 136, 64), (160, 40, 24, 72, 72, 32),
+    # thirty-two rows at a time in the shrink
+    (4100, 2, 64, 520, 264, 64), (4100, 3, 16, 200, 136, 32), (4095, 2, 24, 136, 72, 256),
+    (4200, 1, 160, 136, 328, 64)]
 
 
 @pytest.mark.parametrize("S,n,r,K,N,block_m", CASES)
@@ -150,6 +159,22 @@ def test_lora_non_finite_factor_columns(r):
     assert not bool(torch.isfinite(got[1::2, 77]).any())
     got[1::2, 77] = ref[1::2, 77]
     assert torch.equal(got, ref)
+
+
+def test_lora_workspace_of_a_larger_batch():
+    # one workspace for the largest batch serves every smaller one; nothing is
+    # read that the call did not write
+    say("lora: one workspace")
+    n, r, K, N = 3, 40, 1032, 136
+    sizes = [300, 1, 17, 64, 2, 299]
+    need = max(moe().lora_workspace_bytes(S, n, K, r, 64) for S in sizes)
+    assert need == moe().lora_workspace_bytes(300, n, K, r, 64)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")   # NaN in fp32
+    for S in sizes:
+        d = _inputs(S, n, r, K, N)
+        y = d["y"].clone()
+        ws.fill_(0xFF)
+        _check(d, _run(d, 64, workspace=ws), y)
 
 
 def test_lora_empty_and_checks():

@@ -17,7 +17,9 @@ SHAPES = [(1, 8, "bf16"), (3, 16, "bf16"), (5, 136, "bf16"), (9, 512, "bf16"), (
           (2, 4104, "bf16"), (3, 7168, "bf16"), (1, 8200, "bf16"), (2, 16384, "bf16"),
           (7, 256, "f32"), (1, 4, "f32"), (5, 12, "f32"), (3, 1028, "f32"), (2, 2052, "f32"),
           (2, 4100, "f32"), (2, 8188, "f32"), (1, 16380, "f32"), (2, 16384, "f32"),
-          (300, 64, "bf16"), (65, 4096, "bf16")]
+          (300, 64, "bf16"), (65, 4096, "bf16"),
+          # two vectors per thread from 512 rows on
+          (511, 4360, "bf16"), (512, 4360, "bf16"), (513, 2300, "f32")]
 
 
 def _check_in(x, res, w, alpha, out, s_out, dtype, eps=EPS):
@@ -230,6 +232,23 @@ def test_norm_out_rows_past_32_bit_offsets():
     torch.cuda.synchronize()
     assert y.numel() > 2 ** 31
     assert bool((out[-1] == 18).all()) and bool((out[0] == 8).all()) and not bool(out[1:-1].any())
+
+
+@pytest.mark.parametrize("T,k,H,ydt,dt", [(2100, 8, 4104, "bf16", "bf16"),
+                                          (4200, 8, 1032, "f32", "bf16")])
+def test_norm_out_streamed(T, k, H, ydt, dt):
+    # y beyond the size up to which it is read through the caches
+    say(f"norm_out T={T} k={k} H={H} y {ydt}, streamed")
+    a = _args_out(T, k, H, ydt, dt, 21, E=16, local=12)
+    assert a["y"].numel() * a["y"].element_size() > 128 << 20
+    out, nxt = moe().norm_out(**a, scale=0.5, eps=EPS)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(out.float()).all() and torch.isfinite(nxt.float()).all())
+    rows = torch.tensor([0, 1, 63, 64, T // 2, T - 2, T - 1])
+    pick = {n: t if t is None or isinstance(t, int) or n in ("weight", "next_weight")
+            else t.view(T, k * H)[rows.cuda()].view(-1, H) if n == "y" else t[rows.cuda()]
+            for n, t in a.items()}
+    _check_out(pick, 0.5, out[rows.cuda()], nxt[rows.cuda()], dt)
 
 
 def test_norm_argument_checks():

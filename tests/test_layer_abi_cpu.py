@@ -72,7 +72,7 @@ def test_router_validation():
     assert router(T=0, x=None, out=None) == OK
     assert router(xdt=FP8) == UNSUP and router(wdt=FP8) == UNSUP
     assert router(xdt=F32, wdt=BF16) == UNSUP
-    for bad in (dict(T=-1), dict(E=0), dict(E=1025), dict(H=0), dict(H=12), dict(H=4),
+    for bad in (dict(T=-1), dict(E=0), dict(E=1025), dict(H=0), dict(H=12), dict(H=4), dict(H=1 << 24),
                 dict(T=1 << 24), dict(T=(1 << 31) // 8, E=8)):
         assert router(**bad) == SHAPE, bad
     for name in ("x", "w", "out"):
@@ -91,6 +91,7 @@ def test_lora_validation():
     assert lora(S=0, x=None, y=None, ws=None) == OK
     assert lora(xdt=FP8) == UNSUP and lora(ydt=FP8) == UNSUP
     for bad in (dict(S=-1), dict(S=1 << 24), dict(n=0), dict(n=1025), dict(K=0), dict(K=12),
+                dict(K=1 << 24, ldx=1 << 24), dict(N=1 << 24, ldy=1 << 24, ldo=1 << 24),
                 dict(N=0), dict(N=12), dict(r=0), dict(r=4), dict(r=12), dict(r=264), dict(M=0),
                 dict(M=12), dict(M=512), dict(ldx=56), dict(ldx=68), dict(ldy=120), dict(ldy=132),
                 dict(ldo=120), dict(ldo=132)):
