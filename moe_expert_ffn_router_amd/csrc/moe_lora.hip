@@ -179,39 +179,42 @@ struct Y4 {
 };
 
 // out = y + scale * z b for those rows and columns; frag(s, j): b's fragments.
+// Two of the J tiles at a time: their sums go into y's registers.
 template <int J, int STEPS, typename YT, typename F>
 __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, int t,
-                                         const Z16<STEPS, YT>& z, const Y4<J, YT>& y,
-                                         float scale, int n, F frag) {
+                                         const Z16<STEPS, YT>& z, Y4<J, YT>& y, float scale,
+                                         int n, F frag) {
   constexpr int kWords = Y4<J, YT>::kWords;
-  f32x4 acc[J];
 #pragma unroll
-  for (int j = 0; j < J; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < J; j += 2) {
+    f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s)
+    for (int s = 0; s < STEPS; ++s) {
+      const bf16x8 b0 = frag(s, j), b1 = frag(s, j + 1);
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const bf16x8 bf = frag(s, j);
-#pragma unroll
-      for (int q = z_planes<YT>() - 1; q >= 0; --q) acc[j] = mfma_bf16(z.f[s][q], bf, acc[j]);
+      for (int q = z_planes<YT>() - 1; q >= 0; --q) {
+        lo = mfma_bf16(z.f[s][q], b0, lo);
+        hi = mfma_bf16(z.f[s][q], b1, hi);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(YT) == 2) {
+        const uint32_t w = y.w[i][j / 2];
+        y.w[i][j / 2] = pack_bf16(bf16_bits_to_f32(w & 0xffffu) + scale * lo[i],
+                                  __uint_as_float(w & 0xffff0000u) + scale * hi[i]);
+      } else {
+        y.w[i][j] = __float_as_uint(__uint_as_float(y.w[i][j]) + scale * lo[i]);
+        y.w[i][j + 1] = __float_as_uint(__uint_as_float(y.w[i][j + 1]) + scale * hi[i]);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
     if (at < g.count && n < p.N) {
-      uint32_t o[kWords];
-#pragma unroll
-      for (int q = 0; q < kWords; ++q) {
-        const uint32_t w = y.w[i][q];
-        if constexpr (sizeof(YT) == 2) {
-          const float lo = bf16_bits_to_f32(w & 0xffffu) + scale * acc[2 * q][i];
-          const float hi = __uint_as_float(w & 0xffff0000u) + scale * acc[2 * q + 1][i];
-          o[q] = pack_bf16(lo, hi);
-        } else {
-          o[q] = __float_as_uint(__uint_as_float(w) + scale * acc[q][i]);
-        }
-      }
       YT* op = (YT*)p.out + (size_t)row * p.ldo + n;
+      const uint32_t* o = y.w[i];
       if constexpr (kWords == 2) {
         *(u32x2*)op = u32x2{o[0], o[1]};
       } else {
@@ -386,7 +389,7 @@ __global__ __launch_bounds__(256, STEPS == 1 ? 4 : 1) void expand_tiles_kernel(L
       even.load(p, g, wave, column(blockIdx.x));
       z.load(p, c, g, wave, g4 * 8);
     }
-    auto step = [&](int u, const Y4<J, YT>& now, Y4<J, YT>& next) {
+    auto step = [&](int u, Y4<J, YT>& now, Y4<J, YT>& next) {
       const int rows_b = min(16 * J, p.N - u * 16 * J);
       __syncthreads();  // the previous columns' b is read
 #pragma unroll
