@@ -19,7 +19,7 @@ using skinny::kChunk;
 struct Plan {
   int log2m;
   bool many;   // rows of an adapter on average: 32 or more
-  bool tiles;  // 4 or more: the expansion shares b between rows
+  bool tiles;  // the expansion shares b between rows
   int slices;  // of K, a power of two
   int rows;    // of a group of the expansion: consecutive positions of a block
   int rows_a;  // of a group of the shrink
@@ -433,7 +433,11 @@ static Plan plan_of(const LoraProblem& p) {
   while ((1 << c.log2m) < p.block_m) ++c.log2m;
   c.rows = p.block_m < 64 ? p.block_m : 64;
   c.many = p.block_m >= 32 && (long)p.S >= 32L * p.n;
-  c.tiles = (long)p.S >= 4L * p.n;
+  // b shared between rows from 8 rows an adapter on (N 4096, r 16: 512 adapters x
+  // 4 rows 44.5 us so, 41.6 row by row; 16 adapters x 8 the same); with so few
+  // adapters that their groups do not fill the chip, from 2 (16 adapters x 2 rows
+  // 7.3 us, 8.3 row by row; a rank of 128 x 4 rows 16.7, 14.2)
+  c.tiles = (long)p.S >= 8L * p.n || (p.n <= 16 && p.S >= 2 * p.n && p.r <= 64);
   // 16 rows to a group of the shrink until 32 of them are 256 groups
   c.rows_a = c.many ? (p.S >= 4096 ? 32 : 16) : c.rows;
   // slices of K until some 256 workgroups (of much-used adapters: the expansion

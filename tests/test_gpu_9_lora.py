@@ -54,7 +54,10 @@ CASES = [  # S, n, r, K, N, block_m
     # few rows of an adapter with ranks above 32; many slices of K
     (7, 5, 64, 72, 520, 16), (6, 4, 256, 136, 264, 64), (9, 9, 40, 1032, 200, 2),
     (3, 2, 16, 8264, 72, 64), (5, 3, 128, 4096, 136, 64), (2, 1, 64, 8192, 72, 16),
-    # four rows an adapter or fewer, and thirty-two or fewer
+    # b shared between rows or not: 2 and 8 rows an adapter, 16 and 17 adapters, rank 64 on
+    (32, 16, 16, 136, 264, 64), (31, 16, 16, 136, 264, 64), (136, 17, 8, 72, 264, 64),
+    (135, 17, 8, 72, 264, 64), (40, 17, 64, 72, 264, 64), (8, 4, 72, 72, 264, 64),
+    # thirty-two rows an adapter or fewer
     (12, 3, 32, 136, 264, 64), (11, 3, 32, 136, 264, 64), (96, 3, 8, 520, 136, 64),
     (95, 3, 8, 520, 136, 64), (160, 40, 24, 72, 72, 32),
     # thirty-two rows at a time in the shrink
