@@ -44,6 +44,15 @@ __device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&out)[PLANES
   for (int p = 0; p < PLANES; ++p) out[p] = __builtin_bit_cast(bf16x8, w[p]);
 }
 
+// The lanes of a wave exchange data through LDS without a barrier: the hardware
+// performs a wave's LDS accesses in order, and this keeps the compiler from
+// reordering them (no instruction).
+__device__ __forceinline__ void wave_lds_order() {
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_wave_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 // A tile of R rows, one chunk wide: as loaded (kLoads 16-byte words per lane,
 // load i covering rows i * kRows ..) and in LDS, where column c (16 bytes) of
 // row r is kept at column c ^ (r % kCols), so that the 8 rows a fragment read
@@ -79,11 +88,14 @@ struct Tile {
     const int r = l % R, half = R == 16 ? step : l / 8;
     const char* base = lds + r * kRowBytes;
     if constexpr (sizeof(T) == 2) {
-      out[0] = *(const bf16x8*)(base + (((half * 4 + g) ^ (r % kCols)) << 4));
+      out[0] = __builtin_bit_cast(
+          bf16x8, *(const u32x4*)(base + (((half * 4 + g) ^ (r % kCols)) << 4)));
     } else {
       const int c = half * 8 + g * 2;
-      const f32x4 a = *(const f32x4*)(base + ((c ^ (r % kCols)) << 4));
-      const f32x4 b = *(const f32x4*)(base + (((c + 1) ^ (r % kCols)) << 4));
+      const f32x4 a =
+          __builtin_bit_cast(f32x4, *(const u32x4*)(base + ((c ^ (r % kCols)) << 4)));
+      const f32x4 b =
+          __builtin_bit_cast(f32x4, *(const u32x4*)(base + (((c + 1) ^ (r % kCols)) << 4)));
       const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
       split8<kPlanes>(v, out);
     }
@@ -166,11 +178,12 @@ struct Product {
       g.x[d].load(x, (c + d * step) * kChunk);
     }
   }
-  // Passes chunk d of the group through LDS into acc. The LDS accesses of a
-  // wave are performed in order, so one piece of LDS serves every chunk.
+  // A chunk through LDS into acc: one piece of LDS serves every chunk.
   __device__ __forceinline__ void put(const Chunk<XT, MT, R>& cx, const Chunk<WT, NT, R>& cw) {
+    wave_lds_order();
     cx.put(lds);
     cw.put(lds + MT * XTile::kBytes);
+    wave_lds_order();
   }
   __device__ __forceinline__ void multiply() {
 #pragma unroll
