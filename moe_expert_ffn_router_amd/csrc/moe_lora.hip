@@ -79,11 +79,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
       // two chunks in flight where their registers allow it
       constexpr int D = MT * (int)sizeof(XT) / 2 + NT <= 5 ? 2 : 1;
       m.template accumulate<D>(p.K, first + wave, end, NW);
-      skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, float s) {
-        // (not row_at: the lanes that hold the rows need not be here)
+      skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, auto s) {
+        // (not row_at: the lanes that hold the rows need not be here; 4 divides the rank)
         const int q = q0 + wr;
         if (t + xr < g.count && q < p.r)
-          z[(size_t)p.sorted_ids[(long)gi * c.rows_a + t + xr] * p.r + q] = s;
+          *(decltype(s)*)(z + (size_t)p.sorted_ids[(long)gi * c.rows_a + t + xr] * p.r + q) = s;
       });
       __syncthreads();  // the sums are read before the next rows' chunks
     }

@@ -30,9 +30,27 @@ __global__ __launch_bounds__(NW * 64) void router_kernel(const XT* __restrict__ 
   m.w.set([&](int i) { return w + (size_t)min(e0 + i, E - 1) * H; });
   m.clear();
   m.template accumulate<D>(H, wave, (H + skinny::kChunk - 1) / skinny::kChunk, NW);
-  skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, float s) {
+  const bool whole = E % 4 == 0 && (uintptr_t)logits % 16 == 0;  // rows of 16-byte words
+  skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, auto s) {
     const int t = t0 + xr, e = e0 + wr;
-    if (t < T && e < E) logits[(size_t)t * E + e] = bias ? s + bias[e] : s;
+    if (t >= T || e >= E) return;
+    float* o = logits + (size_t)t * E + e;
+    if constexpr (sizeof(s) == 4) {
+      *o = bias ? s + bias[e] : s;
+    } else {
+      if (bias) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < E) s[q] += bias[e + q];
+      }
+      if (whole) {
+        *(f32x4*)o = s;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < E) o[q] = s[q];
+      }
+    }
   });
 }
 

@@ -262,8 +262,9 @@ constexpr int lds_bytes() {
 }
 
 // Sums the accumulators of the NW waves of a workgroup in wave order and calls
-// store(w row, x row, sum) for every row of the R MT of x and the R NT of w; a
-// thread adds up single values, so that a small tile has many threads at it.
+// store(w row, x row, sum) for every row of the R MT of x and the R NT of w. A
+// sum is four consecutive w rows' (f32x4) where that leaves every thread one,
+// else a single value, so that a small tile has many threads at it.
 template <int MT, int NT, int R, int NW, typename F>
 __device__ __forceinline__ void reduce_waves(const f32x4 (&acc)[NT][MT], char* lds, F store) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -276,7 +277,15 @@ __device__ __forceinline__ void reduce_waves(const f32x4 (&acc)[NT][MT], char* l
     for (int i = 0; i < MT; ++i)
       ((f32x4*)part)[wave * (kOne / 4) + (j * MT + i) * 64 + lane] = acc[j][i];
   __syncthreads();
-  if constexpr (R == 16) {
+  if constexpr (R == 16 && kOne >= NW * 256) {
+    for (int u = threadIdx.x; u < kOne / 4; u += NW * 64) {
+      f32x4 s = ((const f32x4*)part)[u];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) s += ((const f32x4*)part)[w * (kOne / 4) + u];
+      const int tile = u >> 6, l = u & 63;
+      store(tile / MT * R + (l >> 4) * 4, tile % MT * R + (l & 15), s);
+    }
+  } else if constexpr (R == 16) {
     for (int u = threadIdx.x; u < kOne; u += NW * 64) {
       float s = 0.f;
 #pragma unroll

@@ -52,6 +52,20 @@ def test_router_parity(T, E, H, dtypes):
     _check(x, w, None, moe().router_logits(x, w))
 
 
+@pytest.mark.parametrize("T", [5, 300, 4100])
+def test_router_logits_off_the_16_byte_grid(T):
+    say(f"router T={T}: logits 4 bytes off")
+    g = gen(T)
+    x, w, bias = rand(g, T, 72, dtype="bf16"), rand(g, 64, 72, dtype="bf16"), rand(g, 64)
+    buf = torch.full((T * 64 + 8,), 12345.0, device="cuda")
+    out = buf[1:1 + T * 64].view(T, 64)
+    assert out.data_ptr() % 16 == 4
+    moe().router_logits(x, w, bias, out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, moe().router_logits(x, w, bias))
+    assert float(buf[0]) == 12345.0 and bool((buf[1 + T * 64:] == 12345.0).all())
+
+
 def test_router_wide_range():
     # magnitudes from 2^-60 to 2^60 in one row: every product counts at its own size
     say("router: wide range")
