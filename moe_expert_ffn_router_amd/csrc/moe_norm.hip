@@ -5,7 +5,11 @@
 // to its stores, so each input is read once and each output written once, and
 // the only other work is one (norm_in) or up to two (norm_out) sums of squares
 // per row. Bound by HBM: 2 bytes per bf16 element and stream; for norm_out the
-// k expert rows per token are the largest of them.
+// k expert rows per token are the largest of them. Measured (captured into a
+// graph): norm_in 4096 x 4096 bf16 with residual 21.6 us = 6.2 TB/s, 16 x 4096
+// 2.7 us; norm_out 4096 x top-8 x 4096 bf16, everything on, 61.7 us = 6.5 TB/s,
+// 64 x top-8 x 7168 fp32 7.9 us (a row per CU: 64 of them, 330 KB each),
+// 16 x top-8 x 4096 bf16 3.8 us.
 //
 // W waves serve a row: thread i of the row's 64 W holds the vectors i,
 // i + 64 W, ... of VEC elements, NV of them. VEC is what 16 bytes of the largest
@@ -36,7 +40,8 @@ __device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4 r = NT ? __builtin_nontemporal_load((const u32x4*)p + i / 4) : ((const u32x4*)p)[i / 4];
+      const u32x4* from = (const u32x4*)p + i / 4;
+      const u32x4 r = NT ? __builtin_nontemporal_load(from) : *from;
 #pragma unroll
       for (int q = 0; q < 4; ++q) v.w[i + q] = r[q];
     }

@@ -72,7 +72,9 @@ struct Tile {
   static constexpr int kSteps = R / 8;           // MFMAs of a chunk
 
   __device__ __forceinline__ static int col() { return (threadIdx.x & 63) % kCols; }
-  __device__ __forceinline__ static int row(int i) { return i * kRows + (threadIdx.x & 63) / kCols; }
+  __device__ __forceinline__ static int row(int i) {
+    return i * kRows + (threadIdx.x & 63) / kCols;
+  }
   // the chunk's first k this lane loads
   __device__ __forceinline__ static int at() { return col() * (16 / (int)sizeof(T)); }
 

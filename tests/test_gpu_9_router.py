@@ -31,7 +31,7 @@ SHAPES = [(1, 1, 8), (1, 8, 256), (3, 5, 16), (16, 64, 4096), (17, 65, 264), (31
           (64, 128, 7168), (33, 128, 520), (100, 7, 72), (200, 256, 1024), (5, 1024, 136),
           (129, 300, 2056), (1, 128, 16392), (300, 60, 2048), (1030, 96, 512),
           # 8-row tiles, 16-row tiles and tiles of 32 tokens, on both sides of their limits
-          (127 * 16, 16, 136), (127 * 16 + 1, 16, 136), (127 * 32, 64, 72), (127 * 32 + 1, 33, 200),
+          (95 * 16, 16, 136), (95 * 16 + 1, 16, 136), (95 * 32, 64, 72), (95 * 32 + 1, 33, 200),
           (2040, 128, 1032), (4100, 70, 264), (1000, 1000, 64)]
 
 
