@@ -271,35 +271,79 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int 
 // had 2 KB in flight and the expert slots above took 21 us; they take 10.8 here,
 // where 45 MB at the rate of a copy are 9.
 template <int PIECES, typename YT>
-__global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan c, int groups) {
-  constexpr int U = 8 / PIECES;  // columns of a lane, 64 apart
-  constexpr int R = PIECES * 8, RB = 2;  // rank; rows of y in flight
-  __shared__ __align__(16) float zl[64 * R];
-  const int lane = threadIdx.x & 63;
-  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * U * 64 + lane;
-  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi, c.rows);
-    if (g.count == 0) continue;  // the whole workgroup
-    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
-    const uint16_t* b = p.b + (size_t)g.adapter * p.N * R;
-    u32x4 bq[U][PIECES];
+struct Columns {
+  static constexpr int U = 8 / PIECES;  // columns of a lane: n0, n0 + 64, ...
+  static constexpr int R = PIECES * 8;  // rank
+  static constexpr int RB = 2;          // rows of y in flight
+  u32x4 b[U][PIECES];
+  YT y[RB][U];
+
+  __device__ __forceinline__ void load_b(const LoraProblem& p, const Group& g, int n0) {
+    const uint16_t* from = p.b + (size_t)g.adapter * p.N * R;
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int q = 0; q < PIECES; ++q)
-        bq[u][q] = ((const u32x4*)(b + (size_t)min(n0 + u * 64, p.N - 1) * R))[q];
-    YT yv[RB][U];
-    auto load_y = [&](int i0) {
+        b[u][q] = ((const u32x4*)(from + (size_t)min(n0 + u * 64, p.N - 1) * R))[q];
+  }
+  __device__ __forceinline__ void load_y(const LoraProblem& p, const Group& g, int i0, int n0) {
 #pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        if (i0 + i < g.count) {
-          const YT* yp = (const YT*)p.y + (size_t)row_at(g, i0 + i) * p.ldy;
+    for (int i = 0; i < RB; ++i) {
+      if (i0 + i < g.count) {
+        const YT* yp = (const YT*)p.y + (size_t)row_at(g, i0 + i) * p.ldy;
 #pragma unroll
-          for (int u = 0; u < U; ++u) yv[i][u] = yp[min(n0 + u * 64, p.N - 1)];
+        for (int u = 0; u < U; ++u) y[i][u] = yp[min(n0 + u * 64, p.N - 1)];
+      }
+    }
+  }
+  // rows i0 .. of the group, RB of them; z: theirs, in LDS
+  __device__ __forceinline__ void add(const LoraProblem& p, const Group& g, int i0, int n0,
+                                      float scale, const float* z) const {
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      if (i0 + i < g.count) {
+        YT* op = (YT*)p.out + (size_t)row_at(g, i0 + i) * p.ldo;
+        float acc[U] = {};
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+          const f32x4 lo = *(const f32x4*)(z + i * R + q * 8);
+          const f32x4 hi = *(const f32x4*)(z + i * R + q * 8 + 4);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t w = b[u][q][e];
+              acc[u] += (e < 2 ? lo : hi)[e * 2 & 3] * bf16_bits_to_f32(w & 0xffffu);
+              acc[u] += (e < 2 ? lo : hi)[(e * 2 & 3) + 1] * __uint_as_float(w & 0xffff0000u);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (n0 + u * 64 < p.N) {
+            if constexpr (sizeof(YT) == 2)
+              op[n0 + u * 64] = (YT)pack_bf16(bf16_bits_to_f32(y[i][u]) + scale * acc[u], 0.f);
+            else
+              op[n0 + u * 64] = y[i][u] + scale * acc[u];
+          }
         }
       }
-    };
-    load_y(0);
+    }
+  }
+};
+
+template <int PIECES, typename YT>
+__global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan c, int groups) {
+  typedef Columns<PIECES, YT> Cols;
+  constexpr int R = Cols::R;
+  __shared__ __align__(16) float zl[64 * R];
+  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * Cols::U * 64 + (threadIdx.x & 63);
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows);
+    if (g.count == 0) continue;  // the whole workgroup
+    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+    Cols m;
+    m.load_b(p, g, n0);
+    m.load_y(p, g, 0, n0);
     for (int e0 = 0; e0 < g.count * R; e0 += 256) {
       const int e = e0 + threadIdx.x;
       const size_t at = (size_t)row_at(g, e / R) * R + e % R, slice = (size_t)p.S * R;
@@ -314,39 +358,56 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
       if (e < g.count * R) zl[e] = v;
     }
     __syncthreads();
-    for (int i0 = 0; i0 < g.count; i0 += RB) {
-      if (i0) load_y(i0);
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        if (i0 + i < g.count) {
-          YT* op = (YT*)p.out + (size_t)row_at(g, i0 + i) * p.ldo;
-          float acc[U] = {};
-#pragma unroll
-          for (int q = 0; q < PIECES; ++q) {
-            const f32x4 lo = *(const f32x4*)(zl + (i0 + i) * R + q * 8);
-            const f32x4 hi = *(const f32x4*)(zl + (i0 + i) * R + q * 8 + 4);
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t w = bq[u][q][e];
-                acc[u] += (e < 2 ? lo : hi)[e * 2 & 3] * bf16_bits_to_f32(w & 0xffffu);
-                acc[u] += (e < 2 ? lo : hi)[(e * 2 & 3) + 1] * __uint_as_float(w & 0xffff0000u);
-              }
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (n0 + u * 64 < p.N) {
-              if constexpr (sizeof(YT) == 2)
-                op[n0 + u * 64] = (YT)pack_bf16(bf16_bits_to_f32(yv[i][u]) + scale * acc[u], 0.f);
-              else
-                op[n0 + u * 64] = yv[i][u] + scale * acc[u];
-            }
-          }
-        }
-      }
+    for (int i0 = 0; i0 < g.count; i0 += Cols::RB) {
+      if (i0) m.load_y(p, g, i0, n0);
+      m.add(p, g, i0, n0, scale, zl + i0 * R);
     }
     __syncthreads();  // z is read before the next group's comes in
+  }
+}
+
+// Both steps in one launch, for batches whose groups do not fill the chip: there
+// a second launch costs more than reading a once per 8 waves' columns. A
+// workgroup forms z of 8 rows at a time (all of K, split over its waves, as the
+// shrink does) and adds its columns, whose b has been on its way meanwhile.
+constexpr int kOneWaves = 8;
+
+template <int PIECES, typename XT, typename YT>
+__global__ __launch_bounds__(kOneWaves * 64) void one_launch_kernel(LoraProblem p, Plan c,
+                                                                    int groups) {
+  constexpr int NW = kOneWaves;
+  typedef Columns<PIECES, YT> Cols;
+  typedef skinny::Product<1, PIECES, 8, XT, uint16_t> Shrink;
+  constexpr int R = Cols::R;
+  __shared__ __align__(16) char lds[skinny::lds_bytes<1, PIECES, 8, NW, XT, uint16_t>()];
+  __shared__ __align__(16) float zl[8 * R];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = (blockIdx.x * NW + wave) * Cols::U * 64 + (threadIdx.x & 63);
+  const int chunks = (p.K + kChunk - 1) / kChunk;
+  for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
+    const Group g = group_at(p, c, gi, c.rows);
+    const uint16_t* a = p.a + (size_t)g.adapter * R * p.K;
+    Cols cols;
+    for (int t = 0; t < g.count; t += 8) {  // the whole workgroup
+      Shrink m;
+      m.lds = lds + wave * m.kLdsBytes;
+      m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, t + i) * p.ldx; });
+      m.w.set([&](int i) { return a + (size_t)i * p.K; });
+      m.clear();
+      m.template accumulate<PIECES * (int)sizeof(XT) <= 8 ? 4 : 2>(p.K, wave, chunks, NW);
+      if (t == 0) cols.load_b(p, g, n0);
+      cols.load_y(p, g, t, n0);
+      const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+      skinny::reduce_waves<1, PIECES, 8, NW>(m.acc, lds, [&](int wr, int xr, float s) {
+        zl[xr * R + wr] = s;
+      });
+      __syncthreads();
+      for (int i = 0; i < 8 && t + i < g.count; i += Cols::RB) {
+        if (i) cols.load_y(p, g, t + i, n0);
+        cols.add(p, g, t + i, n0, scale, zl + i * R);
+      }
+      __syncthreads();  // z is read before the next rows' comes in
+    }
   }
 }
 
@@ -499,7 +560,7 @@ static void expand(const LoraProblem& p, const Plan& c, hipStream_t stream) {
 
 template <int PIECES, typename YT>
 static void expand_columns(const LoraProblem& p, const Plan& c, hipStream_t stream) {
-  constexpr int kColumns = 4 * 64 * (8 / PIECES);  // of a workgroup
+  constexpr int kColumns = 4 * 64 * Columns<PIECES, YT>::U;  // of a workgroup
   const int groups = groups_of(p, c.rows);
   expand_columns_kernel<PIECES, YT>
       <<<dim3((p.N + kColumns - 1) / kColumns, grid_y(groups)), 256, 0, stream>>>(p, c, groups);
@@ -518,6 +579,38 @@ static void run_expand(const LoraProblem& p, const Plan& c, hipStream_t stream) 
   else expand<4, 8, YT>(p, c, stream);
 }
 
+// Whether both steps run in one launch.
+static bool one_launch(const LoraProblem& p, const Plan& c) {
+  if (c.tiles || p.r > 32) return false;
+  const int columns = kOneWaves * 64 * (8 / (p.r / 8));
+  return (long)(p.n < p.S ? p.n : p.S) * ((p.N + columns - 1) / columns) <= 256;
+}
+
+template <int PIECES, typename XT, typename YT>
+static void run_one(const LoraProblem& p, const Plan& c, hipStream_t stream) {
+  constexpr int kColumns = kOneWaves * 64 * Columns<PIECES, YT>::U;
+  const int groups = groups_of(p, c.rows);
+  one_launch_kernel<PIECES, XT, YT>
+      <<<dim3((p.N + kColumns - 1) / kColumns, grid_y(groups)), kOneWaves * 64, 0, stream>>>(
+          p, c, groups);
+}
+
+template <typename XT, typename YT>
+static hipError_t run(const LoraProblem& p, const Plan& c, hipStream_t stream) {
+  if (one_launch(p, c)) {
+    if (p.r == 8) run_one<1, XT, YT>(p, c, stream);
+    else if (p.r == 16) run_one<2, XT, YT>(p, c, stream);
+    else if (p.r == 24) run_one<3, XT, YT>(p, c, stream);
+    else run_one<4, XT, YT>(p, c, stream);
+    return hipGetLastError();
+  }
+  run_shrink<XT>(p, c, stream);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  run_expand<YT>(p, c, stream);
+  return hipGetLastError();
+}
+
 }  // namespace lora
 
 size_t lora_workspace_bytes(int S, int n, int K, int r, int block_m) {
@@ -531,13 +624,11 @@ size_t lora_workspace_bytes(int S, int n, int K, int r, int block_m) {
 
 hipError_t launch_lora_add(const LoraProblem& p, hipStream_t stream) {
   const lora::Plan c = lora::plan_of(p);
-  if (p.x_dtype == MOE_DTYPE_BF16) lora::run_shrink<uint16_t>(p, c, stream);
-  else lora::run_shrink<float>(p, c, stream);
-  const hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
-  if (p.y_dtype == MOE_DTYPE_BF16) lora::run_expand<uint16_t>(p, c, stream);
-  else lora::run_expand<float>(p, c, stream);
-  return hipGetLastError();
+  if (p.x_dtype == MOE_DTYPE_BF16)
+    return p.y_dtype == MOE_DTYPE_BF16 ? lora::run<uint16_t, uint16_t>(p, c, stream)
+                                       : lora::run<uint16_t, float>(p, c, stream);
+  return p.y_dtype == MOE_DTYPE_BF16 ? lora::run<float, uint16_t>(p, c, stream)
+                                     : lora::run<float, float>(p, c, stream);
 }
 
 }  // namespace moe
