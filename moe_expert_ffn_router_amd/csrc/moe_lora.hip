@@ -4,9 +4,10 @@
 // Two launches over the aligned row lists, both bound by memory (2 r flops per
 // element of x, y, a or b): the shrink z = a x, split over K, leaves fp32
 // partial sums in the workspace (r numbers per row: nothing next to x and y);
-// the expansion adds them up and works b into the rows of y.
-// Measured (captured into a graph, both launches): 16 requests with r 16 beside
-// 4096 x 4096 7.8 us, one 5.7 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
+// the expansion adds them up and works b into the rows of y. Small batches run
+// both in one launch.
+// Measured (captured into a graph): 16 requests with r 16 beside 4096 x 4096 6.5
+// us, one 4.1 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
 // -> 7168, 16.7 us = 3.6 TB/s; 4096 rows of prompts, 8 adapters of r 64, 4096 x
 // 4096, 25.4 us = 3.2 TB/s.
 #include "../../include/moe.h"
@@ -369,7 +370,10 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
 // Both steps in one launch, for batches whose groups do not fill the chip: there
 // a second launch costs more than reading a once per 8 waves' columns. A
 // workgroup forms z of 8 rows at a time (all of K, split over its waves, as the
-// shrink does) and adds its columns, whose b has been on its way meanwhile.
+// shrink does) and adds its columns, whose b and y are on their way while the
+// waves' sums are added (asked for before the products, b's registers slow those:
+// 7.0 us instead of 6.5). 16 requests of r 16 beside 4096 x 4096 6.5 us, 7.8 in
+// two launches; one 4.1, 5.7.
 constexpr int kOneWaves = 8;
 
 template <int PIECES, typename XT, typename YT>
@@ -579,11 +583,13 @@ static void run_expand(const LoraProblem& p, const Plan& c, hipStream_t stream) 
   else expand<4, 8, YT>(p, c, stream);
 }
 
-// Whether both steps run in one launch.
+// Whether both steps run in one launch: up to 512 readings of 8 ranks of a (2048 ->
+// 7168, r 8: 256 slots of 512 adapters 11.4 us in one, 12.2 in two; 4096 x 4096: 128
+// requests of r 16 9.5 and 11.4, 256 15.0 and 14.6, 128 of r 32 19.6 and 14.0).
 static bool one_launch(const LoraProblem& p, const Plan& c) {
   if (c.tiles || p.r > 32) return false;
-  const int columns = kOneWaves * 64 * (8 / (p.r / 8));
-  return (long)(p.n < p.S ? p.n : p.S) * ((p.N + columns - 1) / columns) <= 256;
+  const int pieces = p.r / 8, columns = kOneWaves * 64 * (8 / pieces);
+  return (long)(p.n < p.S ? p.n : p.S) * ((p.N + columns - 1) / columns) * pieces <= 512;
 }
 
 template <int PIECES, typename XT, typename YT>

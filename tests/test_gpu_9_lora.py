@@ -57,6 +57,10 @@ CASES = [  # S, n, r, K, N, block_m
     # b shared between rows or not: 2 and 8 rows an adapter, 16 and 17 adapters, rank 64 on
     (32, 16, 16, 136, 264, 64), (31, 16, 16, 136, 264, 64), (136, 17, 8, 72, 264, 64),
     (135, 17, 8, 72, 264, 64), (40, 17, 64, 72, 264, 64), (8, 4, 72, 72, 264, 64),
+    # one launch or two: 512 readings of a
+    (600, 512, 8, 72, 264, 64), (600, 513, 8, 72, 264, 64), (300, 171, 24, 72, 200, 64),
+    (300, 170, 24, 72, 200, 64), (200, 128, 32, 136, 1024, 64), (200, 129, 32, 136, 1024, 64),
+    (20, 20, 32, 136, 1032, 64), (256, 256, 16, 200, 2056, 16), (3, 3, 24, 4168, 1032, 1),
     # thirty-two rows an adapter or fewer
     (12, 3, 32, 136, 264, 64), (11, 3, 32, 136, 264, 64), (96, 3, 8, 520, 136, 64),
     (95, 3, 8, 520, 136, 64), (160, 40, 24, 72, 72, 32),
@@ -104,6 +108,20 @@ def test_lora_uneven_batches(kind):
     got = _run(d, 16)
     d["x"][away.cuda()] = 0
     _check(d, got, y)
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 32, 40])
+@pytest.mark.parametrize("S,n", [(100, 20), (620, 600)])
+def test_lora_one_popular_adapter(S, n, r):
+    # many rows of one adapter where the sizes let few be expected
+    say(f"lora: S={S} n={n} r={r}, one adapter for almost all")
+    ids = torch.full((S,), 7)
+    ids[5::17] = n - 1
+    ids[3::29] = -1
+    d = _inputs(S, n, r, 136, 328, ids=ids)
+    y = d["y"].clone()
+    _check(d, _run(d, 64, out=d["y"].clone()), y)
+    _check(d, _run(d, 8), y)
 
 
 @pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32")])
