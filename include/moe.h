@@ -413,7 +413,8 @@ moe_status moe_forward_small_static(const float* logits, const uint16_t* x, cons
  *  x, residual, residual_out, out   [T, H] of `dtype` (MOE_DTYPE_BF16 or
  *                MOE_DTYPE_F32); residual and residual_out may be NULL.
  *                out or residual_out may be the buffer of x or of residual
- *                (each element is read before it is written), not each other's.
+ *                (each element is read before it is written), not each other's
+ *                (MOE_ERR_UNSUPPORTED).
  *  weight        [H] float32.
  *  Limits: 0 <= T < 2^24, H a multiple of 8 (MOE_DTYPE_F32: 4) and at most
  *  MOE_NORM_MAX_H, eps finite and >= 0 (MOE_ERR_UNSUPPORTED otherwise; with
@@ -452,7 +453,7 @@ moe_status moe_norm_in(const void* x, const void* residual, const float* weight,
  *  out           [T, H], written.
  *  shared, residual, out and next are of `dtype` (MOE_DTYPE_BF16 or _F32).
  *  out or next may be the buffer of residual or of shared, not each other's,
- *  and do not overlap y.
+ *  and do not overlap y (MOE_ERR_UNSUPPORTED).
  *  Limits: k >= 1, 0 <= T, T * k < 2^24, 1 <= E when topk_ids is given (k may
  *  exceed E: a small shard), H, eps and alignment as moe_norm_in (H a multiple
  *  of 4 only when y_dtype and dtype are both MOE_DTYPE_F32); topk_weights,
@@ -500,9 +501,11 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                [0, n) marks a row without an adapter. One alignment serves
  *                every projection of a step.
  *  y             [S, N] of y_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row
- *                stride ldy elements; out likewise with stride ldo; out = y
- *                with equal strides updates in place; otherwise they do not
- *                overlap.
+ *                stride ldy elements; out likewise with stride ldo. out = y
+ *                with equal strides updates in place; otherwise out shares no
+ *                element with y, and never with x (MOE_ERR_UNSUPPORTED; also
+ *                where rows of different strides lie between each other).
+ *                Column slices of one matrix are apart.
  *  workspace     moe_lora_workspace_bytes(S, n, K, r, block_m) bytes (or
  *                more), 256-byte aligned, no initialisation needed.
  *                It holds for every smaller S too. Calls that share one must

@@ -335,6 +335,24 @@ bool bf16_or_f32(int dtype) { return dtype == MOE_DTYPE_BF16 || dtype == MOE_DTY
 size_t elem_bytes(int dtype) { return dtype == MOE_DTYPE_BF16 ? 2 : 4; }
 constexpr int kMaxLength = 1 << 24;  // of a row, where the kernels count in 32 bits
 
+// Whether two buffers share a byte.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + nb && y < x + na;
+}
+
+// Whether S rows of wa bytes, sa apart, share a byte with S rows of wb bytes, sb
+// apart: interleaved column slices of one matrix do not. (Interleaved rows of
+// different strides count as sharing.)
+bool rows_overlap(const void* a, size_t sa, size_t wa, const void* b, size_t sb, size_t wb,
+                  int S) {
+  if (!overlap(a, sa * (S - 1) + wa, b, sb * (S - 1) + wb)) return false;
+  if (S == 1 || sa != sb) return true;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  const size_t d = y >= x ? (y - x) % sa : (sa - (x - y) % sa) % sa;  // of b's rows in a's
+  return d < wa || d + wb > sa;
+}
+
 // Rows and row length of a norm; mult: what H is a multiple of.
 moe_status check_norm(int T, int H, int mult, float eps) {
   if (T < 0 || (long)T >= kMaxSlots) return MOE_ERR_SHAPE;
@@ -356,6 +374,8 @@ MOE_EXPORT moe_status moe_norm_in(const void* x, const void* residual, const flo
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) ||
       !aligned(residual_out, 16) || !aligned(out, 16))
     return MOE_ERR_ALIGN;
+  const size_t bytes = (size_t)T * H * elem_bytes(dtype);
+  if (overlap(out, bytes, residual_out, bytes)) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_in(
       moe::NormInProblem{x, residual, weight, alpha, eps, T, H, dtype, residual_out, out},
       (hipStream_t)stream));
@@ -379,6 +399,11 @@ MOE_EXPORT moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* to
       !aligned(next_weight, 16) || !aligned(out, 16) || !aligned(next, 16) ||
       !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(gate, 4))
     return MOE_ERR_ALIGN;
+  const size_t bytes = (size_t)T * H * elem_bytes(dtype);
+  const size_t y_bytes = (size_t)T * k * H * elem_bytes(y_dtype);
+  if (overlap(out, bytes, next, bytes) || overlap(y, y_bytes, out, bytes) ||
+      overlap(y, y_bytes, next, bytes))
+    return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_out(
       moe::NormOutProblem{y, y_dtype, topk_ids, topk_weights, shared, gate, residual, weight,
                           next_weight, scale, eps, T, E, H, k, dtype, out, next},
@@ -438,6 +463,11 @@ MOE_EXPORT moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const
       !aligned(block_adapter, 4) || !aligned(num_padded, 4) || !aligned(workspace, 256))
     return MOE_ERR_ALIGN;
   if (workspace_bytes < moe::lora_workspace_bytes(S, n, K, r, block_m)) return MOE_ERR_WORKSPACE;
+  const size_t bx = elem_bytes(x_dtype), by = elem_bytes(y_dtype);
+  if (rows_overlap(x, ldx * bx, K * bx, out, ldo * by, N * by, S) ||
+      ((y != out || ldy != ldo) &&
+       rows_overlap(y, ldy * by, N * by, out, ldo * by, N * by, S)))
+    return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_lora_add(
       moe::LoraProblem{x, x_dtype, ldx, a, b, scale, sorted_ids, block_adapter, num_padded, S, n,
                        K, N, r, block_m, workspace, y, y_dtype, ldy, out, ldo},

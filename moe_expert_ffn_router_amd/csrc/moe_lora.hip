@@ -51,9 +51,10 @@ __device__ __forceinline__ Group group_at(const LoraProblem& p, const Plan& c, l
   r.count = __builtin_popcountll(__ballot(r.row >= 0));
   return r;
 }
-// The row of the group's position i, or of its last row past the end.
+// The row of the group's position i, or of its last row past the end (in bounds
+// also for lists whose blocks do not hold their rows first).
 __device__ __forceinline__ int row_at(const Group& g, int i) {
-  return __shfl(g.row, min(i, g.count - 1));
+  return max(__shfl(g.row, min(i, g.count - 1)), 0);
 }
 
 // ---------------------------------------------------------------- shrink ---

@@ -129,13 +129,16 @@ __device__ __forceinline__ float sum_squares(const float (&v)[NV][VEC]) {
 }
 
 // The row this thread works on: W > 1 waves: one row per workgroup; W = 1:
-// a row per wave, four to a workgroup.
+// a row per wave, four to a workgroup. Workgroups lie in a grid of kGridX
+// columns (a launch counts its threads in 32 bits along a dimension).
+constexpr int kGridX = 1 << 20;
 template <int W>
 __device__ __forceinline__ int my_row() {
+  const int group = blockIdx.y * kGridX + blockIdx.x;
   if constexpr (W == 1)
-    return __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    return __builtin_amdgcn_readfirstlane(group * 4 + (threadIdx.x >> 6));
   else
-    return blockIdx.x;
+    return group;
 }
 
 template <int W, int NV, int VEC, typename IO>
@@ -326,7 +329,8 @@ static void by_row_length(int H, bool pairs, F f) {
 
 template <int W>
 static dim3 grid_of(int T) {
-  return dim3(W == 1 ? (T + 3) / 4 : T);
+  const int groups = W == 1 ? (T + 3) / 4 : T;
+  return dim3(groups < kGridX ? groups : kGridX, (groups + kGridX - 1) / kGridX);
 }
 
 template <int VEC, typename IO>

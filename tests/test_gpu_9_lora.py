@@ -227,6 +227,27 @@ def test_lora_empty_and_checks():
     assert torch.equal(d["y"], y)
 
 
+def test_lora_more_groups_than_a_grid_row():
+    say("lora: 70000 rows in blocks of one")
+    d = _inputs(70000, 3, 8, 8, 16)
+    y = d["y"].clone()
+    _check(d, _run(d, 1), y)
+
+
+def test_lora_refuses_out_over_x():
+    say("lora: out over x, adapters on a matrix itself")
+    m = moe()
+    d = _inputs(20, 3, 16, 64, 64)
+    plan = m.align_block(d["ids"], 3, 16)
+    x = d["x"].clone()
+    with pytest.raises(m.MoEError):
+        m.lora_add(d["x"], d["x"], d["a"], d["b"], *plan, 16)
+    torch.cuda.synchronize()
+    assert torch.equal(d["x"], x)
+    out = m.lora_add(d["x"], d["x"], d["a"], d["b"], *plan, 16, out=x.clone())   # y = x
+    _check({**d, "y": x, "scale": d["scale"]}, out, x, scale=False)
+
+
 def test_lora_rows_past_32_bit_offsets():
     # slices of a matrix of more than 2^31 elements
     S, n, K, N, wide = 40000, 2, 64, 64, 65536

@@ -251,6 +251,20 @@ def test_norm_out_streamed(T, k, H, ydt, dt):
     _check_out(pick, 0.5, out[rows.cuda()], nxt[rows.cuda()], dt)
 
 
+@pytest.mark.parametrize("T,H", [((1 << 22) + 7, 8), ((1 << 20) + 3, 1032)])
+def test_norm_rows_past_the_first_grid_row(T, H):
+    say(f"norm_in T={T} H={H}")
+    x = torch.full((T, H), 2.0, dtype=torch.bfloat16, device="cuda")
+    x[-1] = -3
+    w = torch.arange(1, H + 1, device="cuda").float()
+    out, _ = moe().norm_in(x, w, eps=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(out[-1], (-w).bfloat16())
+    assert bool((out[:-1] == w.bfloat16()).all())
+    o, _ = moe().norm_out(x, residual=x)
+    assert torch.equal(o, 2 * x)
+
+
 def test_norm_argument_checks():
     say("norms: binding checks")
     m = moe()

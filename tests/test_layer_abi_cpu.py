@@ -36,6 +36,18 @@ def test_norm_in_validation():
     assert norm_in(T=0, H=12) == SHAPE
 
 
+def test_norm_outputs_apart():
+    # 4 rows of 64 bf16: 512 bytes
+    assert norm_in(ro=P, out=P) == UNSUP and norm_in(ro=P, out=P + 496) == UNSUP
+    assert norm_in(ro=P + 16, out=P) == UNSUP
+    Q = 1 << 30
+    assert norm_out(out=Q, nxt=Q) == UNSUP and norm_out(out=Q + 496, nxt=Q) == UNSUP
+    assert norm_out(out=P, nxt=Q) == UNSUP                   # y: 8 rows, 1024 bytes
+    assert norm_out(out=Q, nxt=P + 1008) == UNSUP
+    assert norm_out(out=P + 1008, nw=None, nxt=None) == UNSUP
+    assert norm_out(out=P - 496, nw=None, nxt=None) == UNSUP
+
+
 def norm_out(y=P, ydt=BF16, ids=P, wts=P, shared=P, gate=P, res=P, w=P, nw=P, scale=1.0,
              eps=1e-6, T=4, E=8, H=64, k=2, dt=BF16, out=P, nxt=P):
     return lib.moe_norm_out(y, ydt, ids, wts, shared, gate, res, w, nw, scale, eps, T, E, H, k,
@@ -112,6 +124,18 @@ def test_lora_validation():
     for bad in ((-1, 3, 64, 16, 16), (4, 0, 64, 16, 16), (4, 3, 60, 16, 16), (4, 3, 64, 12, 16),
                 (4, 3, 64, 16, 3)):
         assert lib.moe_lora_workspace_bytes(*bad) == 0, bad
+    # out apart from x and, unless it is y, from y: rows of 16 columns of fp32 here, 64
+    # bytes each, in a matrix of 256-byte rows
+    Q = 1 << 30
+    apart = dict(S=4, K=16, N=16, xdt=F32, ydt=F32, ldx=64, ldy=64, ldo=64, y=Q, wsb=need * 8)
+
+    def probe(**kw):
+        return lora(**{**apart, **kw})
+    for out, st in ((P, UNSUP), (P + 48, UNSUP), (P + 256 - 48, UNSUP), (P + 256 * 3, UNSUP),
+                    (Q + 16, UNSUP), (Q + 256, UNSUP), (Q - 48, UNSUP)):
+        assert probe(x=P, out=out) == st, hex(out)
+    assert probe(x=P, out=P + 64, ldo=68) == UNSUP           # strides that cross
+    assert probe(x=P, y=P + 64, out=P + 64, ldo=68, ldy=64) == UNSUP
     # the workspace never shrinks as the batch grows
     last = 0
     for S in (0, 1, 2, 17, 64, 65, 300, 4096, 100000):
