@@ -6,8 +6,8 @@
 // the only other work is one (norm_in) or up to two (norm_out) sums of squares
 // per row. Bound by HBM: 2 bytes per bf16 element and stream; for norm_out the
 // k expert rows per token are the largest of them. Measured (captured into a
-// graph): norm_in 4096 x 4096 bf16 with residual 21.6 us = 6.2 TB/s, 16 x 4096
-// 2.7 us; norm_out 4096 x top-8 x 4096 bf16, everything on, 61.7 us = 6.5 TB/s,
+// graph): norm_in 4096 x 4096 bf16 with residual 21.4 us = 6.3 TB/s, 16 x 4096
+// 2.7 us; norm_out 4096 x top-8 x 4096 bf16, everything on, 61.3 us = 6.6 TB/s,
 // 64 x top-8 x 7168 fp32 7.9 us (a row per CU: 64 of them, 330 KB each),
 // 16 x top-8 x 4096 bf16 3.8 us.
 //

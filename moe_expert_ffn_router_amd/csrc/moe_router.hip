@@ -2,9 +2,9 @@
 // cores with K split over the waves of a workgroup (moe_skinny.h), so that one
 // launch serves a single token as well as a prompt and needs no workspace.
 // Bound by what a CU reads: R (MT + NT) rows of x and w per workgroup. Measured
-// (captured into a graph): 16 tokens x 64 experts x 4096 bf16 3.5 us, 64 x 128 x
-// 7168 with fp32 w 8.3 us (the split of w into planes included), 512 x 128 x 4096
-// 5.6 us, 4096 x 128 x 4096 15.0 us: 786 KB per CU at 63 GB/s, where 32 x 64
+// (captured into a graph): 16 tokens x 64 experts x 4096 bf16 3.4 us, 64 x 128 x
+// 7168 with fp32 w 8.4 us (the split of w into planes included), 512 x 128 x 4096
+// 5.6 us, 4096 x 128 x 4096 14.9 us: 786 KB per CU at 63 GB/s, where 32 x 64
 // tiles, one per CU, are the largest that fill the chip.
 #include "../../include/moe.h"
 #include "moe_common.h"
