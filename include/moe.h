@@ -414,7 +414,7 @@ moe_status moe_forward_small_static(const float* logits, const uint16_t* x, cons
  *                MOE_DTYPE_F32); residual and residual_out may be NULL.
  *                out or residual_out may be the buffer of x or of residual
  *                (each element is read before it is written), not each other's
- *                (MOE_ERR_UNSUPPORTED).
+ *                and not part of one (MOE_ERR_UNSUPPORTED).
  *  weight        [H] float32.
  *  Limits: 0 <= T < 2^24, H a multiple of 8 (MOE_DTYPE_F32: 4) and at most
  *  MOE_NORM_MAX_H, eps finite and >= 0 (MOE_ERR_UNSUPPORTED otherwise; with
@@ -452,8 +452,8 @@ moe_status moe_norm_in(const void* x, const void* residual, const float* weight,
  *  next_weight   [H] float32 and next [T, H], both given or both NULL.
  *  out           [T, H], written.
  *  shared, residual, out and next are of `dtype` (MOE_DTYPE_BF16 or _F32).
- *  out or next may be the buffer of residual or of shared, not each other's,
- *  and do not overlap y (MOE_ERR_UNSUPPORTED).
+ *  out or next may be the buffer of residual or of shared, not part of one nor
+ *  each other's, and do not overlap y (MOE_ERR_UNSUPPORTED).
  *  Limits: k >= 1, 0 <= T, T * k < 2^24, 1 <= E when topk_ids is given (k may
  *  exceed E: a small shard), H, eps and alignment as moe_norm_in (H a multiple
  *  of 4 only when y_dtype and dtype are both MOE_DTYPE_F32); topk_weights,
@@ -473,11 +473,13 @@ moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
  *  w             [E, H] of w_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32; fp32 when
  *                x is fp32, MOE_ERR_UNSUPPORTED otherwise).
  *  bias          [E] float32 or NULL.
- *  logits        [T, E] float32, written.
+ *  logits        [T, E] float32, written; apart from x and w
+ *                (MOE_ERR_UNSUPPORTED).
  *  Limits: 0 <= T < 2^24, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8 below
  *  2^24; x and w 16-byte, bias and logits 4-byte aligned. The result is
  *  deterministic. Infinities and NaN in x or w make the logits that read them
- *  non-finite, and no others.
+ *  non-finite, and no others; fp32 values from 3.39e38 on (which round to a bf16
+ *  infinity) count as infinities.
  */
 moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
                              const float* bias, int T, int E, int H, float* logits,
@@ -512,8 +514,9 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                not overlap in time (two graphs captured with it included).
  *  The rank-r intermediate is kept in fp32 and enters the second product
  *  exactly for fp32 y, to 2^-16 of its values for bf16 y (whose own rounding
- *  is 2^-8); products are summed in fp32. The result is deterministic, and a
- *  row's depends on its own x, y and adapter alone.
+ *  is 2^-8); products are summed in fp32. fp32 x and intermediates from 3.39e38
+ *  on count as infinities. The result is deterministic, and a row's depends on
+ *  its own x, y and adapter alone.
  *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8 below 2^24, r a
  *  multiple of 8 in [8, 256], block_m a power of two in [1, 256]; ldx >= K, ldy
  *  and ldo >= N, each a multiple of 8 (of 4 for fp32); x, a, b, y and out

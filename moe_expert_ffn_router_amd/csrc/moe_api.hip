@@ -341,6 +341,12 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return a && b && x < y + nb && y < x + na;
 }
 
+// Whether an output shares a byte with an input of as many bytes without being its
+// buffer: rows of one would then be written while others of the launch read them.
+bool shifted(const void* out, const void* in, size_t n) {
+  return out != in && overlap(out, n, in, n);
+}
+
 // Whether S rows of wa bytes, sa apart, share a byte with S rows of wb bytes, sb
 // apart: interleaved column slices of one matrix do not. (Interleaved rows of
 // different strides count as sharing.)
@@ -375,7 +381,10 @@ MOE_EXPORT moe_status moe_norm_in(const void* x, const void* residual, const flo
       !aligned(residual_out, 16) || !aligned(out, 16))
     return MOE_ERR_ALIGN;
   const size_t bytes = (size_t)T * H * elem_bytes(dtype);
-  if (overlap(out, bytes, residual_out, bytes)) return MOE_ERR_UNSUPPORTED;
+  if (overlap(out, bytes, residual_out, bytes) || shifted(out, x, bytes) ||
+      shifted(out, residual, bytes) || shifted(residual_out, x, bytes) ||
+      shifted(residual_out, residual, bytes))
+    return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_in(
       moe::NormInProblem{x, residual, weight, alpha, eps, T, H, dtype, residual_out, out},
       (hipStream_t)stream));
@@ -402,7 +411,9 @@ MOE_EXPORT moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* to
   const size_t bytes = (size_t)T * H * elem_bytes(dtype);
   const size_t y_bytes = (size_t)T * k * H * elem_bytes(y_dtype);
   if (overlap(out, bytes, next, bytes) || overlap(y, y_bytes, out, bytes) ||
-      overlap(y, y_bytes, next, bytes))
+      overlap(y, y_bytes, next, bytes) || shifted(out, residual, bytes) ||
+      shifted(out, shared, bytes) || shifted(next, residual, bytes) ||
+      shifted(next, shared, bytes))
     return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_out(
       moe::NormOutProblem{y, y_dtype, topk_ids, topk_weights, shared, gate, residual, weight,
@@ -423,6 +434,10 @@ MOE_EXPORT moe_status moe_router_logits(const void* x, int x_dtype, const void* 
   if (!x || !w || !logits) return MOE_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(logits, 4))
     return MOE_ERR_ALIGN;
+  const size_t bytes = (size_t)T * E * sizeof(float);
+  if (overlap(logits, bytes, x, (size_t)T * H * elem_bytes(x_dtype)) ||
+      overlap(logits, bytes, w, (size_t)E * H * elem_bytes(w_dtype)))
+    return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_router_logits(x, x_dtype, w, w_dtype, bias, T, E, H, logits,
                                               (hipStream_t)stream));
 }

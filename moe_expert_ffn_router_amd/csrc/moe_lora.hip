@@ -30,9 +30,9 @@ struct Plan {
   int rows_a;  // of a group of the shrink
 };
 
-// A group: its adapter, first position and this lane's row (lane l: position
-// pos + l; -1 where there is none). A block's rows come first in it, so count
-// rows are in lanes 0 .. count - 1.
+// A group: its adapter, this lane's row (lane l: position l of the group; -1
+// where there is none) and the positions up to its last row. (The alignment puts
+// a block's rows first; nothing here relies on it.)
 struct Group {
   int adapter, count, row;
 };
@@ -48,14 +48,16 @@ __device__ __forceinline__ Group group_at(const LoraProblem& p, const Plan& c, l
   if (lane >= rows || (unsigned)r.row >= (unsigned)p.S || pos >= padded ||
       (unsigned)r.adapter >= (unsigned)p.n)
     r.row = -1;
-  r.count = __builtin_popcountll(__ballot(r.row >= 0));
+  const uint64_t rows_of = __ballot(r.row >= 0);
+  r.count = rows_of ? 64 - __builtin_clzll(rows_of) : 0;
   return r;
 }
-// The row of the group's position i, or of its last row past the end (in bounds
-// also for lists whose blocks do not hold their rows first).
-__device__ __forceinline__ int row_at(const Group& g, int i) {
-  return max(__shfl(g.row, min(i, g.count - 1)), 0);
+// The row of the group's position i, or of its last row past the end; -1: none.
+__device__ __forceinline__ int at_position(const Group& g, int i) {
+  return __shfl(g.row, min(i, g.count - 1));
 }
+// The same to read from: some row where there is none.
+__device__ __forceinline__ int row_at(const Group& g, int i) { return max(at_position(g, i), 0); }
 
 // ---------------------------------------------------------------- shrink ---
 // A workgroup: R NT ranks of a group's adapter, one slice of K, R MT rows at a
@@ -89,8 +91,10 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
       skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, auto s) {
         // (not row_at: the lanes that hold the rows need not be here; 4 divides the rank)
         const int q = q0 + wr;
-        if (t + xr < g.count && q < p.r)
-          *(decltype(s)*)(z + (size_t)p.sorted_ids[(long)gi * c.rows_a + t + xr] * p.r + q) = s;
+        if (t + xr < g.count && q < p.r) {
+          const int row = p.sorted_ids[(long)gi * c.rows_a + t + xr];
+          if ((unsigned)row < (unsigned)p.S) *(decltype(s)*)(z + (size_t)row * p.r + q) = s;
+        }
       });
       __syncthreads();  // the sums are read before the next rows' chunks
     }
@@ -218,8 +222,8 @@ __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, i
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
-    if (at < g.count && n < p.N) {
+    const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = at_position(g, at);
+    if (at < g.count && row >= 0 && n < p.N) {
       YT* op = (YT*)p.out + (size_t)row * p.ldo + n;
       const uint32_t* o = y.w[i];
       if constexpr (kWords == 2) {
@@ -303,8 +307,9 @@ struct Columns {
                                       float scale, const float* z) const {
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-      if (i0 + i < g.count) {
-        YT* op = (YT*)p.out + (size_t)row_at(g, i0 + i) * p.ldo;
+      const int row = at_position(g, i0 + i);
+      if (i0 + i < g.count && row >= 0) {
+        YT* op = (YT*)p.out + (size_t)row * p.ldo;
         float acc[U] = {};
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) {

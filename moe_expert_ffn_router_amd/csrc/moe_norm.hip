@@ -250,7 +250,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_out_kernel(NormOut
       }
 #pragma unroll
       for (int q = 0; q < B; ++q) {
-        const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), u[q]));
+        const float wj =
+            __uint_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), u[q]) & keep[q]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           keep_vec<YT, VEC>(r[q][i], keep[q] & c.mask[i]);

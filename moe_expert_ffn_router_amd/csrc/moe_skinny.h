@@ -14,7 +14,8 @@
 //
 // fp32 operands enter exactly, as three bf16 planes each (round to nearest, the
 // remainder again, and what is left: 8 + 8 + 8 bits). The products of planes
-// p + q <= 2 are summed; the dropped ones are below 2^-23 of the product.
+// p + q <= 2 are summed; the dropped ones are below 2^-23 of the product. (A value
+// that rounds to a bf16 infinity, 3.39e38 or more, gives one less itself: NaN.)
 #pragma once
 
 #include "moe_common.h"

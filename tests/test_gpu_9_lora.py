@@ -198,6 +198,28 @@ def test_lora_workspace_of_a_larger_batch():
         _check(d, _run(d, 64, workspace=ws), y)
 
 
+@pytest.mark.parametrize("S,r", [(70, 40), (70, 16), (12, 40), (12, 16), (600, 16)])
+def test_lora_lists_in_another_order(S, r):
+    # empty places before a block's rows: the same rows, and nothing out of place
+    say(f"lora: lists whose blocks do not hold their rows first, S={S} r={r}")
+    n = 257 if S == 600 else 3
+    d = _inputs(S, n, r, 72, 136)
+    M = 16
+    ids, blocks, padded = moe().align_block(d["ids"], n, M)
+    ids = ids[:ids.numel() // M * M].view(-1, M).flip(1).reshape(-1).contiguous()
+    need = moe().lora_workspace_bytes(S, n, 72, r, M)
+    buf = torch.full((need + 65536,), 77, dtype=torch.uint8, device="cuda")
+    y = d["y"].clone()
+    ref = _run({**d, "y": y.clone()}, M)
+    moe().lora_add(d["y"], d["x"], d["a"], d["b"], ids, blocks, padded, M, scale=d["scale"],
+                   workspace=buf[:need])
+    torch.cuda.synchronize()
+    assert bool((buf[need:] == 77).all())
+    assert torch.equal(d["y"], ref)
+    away = (d["ids"].view(-1) < 0)
+    assert torch.equal(d["y"][away], y[away])
+
+
 def test_lora_empty_and_checks():
     say("lora: S=0, binding checks")
     m = moe()

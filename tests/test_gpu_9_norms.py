@@ -211,6 +211,20 @@ def test_norm_out_defaults_and_three_dim_y():
     _check_out(c, 1.0, out, None, "f32")
 
 
+def test_norm_out_infinite_weight_counts_once():
+    # rows of 3 slots (fewer than are loaded together), the last one's weight infinite:
+    # infinities of y's signs, no NaN from the places of slots that are not there
+    say("norm_out: an infinite weight")
+    y = rand(gen(14), 3 * 3, 136, dtype="f32")
+    w = torch.tensor([[0.5, 0.25, float("inf")], [1.0, 2.0, 3.0], [0.5, 0.25, -float("inf")]],
+                     device="cuda")
+    out, _ = moe().norm_out(y, w)
+    inf = float("inf")
+    assert torch.equal(out[0], torch.sign(y[2]) * inf)
+    assert torch.equal(out[2], torch.sign(y[8]) * -inf)
+    assert bool(torch.isfinite(out[1]).all())
+
+
 def test_norm_empty_batch():
     say("norms T=0")
     x, w = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), torch.ones(64, device="cuda")

@@ -48,6 +48,23 @@ def test_norm_outputs_apart():
     assert norm_out(out=P - 496, nw=None, nxt=None) == UNSUP
 
 
+def test_outputs_are_not_part_of_an_input():
+    # rows of 64 bf16, 512 bytes of them; the very buffer is allowed and tested on the GPU
+    Q, R, Z = 1 << 30, 1 << 31, 1 << 32
+    for d in (128, -128, 496, -496):
+        assert norm_in(x=Q, res=R, ro=None, out=Q + d) == UNSUP
+        assert norm_in(x=Q, res=R, ro=None, out=R + d) == UNSUP
+        assert norm_in(x=Q, res=R, ro=Q + d, out=Z) == UNSUP
+        assert norm_in(x=Q, res=R, ro=R + d, out=Z) == UNSUP
+        assert norm_out(res=Q, shared=R, out=Q + d, nw=None, nxt=None) == UNSUP
+        assert norm_out(res=Q, shared=R, out=R + d, nw=None, nxt=None) == UNSUP
+        assert norm_out(res=Q, shared=R, out=Z, nxt=Q + d) == UNSUP
+        assert norm_out(res=Q, shared=R, out=Z, nxt=R + d) == UNSUP
+    # logits: 4 x 8 fp32, 128 bytes; x 512 bytes, w 1024
+    for out in (Q, Q + 508, Q - 124, R, R + 1020, R - 124):
+        assert router(x=Q, w=R, out=out) == UNSUP
+
+
 def norm_out(y=P, ydt=BF16, ids=P, wts=P, shared=P, gate=P, res=P, w=P, nw=P, scale=1.0,
              eps=1e-6, T=4, E=8, H=64, k=2, dt=BF16, out=P, nxt=P):
     return lib.moe_norm_out(y, ydt, ids, wts, shared, gate, res, w, nw, scale, eps, T, E, H, k,
