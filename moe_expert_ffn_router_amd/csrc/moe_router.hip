@@ -3,9 +3,13 @@
 // launch serves a single token as well as a prompt and needs no workspace.
 // Bound by what a CU reads: R (MT + NT) rows of x and w per workgroup. Measured
 // (captured into a graph): 16 tokens x 64 experts x 4096 bf16 3.4 us, 64 x 128 x
-// 7168 with fp32 w 8.4 us (the split of w into planes included), 512 x 128 x 4096
-// 5.6 us, 4096 x 128 x 4096 14.9 us: 786 KB per CU at 63 GB/s, where 32 x 64
-// tiles, one per CU, are the largest that fill the chip.
+// 7168 with fp32 w 8.4 us (the split of w into planes included), 1024 x 128 x 4096
+// 7.3 us, 4096 x 128 x 4096 14.9 us: 786 KB per CU at 63 GB/s, where 32 x 64
+// tiles, one per CU, are the largest that fill the chip; with fp32 w 19.6 us.
+#include <limits.h>
+
+#include <algorithm>
+
 #include "../../include/moe.h"
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -70,21 +74,37 @@ static void run(const XT* x, const WT* w, const float* bias, int T, int E, int H
 template <typename XT, typename WT>
 static void dispatch(const XT* x, const WT* w, const float* bias, int T, int E, int H,
                      float* logits, hipStream_t stream) {
-  // fp32 tokens take twice the registers of bf16: half the tiles, half the depth
-  constexpr int kHalf = sizeof(XT) == 4 ? 2 : 1;
-  // the largest tiles of which there are 96 (x 4096, 128 experts, bf16): 1024
-  // tokens in 64 of 32 x 64 tokens and experts 11.7 us, in 512 of 16 x 16 9.5; 1536
-  // 11.9 and 13.0; 128 tokens in 64 of 16 x 16 4.8, in 256 of 8 x 8 3.9; 240 5.0
-  // and 5.8
-  const long big = (long)((T + 31) / 32) * ((E + 63) / 64);
-  const long small = (long)((T + 15) / 16) * ((E + 15) / 16);
-  if (big >= 96)
-    run<2, 4 / kHalf, 16, 8, 1>(x, w, bias, T, E, H, logits, stream);
-  else if (small >= 96)
-    run<1, 1, 16, 16, sizeof(XT) == 4 ? 1 : sizeof(WT) == 4 ? 2 : 4>(x, w, bias, T, E, H, logits,
+  constexpr bool kX4 = sizeof(XT) == 4, kW4 = sizeof(WT) == 4;
+  // fp32 w beside bf16 x: its rows are twice as long and every workgroup splits
+  // them into planes, so tiles take half the experts and twice the tokens (4096
+  // tokens x 4096, 128 experts 19.6 us instead of 27.5)
+  constexpr bool kTall = kW4 && !kX4;
+  // The tiles for which a CU reads the least of x and w, the larger where that is
+  // the same. x 4096, bf16: 128 experts, 128 tokens 8 x 8 tiles 3.9 us (16 x 16
+  // 4.8), 1024 16 x 32 7.3 (16 x 16 9.6), 1536 32 x 32 9.0 (32 x 64 11.9, 16 x 16
+  // 13.0); 16384 32 x 64 59.5; 8 experts, 4096 tokens 16 x 16 7.8 (32 x 64 12.9).
+  auto bytes = [&](int t, int e) {
+    const long tiles = (long)((T + t - 1) / t) * ((E + e - 1) / e);
+    return (tiles + 255) / 256 * (t * sizeof(XT) + e * sizeof(WT));
+  };
+  const long big = kX4 ? LONG_MAX : kTall ? bytes(64, 32) : bytes(32, 64);
+  const long square = bytes(32, 32), wide = kTall ? bytes(32, 16) : bytes(16, 32);
+  const long mid = bytes(16, 16), small = bytes(8, 8);
+  const long least = std::min({big, square, wide, mid, small});
+  // with fp32 operands fewer waves or chunks in flight: registers and LDS
+  if constexpr (!kX4) {
+    if (big == least)
+      return run<kTall ? 4 : 2, kTall ? 2 : 4, 16, 8, 1>(x, w, bias, T, E, H, logits, stream);
+  }
+  if (square == least)
+    run<2, 2, 16, kW4 ? 8 : 16, kW4 ? 1 : 2>(x, w, bias, T, E, H, logits, stream);
+  else if (wide == least)
+    run<kTall ? 2 : 1, kTall ? 1 : 2, 16, kX4 ? 8 : 16, kW4 ? 1 : 2>(x, w, bias, T, E, H, logits,
                                                                      stream);
+  else if (mid == least)
+    run<1, 1, 16, 16, kX4 ? 1 : kW4 ? 2 : 4>(x, w, bias, T, E, H, logits, stream);
   else
-    run<1, 1, 8, 16, sizeof(XT) == 4 ? 2 : 4>(x, w, bias, T, E, H, logits, stream);
+    run<1, 1, 8, 16, kX4 ? 2 : 4>(x, w, bias, T, E, H, logits, stream);
 }
 
 }  // namespace router

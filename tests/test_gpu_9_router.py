@@ -32,7 +32,11 @@ SHAPES = [(1, 1, 8), (1, 8, 256), (3, 5, 16), (16, 64, 4096), (17, 65, 264), (31
           (129, 300, 2056), (1, 128, 16392), (300, 60, 2048), (1030, 96, 512),
           # 8-row tiles, 16-row tiles and tiles of 32 tokens, on both sides of their limits
           (95 * 16, 16, 136), (95 * 16 + 1, 16, 136), (95 * 32, 64, 72), (95 * 32 + 1, 33, 200),
-          (2040, 128, 1032), (4100, 70, 264), (1000, 1000, 64)]
+          (2040, 128, 1032), (4100, 70, 264), (1000, 1000, 64),
+          # every tile on both sides of the sizes from which a CU gets one more
+          (2048, 8, 72), (2049, 8, 72), (520, 130, 200), (1024, 128, 136), (1025, 128, 264),
+          (2048, 128, 72), (2049, 97, 136), (4096, 20, 520), (4100, 33, 136), (8200, 64, 72),
+          (4097, 128, 1032)]
 
 
 @pytest.mark.parametrize("T,E,H", SHAPES)
