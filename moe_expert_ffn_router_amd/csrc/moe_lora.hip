@@ -59,6 +59,48 @@ __device__ __forceinline__ int at_position(const Group& g, int i) {
 // The same to read from: some row where there is none.
 __device__ __forceinline__ int row_at(const Group& g, int i) { return max(at_position(g, i), 0); }
 
+// A workgroup's pieces of N rows: the piece 0 of its group, the piece 1 of the group
+// an eighth of them further on, and so forth. A block of few rows has a piece 0
+// alone; the pieces of a full one, a much-used adapter's, are in as many workgroups
+// (256 rows of 4 of 256 adapters, r 16 beside 4096 x 4096: 14.3 us, 46 with the
+// pieces of a group in turn; groups of 8 rows each take 18, but 36 instead of 15.7
+// where every row has an adapter of its own).
+template <int N>
+struct Pieces {
+  int row, adapter;  // of lane l: piece l / N, position l % N
+  uint64_t left;     // lanes with a row, of the pieces still to do
+
+  // the first position of piece j (j * shift < groups)
+  __device__ __forceinline__ static long position(int g, int rows, int groups, int j) {
+    int at = g + j * (groups / 8);
+    if (at >= groups) at -= groups;
+    return (long)at * rows + j * N;
+  }
+  __device__ __forceinline__ Pieces(const LoraProblem& p, const Plan& c, int g, int rows,
+                                    int groups) {
+    const int me = threadIdx.x & 63, lane = min(me, rows - 1);
+    const long pos = position(g, rows, groups, lane / N) + lane % N;
+    const int padded = p.num_padded[0];
+    adapter = p.block_adapter[pos >> c.log2m];
+    row = p.sorted_ids[pos];
+    left = __ballot(me < rows && (unsigned)row < (unsigned)p.S && pos < padded &&
+                    (unsigned)adapter < (unsigned)p.n);
+  }
+  // the next piece's number; its rows
+  __device__ __forceinline__ int next() const { return __builtin_ctzll(left) / N; }
+  __device__ __forceinline__ Group take(int j) {
+    const uint64_t mine = left >> (j * N) & ((1ull << N) - 1);
+    const int lane = threadIdx.x & 63;
+    Group r;
+    r.adapter = __builtin_amdgcn_readlane(adapter, j * N);
+    r.row = __shfl(row, min(j * N + lane, 63));
+    if (!(mine >> lane & 1)) r.row = -1;
+    r.count = 64 - __builtin_clzll(mine);
+    left &= ~(((1ull << N) - 1) << (j * N));
+    return r;
+  }
+};
+
 // ---------------------------------------------------------------- shrink ---
 // A workgroup: R NT ranks of a group's adapter, one slice of K, R MT rows at a
 // time. Bound by reading x and, for few rows, a; every 16 or 32 rows read a again,
@@ -77,12 +119,15 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
   const int end = (int)((long)chunks * (slice + 1) / c.slices);
   float* z = (float*)p.workspace + (size_t)slice * p.S * p.r;
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi, c.rows_a);
-    const uint16_t* a = p.a + (size_t)g.adapter * p.r * p.K;
-    for (int t = 0; t < g.count; t += R * MT) {  // the whole workgroup
+    Pieces<R * MT> pieces(p, c, gi, c.rows_a, groups);
+    while (pieces.left) {  // the whole workgroup
+      const int j = pieces.next();
+      const Group g = pieces.take(j);
+      const uint16_t* a = p.a + (size_t)g.adapter * p.r * p.K;
+      const int* ids = p.sorted_ids + pieces.position(gi, c.rows_a, groups, j);
       skinny::Product<MT, NT, R, XT, uint16_t> m;
       m.lds = lds + wave * m.kLdsBytes;
-      m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, t + i) * p.ldx; });
+      m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, i) * p.ldx; });
       m.w.set([&](int i) { return a + (size_t)min(q0 + i, p.r - 1) * p.K; });
       m.clear();
       // two chunks in flight where their registers allow it
@@ -91,8 +136,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
       skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, auto s) {
         // (not row_at: the lanes that hold the rows need not be here; 4 divides the rank)
         const int q = q0 + wr;
-        if (t + xr < g.count && q < p.r) {
-          const int row = p.sorted_ids[(long)gi * c.rows_a + t + xr];
+        if (xr < g.count && q < p.r) {
+          const int row = ids[xr];
           if ((unsigned)row < (unsigned)p.S) *(decltype(s)*)(z + (size_t)row * p.r + q) = s;
         }
       });
@@ -248,22 +293,22 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int 
   if (n0 >= p.N) return;  // whole waves
   const int n = n0 + (threadIdx.x & 15) * J;
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi, c.rows);
-    if (g.count == 0) continue;
-    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
-    const uint16_t* b = p.b + ((size_t)g.adapter * p.N + min(n, p.N - J)) * p.r;  // J divides N
-    u32x4 bq[STEPS][J];
+    Pieces<16> pieces(p, c, gi, c.rows, groups);
+    while (pieces.left) {
+      const Group g = pieces.take(pieces.next());
+      const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+      const uint16_t* b = p.b + ((size_t)g.adapter * p.N + min(n, p.N - J)) * p.r;  // J divides N
+      u32x4 bq[STEPS][J];
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)
+      for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-        bq[s][j] = *(const u32x4*)(b + (size_t)j * p.r + min(s * 32 + g4 * 8, p.r - 8));
-    for (int t = 0; t * 16 < g.count; ++t) {
+        for (int j = 0; j < J; ++j)
+          bq[s][j] = *(const u32x4*)(b + (size_t)j * p.r + min(s * 32 + g4 * 8, p.r - 8));
       Z16<STEPS, YT> z;
       Y4<J, YT> y;
-      y.load(p, g, t, n);
-      z.load(p, c, g, t, g4 * 8);
-      add_rows(p, g, t, z, y, scale, n, [&](int s, int j) {
+      y.load(p, g, 0, n);
+      z.load(p, c, g, 0, g4 * 8);
+      add_rows(p, g, 0, z, y, scale, n, [&](int s, int j) {
         return __builtin_bit_cast(bf16x8, s * 32 + g4 * 8 < p.r ? bq[s][j] : u32x4{0, 0, 0, 0});
       });
     }
@@ -342,17 +387,17 @@ template <int PIECES, typename YT>
 __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan c, int groups) {
   typedef Columns<PIECES, YT> Cols;
   constexpr int R = Cols::R;
-  __shared__ __align__(16) float zl[64 * R];
+  __shared__ __align__(16) float zl[8 * R];
   const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 6)) * Cols::U * 64 + (threadIdx.x & 63);
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi, c.rows);
-    if (g.count == 0) continue;  // the whole workgroup
-    const float scale = p.scale ? p.scale[g.adapter] : 1.f;
-    Cols m;
-    m.load_b(p, g, n0);
-    m.load_y(p, g, 0, n0);
-    for (int e0 = 0; e0 < g.count * R; e0 += 256) {
-      const int e = e0 + threadIdx.x;
+    Pieces<8> pieces(p, c, gi, c.rows, groups);
+    while (pieces.left) {  // the whole workgroup
+      const Group g = pieces.take(pieces.next());
+      const float scale = p.scale ? p.scale[g.adapter] : 1.f;
+      Cols m;
+      m.load_b(p, g, n0);
+      m.load_y(p, g, 0, n0);
+      const int e = threadIdx.x;  // R of 8 rows: 256 values at most
       const size_t at = (size_t)row_at(g, e / R) * R + e % R, slice = (size_t)p.S * R;
       const float* z = (const float*)p.workspace + at;
       float v = z[0];
@@ -363,13 +408,13 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
           v += (z[k * slice] + z[(k + 1) * slice]) + (z[(k + 2) * slice] + z[(k + 3) * slice]);
       }
       if (e < g.count * R) zl[e] = v;
+      __syncthreads();
+      for (int i0 = 0; i0 < g.count; i0 += Cols::RB) {
+        if (i0) m.load_y(p, g, i0, n0);
+        m.add(p, g, i0, n0, scale, zl + i0 * R);
+      }
+      __syncthreads();  // z is read before the next piece's comes in
     }
-    __syncthreads();
-    for (int i0 = 0; i0 < g.count; i0 += Cols::RB) {
-      if (i0) m.load_y(p, g, i0, n0);
-      m.add(p, g, i0, n0, scale, zl + i0 * R);
-    }
-    __syncthreads();  // z is read before the next group's comes in
   }
 }
 
@@ -395,28 +440,29 @@ __global__ __launch_bounds__(kOneWaves * 64) void one_launch_kernel(LoraProblem 
   const int n0 = (blockIdx.x * NW + wave) * Cols::U * 64 + (threadIdx.x & 63);
   const int chunks = (p.K + kChunk - 1) / kChunk;
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
-    const Group g = group_at(p, c, gi, c.rows);
-    const uint16_t* a = p.a + (size_t)g.adapter * R * p.K;
-    Cols cols;
-    for (int t = 0; t < g.count; t += 8) {  // the whole workgroup
+    Pieces<8> pieces(p, c, gi, c.rows, groups);
+    while (pieces.left) {  // the whole workgroup
+      const Group g = pieces.take(pieces.next());
+      const uint16_t* a = p.a + (size_t)g.adapter * R * p.K;
+      Cols cols;
       Shrink m;
       m.lds = lds + wave * m.kLdsBytes;
-      m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, t + i) * p.ldx; });
+      m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, i) * p.ldx; });
       m.w.set([&](int i) { return a + (size_t)i * p.K; });
       m.clear();
       m.template accumulate<PIECES * (int)sizeof(XT) <= 8 ? 4 : 2>(p.K, wave, chunks, NW);
-      if (t == 0) cols.load_b(p, g, n0);
-      cols.load_y(p, g, t, n0);
+      cols.load_b(p, g, n0);
+      cols.load_y(p, g, 0, n0);
       const float scale = p.scale ? p.scale[g.adapter] : 1.f;
       skinny::reduce_waves<1, PIECES, 8, NW>(m.acc, lds, [&](int wr, int xr, float s) {
         zl[xr * R + wr] = s;
       });
       __syncthreads();
-      for (int i = 0; i < 8 && t + i < g.count; i += Cols::RB) {
-        if (i) cols.load_y(p, g, t + i, n0);
-        cols.add(p, g, t + i, n0, scale, zl + i * R);
+      for (int i = 0; i < g.count; i += Cols::RB) {
+        if (i) cols.load_y(p, g, i, n0);
+        cols.add(p, g, i, n0, scale, zl + i * R);
       }
-      __syncthreads();  // z is read before the next rows' comes in
+      __syncthreads();  // z is read before the next piece's comes in
     }
   }
 }

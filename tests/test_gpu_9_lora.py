@@ -124,6 +124,21 @@ def test_lora_one_popular_adapter(S, n, r):
     _check(d, _run(d, 8), y)
 
 
+@pytest.mark.parametrize("M", [16, 32, 64, 256])
+@pytest.mark.parametrize("S,n,r", [(500, 100, 8), (500, 100, 16), (500, 400, 32), (500, 100, 64),
+                                   (60, 8, 24), (55, 7, 72), (33, 5, 128), (14, 9, 16)])
+def test_lora_runs_of_rows(S, n, r, M):
+    # a few adapters with whole blocks of rows each, beside many with one or none: less
+    # than eight groups, more, and numbers that eight does not divide
+    say(f"lora: runs of rows, S={S} n={n} r={r} M={M}")
+    g = gen(S + n)
+    ids = torch.randint(0, n, (6,), generator=g)[torch.arange(S) * 6 // S]
+    ids[::7] = torch.randint(-1, n, (len(ids[::7]),), generator=g)
+    d = _inputs(S, n, r, 200, 136, ids=ids)
+    y = d["y"].clone()
+    _check(d, _run(d, M, out=d["y"].clone()), y)
+
+
 @pytest.mark.parametrize("xdt,ydt", [("bf16", "bf16"), ("f32", "f32")])
 def test_lora_column_slices(xdt, ydt):
     # x, y and out as column slices of wider matrices; what lies beside them stays
