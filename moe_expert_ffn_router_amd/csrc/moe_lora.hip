@@ -567,11 +567,12 @@ static Plan plan_of(const LoraProblem& p) {
   // 16 rows to a group of the shrink until 32 of them are 256 groups
   c.rows_a = c.many ? (p.S >= 4096 ? 32 : 16) : c.rows;
   // slices of K until some 256 workgroups (of much-used adapters) or 512 have work;
-  // fewer from a rank of 64 on, since the expansion reads the rows' z of every slice
+  // fewer past a rank of 64, since the expansion reads the rows' z of every slice
   // once per 128 columns (512 rows of 8 adapters, 4096 x 4096: r 128 18.9 us, 32 with
-  // as many as for r 64; r 256 31, 60)
+  // as many as for r 64; r 256 31, 60), and past 32 where it takes rows 16 at a time
+  // of which few are there (64 rows of 64 adapters, r 64: 16.9 us, 20.1)
   const long groups = c.many ? p.S / c.rows_a + 1 : p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1;
-  const long weight = p.r > 64 ? (p.r + 31) / 32 : 1;
+  const long weight = p.r > 64 || (p.r > 32 && !c.tiles) ? (p.r + 31) / 32 : 1;
   const long most = max_slices(p.K), want = c.many ? 320 : 512;
   c.slices = 1;
   while (c.slices * 2 <= most && c.slices * 2 * groups * weight <= want) c.slices *= 2;
