@@ -554,6 +554,10 @@ static int max_slices(int K) {
   return most < 1 ? 1 : most > kMaxSlices ? kMaxSlices : most;
 }
 
+static int groups_of(const LoraProblem& p, int rows) {
+  return (int)(align_capacity(p.S, p.n, p.block_m) / rows);
+}
+
 static Plan plan_of(const LoraProblem& p) {
   Plan c{};
   while ((1 << c.log2m) < p.block_m) ++c.log2m;
@@ -562,10 +566,14 @@ static Plan plan_of(const LoraProblem& p) {
   // b shared between rows from 8 rows an adapter on (N 4096, r 16: 512 adapters x
   // 4 rows 44.5 us so, 41.6 row by row; 16 adapters x 8 the same); with so few
   // adapters that their groups do not fill the chip, from 2 (16 adapters x 2 rows
-  // 7.3 us, 8.3 row by row; a rank of 128 x 4 rows 16.7, 14.2)
+  // 7.8 us, 8.3 row by row; r 8 x 6 rows, 2048 -> 7168, 8.5, 11.5; a rank of 128 x 4
+  // rows 16.7, 14.2)
   c.tiles = (long)p.S >= 8L * p.n || (p.n <= 16 && p.S >= 2 * p.n && p.r <= 64);
   // 16 rows to a group of the shrink until 32 of them are 256 groups
-  c.rows_a = c.many ? (p.S >= 4096 ? 32 : 16) : c.rows;
+  if (c.many) c.rows_a = p.S >= 4096 ? 32 : 16;
+  // and 16 where fewer than 8 groups cannot share out their pieces (28 rows of an
+  // adapter of r 128, 936 -> 360, 9.9 us instead of 12.9)
+  else c.rows_a = c.tiles && c.rows > 16 && groups_of(p, c.rows) < 8 ? 16 : c.rows;
   // slices of K until some 256 workgroups (of much-used adapters) or 512 have work;
   // fewer past a rank of 64, since the expansion reads the rows' z of every slice
   // once per 128 columns (512 rows of 8 adapters, 4096 x 4096: r 128 18.9 us, 32 with
@@ -579,9 +587,6 @@ static Plan plan_of(const LoraProblem& p) {
   return c;
 }
 
-static int groups_of(const LoraProblem& p, int rows) {
-  return (int)(align_capacity(p.S, p.n, p.block_m) / rows);
-}
 static int grid_y(int groups) { return groups < 65535 ? groups : 65535; }
 
 template <int MT, int NT, int R, typename XT>
@@ -594,7 +599,14 @@ static void shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
 template <typename XT>
 static void run_shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   const bool pairs = c.many && c.rows_a == 32;
-  if (p.r > 32) pairs ? shrink<2, 4, 16, XT>(p, c, stream) : shrink<1, 4, 16, XT>(p, c, stream);
+  // 16 ranks to a workgroup while those are few (the same 28 rows 8.4 us instead of
+  // 9.9; 80 rows of 6 adapters of r 64, 1520 -> 5936, 9.3 and 10.7; with 176 of them,
+  // 32 rows of 16 adapters of r 64, 2048 x 2048, 9.8 and 9.0)
+  const long narrow =
+      (p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1) * (long)c.slices * ((p.r + 15) / 16);
+  if (c.tiles && !pairs && p.r > 16 && narrow <= 128) shrink<1, 1, 16, XT>(p, c, stream);
+  else if (p.r > 32)
+    pairs ? shrink<2, 4, 16, XT>(p, c, stream) : shrink<1, 4, 16, XT>(p, c, stream);
   else if (p.r > 16)
     pairs ? shrink<2, 2, 16, XT>(p, c, stream) : shrink<1, 2, 16, XT>(p, c, stream);
   else if (pairs) shrink<2, 1, 16, XT>(p, c, stream);

@@ -66,7 +66,10 @@ CASES = [  # S, n, r, K, N, block_m
     (95, 3, 8, 520, 136, 64), (160, 40, 24, 72, 72, 32),
     # thirty-two rows at a time in the shrink
     (4100, 2, 64, 520, 264, 64), (4100, 3, 16, 200, 136, 32), (4095, 2, 24, 136, 72, 256),
-    (4200, 1, 160, 136, 328, 64)]
+    (4200, 1, 160, 136, 328, 64),
+    # few workgroups of the shrink: 16 ranks each, groups of 16 rows below 8 groups of 64
+    (28, 1, 128, 936, 360, 64), (80, 6, 64, 1520, 1000, 64), (90, 11, 40, 1032, 136, 64),
+    (30, 3, 24, 200, 136, 256)]
 
 
 @pytest.mark.parametrize("S,n,r,K,N,block_m", CASES)
