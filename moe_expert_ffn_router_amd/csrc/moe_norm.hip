@@ -15,6 +15,8 @@
 // i + 64 W, ... of VEC elements, NV of them. VEC is what 16 bytes of the largest
 // input hold (y; x of norm_in): with 32 bytes of fp32 to a lane a load of 16
 // would touch every other piece of a line.
+#include <type_traits>
+
 #include "../../include/moe.h"
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -230,14 +232,17 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_out_kernel(NormOut
       if (p.topk_ids) mine = (unsigned)p.topk_ids[s] < (unsigned)p.E;
     }
     uint64_t left = __ballot(mine);
-    while (left) {
-      // the next B slots; where fewer are left the last one again, as zeros
+    // B slots; where fewer are left the last one again, as zeros (its weight too,
+    // which may be infinite). Full batches without that: 61.1 us of the largest case
+    // above instead of 68.4.
+    auto batch_of = [&](auto full) {
+      constexpr bool kFull = decltype(full)::value;
       int u[B], some = 0;
       uint32_t keep[B];
 #pragma unroll
       for (int q = 0; q < B; ++q) {
-        keep[q] = left ? ~0u : 0u;
-        if (left) some = __builtin_ctzll(left);
+        keep[q] = kFull || left ? ~0u : 0u;
+        if (kFull || left) some = __builtin_ctzll(left);
         left &= left - 1;
         u[q] = some;
       }
@@ -259,7 +264,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_out_kernel(NormOut
           for (int e = 0; e < VEC; ++e) v[i][e] += wj * elem<YT, VEC>(r[q][i], e);
         }
       }
-    }
+    };
+    for (int n = __builtin_popcountll(left); n >= B; n -= B) batch_of(std::true_type{});
+    if (left) batch_of(std::false_type{});
   }
   if (p.shared) {
     const float g = p.gate ? 1.0f / (1.0f + expf(-p.gate[row])) : 1.0f;
