@@ -6,8 +6,8 @@
 // partial sums in the workspace (r numbers per row: nothing next to x and y);
 // the expansion adds them up and works b into the rows of y. Small batches run
 // both in one launch.
-// Measured (captured into a graph): 16 requests with r 16 beside 4096 x 4096 6.5
-// us, one 4.1 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
+// Measured (captured into a graph): 16 requests with r 16 beside 4096 x 4096 6.8
+// us, one 4.3 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
 // -> 7168, 16.7 us = 3.6 TB/s; 4096 rows of prompts, 8 adapters of r 64, 4096 x
 // 4096, 25.2 us = 3.2 TB/s.
 #include "../../include/moe.h"
@@ -30,34 +30,42 @@ struct Plan {
   int rows_a;  // of a group of the shrink
 };
 
-// A group: its adapter, this lane's row (lane l: position l of the group; -1
-// where there is none) and the positions up to its last row. (The alignment puts
-// a block's rows first; nothing here relies on it.)
+// Some rows of an adapter: lane l < count has the l-th.
 struct Group {
   int adapter, count, row;
 };
+// The rows of the lanes in `which`. The alignment puts a block's rows first; should
+// a list not, they are brought together here.
+__device__ __forceinline__ Group group_of(int adapter, int row, uint64_t which) {
+  Group r;
+  r.adapter = adapter;
+  r.count = __builtin_popcountll(which);
+  if (which & (which + 1)) {
+    int from = 0, i = 0;
+    for (uint64_t left = which; left; left &= left - 1, ++i)
+      if ((int)(threadIdx.x & 63) == i) from = __builtin_ctzll(left);
+    row = __shfl(row, from);
+  }
+  r.row = row;
+  return r;
+}
+// The group's row i, or its last one past the end.
+__device__ __forceinline__ int row_at(const Group& g, int i) {
+  return __shfl(g.row, min(i, g.count - 1));
+}
+// The rows at g * rows .. of the lists.
 __device__ __forceinline__ Group group_at(const LoraProblem& p, const Plan& c, long g, int rows) {
   const long pos = g * rows;
   const int lane = threadIdx.x & 63;
   // the loads do not wait for each other: past *num_padded the lists still
   // hold what the alignment wrote there
   const int padded = p.num_padded[0];
-  Group r;
-  r.adapter = p.block_adapter[pos >> c.log2m];
-  r.row = p.sorted_ids[pos + min(lane, rows - 1)];
-  if (lane >= rows || (unsigned)r.row >= (unsigned)p.S || pos >= padded ||
-      (unsigned)r.adapter >= (unsigned)p.n)
-    r.row = -1;
-  const uint64_t rows_of = __ballot(r.row >= 0);
-  r.count = rows_of ? 64 - __builtin_clzll(rows_of) : 0;
-  return r;
+  const int adapter = p.block_adapter[pos >> c.log2m];
+  const int row = p.sorted_ids[pos + min(lane, rows - 1)];
+  return group_of(adapter, row,
+                  __ballot(lane < rows && (unsigned)row < (unsigned)p.S && pos < padded &&
+                           (unsigned)adapter < (unsigned)p.n));
 }
-// The row of the group's position i, or of its last row past the end; -1: none.
-__device__ __forceinline__ int at_position(const Group& g, int i) {
-  return __shfl(g.row, min(i, g.count - 1));
-}
-// The same to read from: some row where there is none.
-__device__ __forceinline__ int row_at(const Group& g, int i) { return max(at_position(g, i), 0); }
 
 // A workgroup's pieces of N rows: the piece 0 of its group, the piece 1 of the group
 // an eighth of them further on, and so forth. A block of few rows has a piece 0
@@ -90,14 +98,9 @@ struct Pieces {
   __device__ __forceinline__ int next() const { return __builtin_ctzll(left) / N; }
   __device__ __forceinline__ Group take(int j) {
     const uint64_t mine = left >> (j * N) & ((1ull << N) - 1);
-    const int lane = threadIdx.x & 63;
-    Group r;
-    r.adapter = __builtin_amdgcn_readlane(adapter, j * N);
-    r.row = __shfl(row, min(j * N + lane, 63));
-    if (!(mine >> lane & 1)) r.row = -1;
-    r.count = 64 - __builtin_clzll(mine);
     left &= ~(((1ull << N) - 1) << (j * N));
-    return r;
+    return group_of(__builtin_amdgcn_readlane(adapter, j * N),
+                    __shfl(row, min(j * N + (int)(threadIdx.x & 63), 63)), mine);
   }
 };
 
@@ -112,6 +115,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
                                                                    int rank_tiles, int groups) {
   constexpr int NW = kShrinkWaves;
   __shared__ __align__(16) char lds[skinny::lds_bytes<MT, NT, R, NW, XT, uint16_t>()];
+  __shared__ int rows[R * MT];
   const int slice = blockIdx.x / rank_tiles, q0 = blockIdx.x % rank_tiles * NT * R;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int chunks = (p.K + kChunk - 1) / kChunk;
@@ -121,10 +125,9 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
   for (int gi = blockIdx.y; gi < groups; gi += gridDim.y) {
     Pieces<R * MT> pieces(p, c, gi, c.rows_a, groups);
     while (pieces.left) {  // the whole workgroup
-      const int j = pieces.next();
-      const Group g = pieces.take(j);
+      const Group g = pieces.take(pieces.next());
+      if (threadIdx.x < R * MT) rows[threadIdx.x] = g.row;
       const uint16_t* a = p.a + (size_t)g.adapter * p.r * p.K;
-      const int* ids = p.sorted_ids + pieces.position(gi, c.rows_a, groups, j);
       skinny::Product<MT, NT, R, XT, uint16_t> m;
       m.lds = lds + wave * m.kLdsBytes;
       m.x.set([&](int i) { return (const XT*)p.x + (size_t)row_at(g, i) * p.ldx; });
@@ -134,14 +137,11 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
       constexpr int D = MT * (int)sizeof(XT) / 2 + NT <= 5 ? 2 : 1;
       m.template accumulate<D>(p.K, first + wave, end, NW);
       skinny::reduce_waves<MT, NT, R, NW>(m.acc, lds, [&](int wr, int xr, auto s) {
-        // (not row_at: the lanes that hold the rows need not be here; 4 divides the rank)
+        // (rows: the lanes that hold them need not be here; 4 divides the rank)
         const int q = q0 + wr;
-        if (xr < g.count && q < p.r) {
-          const int row = ids[xr];
-          if ((unsigned)row < (unsigned)p.S) *(decltype(s)*)(z + (size_t)row * p.r + q) = s;
-        }
+        if (xr < g.count && q < p.r) *(decltype(s)*)(z + (size_t)rows[xr] * p.r + q) = s;
       });
-      __syncthreads();  // the sums are read before the next rows' chunks
+      __syncthreads();  // the sums and rows are read before the next ones
     }
   }
 }
@@ -267,8 +267,8 @@ __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, i
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = at_position(g, at);
-    if (at < g.count && row >= 0 && n < p.N) {
+    const int at = t * 16 + ((threadIdx.x >> 4) & 3) * 4 + i, row = row_at(g, at);
+    if (at < g.count && n < p.N) {
       YT* op = (YT*)p.out + (size_t)row * p.ldo + n;
       const uint32_t* o = y.w[i];
       if constexpr (kWords == 2) {
@@ -352,9 +352,8 @@ struct Columns {
                                       float scale, const float* z) const {
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
-      const int row = at_position(g, i0 + i);
-      if (i0 + i < g.count && row >= 0) {
-        YT* op = (YT*)p.out + (size_t)row * p.ldo;
+      if (i0 + i < g.count) {
+        YT* op = (YT*)p.out + (size_t)row_at(g, i0 + i) * p.ldo;
         float acc[U] = {};
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) {
@@ -423,8 +422,8 @@ __global__ __launch_bounds__(256) void expand_columns_kernel(LoraProblem p, Plan
 // workgroup forms z of 8 rows at a time (all of K, split over its waves, as the
 // shrink does) and adds its columns, whose b and y are on their way while the
 // waves' sums are added (asked for before the products, b's registers slow those:
-// 7.0 us instead of 6.5). 16 requests of r 16 beside 4096 x 4096 6.5 us, 7.8 in
-// two launches; one 4.1, 5.7.
+// by 0.5 us). 16 requests of r 16 beside 4096 x 4096 6.8 us, 7.8 in two launches;
+// one 4.3, 5.7.
 constexpr int kOneWaves = 8;
 
 template <int PIECES, typename XT, typename YT>
