@@ -8,8 +8,8 @@
 // both in one launch.
 // Measured (captured into a graph): 16 requests with r 16 beside 4096 x 4096 6.8
 // us, one 4.3 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
-// -> 7168, 16.7 us = 3.6 TB/s; 4096 rows of prompts, 8 adapters of r 64, 4096 x
-// 4096, 25.2 us = 3.2 TB/s.
+// -> 7168, 16.9 us = 3.5 TB/s; 4096 rows of prompts, 8 adapters of r 64, 4096 x
+// 4096, 26.0 us = 3.1 TB/s.
 #include "../../include/moe.h"
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -107,7 +107,7 @@ struct Pieces {
 // ---------------------------------------------------------------- shrink ---
 // A workgroup: R NT ranks of a group's adapter, one slice of K, R MT rows at a
 // time. Bound by reading x and, for few rows, a; every 16 or 32 rows read a again,
-// from L2 (the prompts above: 9.0 us, 5 of them for x at the rate of a copy).
+// from L2 (the prompts above: 10.0 us, 5 of them for x at the rate of a copy).
 constexpr int kShrinkWaves = 8;
 
 template <int MT, int NT, int R, typename XT>
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int 
 // takes whole rows of b, one column of the output each, and fp32 FMAs do the
 // little there is to compute; z lies in LDS, read by all lanes alike, and 8 KB of
 // b per wave are in flight. On matrix tiles, one row of 16 of them used, a wave
-// had 2 KB in flight and the expert slots above took 21 us; they take 11.2 here,
+// had 2 KB in flight and the expert slots above took 21 us; they take 11.3 here,
 // where 45 MB at the rate of a copy are 9.
 template <int PIECES, typename YT>
 struct Columns {
@@ -471,7 +471,7 @@ __global__ __launch_bounds__(kOneWaves * 64) void one_launch_kernel(LoraProblem 
 // all its rows, 16 bytes per lane along b. z stays in registers from one set of
 // columns to the next (it is as large as y's columns from a rank of 64 on), and
 // the next ones' b and y are in flight while these are worked on. The prompts
-// above: 15.7 us, 10 of them for y and out at the rate of a copy.
+// above: 16 us, 10 of them for y and out at the rate of a copy.
 // (Held to 128 registers a rank of 16 took 26.8 us instead of 29.0, 4096 rows of
 // 64 adapters; from a rank of 64 on the registers are needed: 39 instead of 27.)
 template <int J, int STEPS, typename YT>
