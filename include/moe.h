@@ -413,8 +413,8 @@ moe_status moe_forward_small_static(const float* logits, const uint16_t* x, cons
  *  x, residual, residual_out, out   [T, H] of `dtype` (MOE_DTYPE_BF16 or
  *                MOE_DTYPE_F32); residual and residual_out may be NULL.
  *                out or residual_out may be the buffer of x or of residual
- *                (each element is read before it is written), not each other's
- *                and not part of one (MOE_ERR_UNSUPPORTED).
+ *                (each element is read before it is written), not each other's,
+ *                not part of one and not over weight (MOE_ERR_UNSUPPORTED).
  *  weight        [H] float32.
  *  Limits: 0 <= T < 2^24, H a multiple of 8 (MOE_DTYPE_F32: 4) and at most
  *  MOE_NORM_MAX_H, eps finite and >= 0 (MOE_ERR_UNSUPPORTED otherwise; with
@@ -453,7 +453,7 @@ moe_status moe_norm_in(const void* x, const void* residual, const float* weight,
  *  out           [T, H], written.
  *  shared, residual, out and next are of `dtype` (MOE_DTYPE_BF16 or _F32).
  *  out or next may be the buffer of residual or of shared, not part of one nor
- *  each other's, and do not overlap y (MOE_ERR_UNSUPPORTED).
+ *  each other's, and overlap no other operand (MOE_ERR_UNSUPPORTED).
  *  Limits: k >= 1, 0 <= T, T * k < 2^24, 1 <= E when topk_ids is given (k may
  *  exceed E: a small shard), H, eps and alignment as moe_norm_in (H a multiple
  *  of 4 only when y_dtype and dtype are both MOE_DTYPE_F32); topk_weights,

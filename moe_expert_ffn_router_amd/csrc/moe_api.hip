@@ -4,6 +4,8 @@
 
 #include <limits.h>
 
+#include <initializer_list>
+
 #include "../../include/moe.h"
 #include "moe_launch.h"
 
@@ -347,6 +349,18 @@ bool shifted(const void* out, const void* in, size_t n) {
   return out != in && overlap(out, n, in, n);
 }
 
+// Whether an output shares a byte with any of some operands that every row of the launch
+// reads: weights, gates, lists.
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool meets(const void* out, size_t n, std::initializer_list<Span> operands) {
+  for (const Span& s : operands)
+    if (overlap(out, n, s.p, s.n)) return true;
+  return false;
+}
+
 // Whether S rows of wa bytes, sa apart, share a byte with S rows of wb bytes, sb
 // apart: interleaved column slices of one matrix do not. (Interleaved rows of
 // different strides count as sharing.)
@@ -385,6 +399,8 @@ MOE_EXPORT moe_status moe_norm_in(const void* x, const void* residual, const flo
       shifted(out, residual, bytes) || shifted(residual_out, x, bytes) ||
       shifted(residual_out, residual, bytes))
     return MOE_ERR_UNSUPPORTED;
+  const Span w{weight, H * sizeof(float)};
+  if (meets(out, bytes, {w}) || meets(residual_out, bytes, {w})) return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_in(
       moe::NormInProblem{x, residual, weight, alpha, eps, T, H, dtype, residual_out, out},
       (hipStream_t)stream));
@@ -414,6 +430,11 @@ MOE_EXPORT moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* to
       overlap(y, y_bytes, next, bytes) || shifted(out, residual, bytes) ||
       shifted(out, shared, bytes) || shifted(next, residual, bytes) ||
       shifted(next, shared, bytes))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t row = H * sizeof(float), slots = (size_t)T * k * 4;
+  const Span w{weight, row}, nw{next_weight, row}, g{gate, T * sizeof(float)},
+      wts{topk_weights, slots}, ids{topk_ids, slots};
+  if (meets(out, bytes, {w, nw, g, wts, ids}) || meets(next, bytes, {w, nw, g, wts, ids}))
     return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_norm_out(
       moe::NormOutProblem{y, y_dtype, topk_ids, topk_weights, shared, gate, residual, weight,
