@@ -473,7 +473,7 @@ moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
  *  w             [E, H] of w_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32; fp32 when
  *                x is fp32, MOE_ERR_UNSUPPORTED otherwise).
  *  bias          [E] float32 or NULL.
- *  logits        [T, E] float32, written; apart from x and w
+ *  logits        [T, E] float32, written; apart from x, w and bias
  *                (MOE_ERR_UNSUPPORTED).
  *  Limits: 0 <= T < 2^24, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8 below
  *  2^24; x and w 16-byte, bias and logits 4-byte aligned. The result is

@@ -456,8 +456,9 @@ MOE_EXPORT moe_status moe_router_logits(const void* x, int x_dtype, const void* 
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(logits, 4))
     return MOE_ERR_ALIGN;
   const size_t bytes = (size_t)T * E * sizeof(float);
-  if (overlap(logits, bytes, x, (size_t)T * H * elem_bytes(x_dtype)) ||
-      overlap(logits, bytes, w, (size_t)E * H * elem_bytes(w_dtype)))
+  if (meets(logits, bytes, {{x, (size_t)T * H * elem_bytes(x_dtype)},
+                            {w, (size_t)E * H * elem_bytes(w_dtype)},
+                            {bias, E * sizeof(float)}}))
     return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_router_logits(x, x_dtype, w, w_dtype, bias, T, E, H, logits,
                                               (hipStream_t)stream));

@@ -40,3 +40,9 @@ def test_norm_out_outputs_apart_from_every_vector(name, at, size):
         assert norm_out(out=out) == UNSUP and norm_out(nxt=out) == UNSUP
         if name != "nw":
             assert norm_out(out=out, nw=None, nxt=None) == UNSUP
+
+
+def test_router_logits_apart_from_the_bias():
+    # 64 tokens x 16 experts: 4096 bytes of logits, 64 of bias
+    for out in touching(C, 64, 4096):
+        assert lib.moe_router_logits(A, BF16, B, BF16, C, 64, 16, 64, out, None) == UNSUP
