@@ -506,10 +506,12 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                stride ldy elements; out likewise with stride ldo. out = y
  *                with equal strides updates in place; otherwise out shares no
  *                element with y, and never with x (MOE_ERR_UNSUPPORTED; also
- *                where rows of different strides lie between each other).
- *                Column slices of one matrix are apart.
+ *                where rows of different strides lie between each other), nor
+ *                with a, b, scale or the lists. Column slices of one matrix are
+ *                apart.
  *  workspace     moe_lora_workspace_bytes(S, n, K, r, block_m) bytes (or
- *                more), 256-byte aligned, no initialisation needed.
+ *                more), 256-byte aligned, no initialisation needed, apart from
+ *                every other operand (MOE_ERR_UNSUPPORTED).
  *                It holds for every smaller S too. Calls that share one must
  *                not overlap in time (two graphs captured with it included).
  *  The rank-r intermediate is kept in fp32 and enters the second product

@@ -373,6 +373,14 @@ bool rows_overlap(const void* a, size_t sa, size_t wa, const void* b, size_t sb,
   return d < wa || d + wb > sa;
 }
 
+// Whether S rows of wa bytes, sa apart, share a byte with a span.
+bool rows_meet(const void* a, size_t sa, size_t wa, int S, const Span& span) {
+  if (!overlap(a, sa * (S - 1) + wa, span.p, span.n)) return false;
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)span.p;
+  const size_t first = y < x + wa ? 0 : (y - x - wa) / sa + 1;  // row that ends past its start
+  return first < (size_t)S && x + first * sa < y + span.n;
+}
+
 // Rows and row length of a norm; mult: what H is a multiple of.
 moe_status check_norm(int T, int H, int mult, float eps) {
   if (T < 0 || (long)T >= kMaxSlots) return MOE_ERR_SHAPE;
@@ -504,6 +512,20 @@ MOE_EXPORT moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const
   if (rows_overlap(x, ldx * bx, K * bx, out, ldo * by, N * by, S) ||
       ((y != out || ldy != ldo) &&
        rows_overlap(y, ldy * by, N * by, out, ldo * by, N * by, S)))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t rows = moe::align_capacity(S, n, block_m);
+  const Span operands[] = {{a, (size_t)n * r * K * 2},
+                           {b, (size_t)n * r * N * 2},
+                           {scale, n * sizeof(float)},
+                           {sorted_ids, rows * sizeof(int32_t)},
+                           {block_adapter, rows / block_m * sizeof(int32_t)},
+                           {num_padded, sizeof(int32_t)}};
+  const Span ws{workspace, moe::lora_workspace_bytes(S, n, K, r, block_m)};
+  for (const Span& o : operands)
+    if (rows_meet(out, ldo * by, N * by, S, o) || meets(ws.p, ws.n, {o}))
+      return MOE_ERR_UNSUPPORTED;
+  if (rows_meet(x, ldx * bx, K * bx, S, ws) || rows_meet(y, ldy * by, N * by, S, ws) ||
+      rows_meet(out, ldo * by, N * by, S, ws))
     return MOE_ERR_UNSUPPORTED;
   return hip_status(moe::launch_lora_add(
       moe::LoraProblem{x, x_dtype, ldx, a, b, scale, sorted_ids, block_adapter, num_padded, S, n,

@@ -46,3 +46,41 @@ def test_router_logits_apart_from_the_bias():
     # 64 tokens x 16 experts: 4096 bytes of logits, 64 of bias
     for out in touching(C, 64, 4096):
         assert lib.moe_router_logits(A, BF16, B, BF16, C, 64, 16, 64, out, None) == UNSUP
+
+
+LORA = dict(S=4, n=3, K=64, N=64, r=16, M=16, ldx=64, ldy=64, ldo=64)
+
+
+def lora(x=A, a=B, b=C, scale=D, sid=E, ba=F, npad=G, ws=H, wsb=1 << 20, y=J, out=K, **sizes):
+    s = {**LORA, **sizes}
+    return lib.moe_lora_add(x, F32, s["ldx"], a, b, scale, sid, ba, npad, s["S"], s["n"], s["K"],
+                            s["N"], s["r"], s["M"], ws, wsb, y, F32, s["ldy"], out, s["ldo"],
+                            None)
+
+
+# factors 3 x 16 x 64 bf16; lists of round_up(4 + 3 x 15, 16) = 64 rows
+LORA_OPERANDS = [("a", B, 6144), ("b", C, 6144), ("scale", D, 12), ("sid", E, 256), ("ba", F, 16),
+                 ("npad", G, 4)]
+
+
+@pytest.mark.parametrize("name,at,size", LORA_OPERANDS)
+def test_lora_out_apart_from_factors_and_lists(name, at, size):
+    for out in touching(at, max(size, 16), 1024):
+        assert lora(out=out) == UNSUP
+        assert lora(out=out, y=out) == UNSUP                 # in place
+    # the last of 4 rows of a column slice, 4096 bytes apart
+    assert lora(out=at - 3 * 4096, ldo=1024) == UNSUP
+    assert lora(out=at - 3 * 4096 - 240, ldo=1024) == UNSUP
+
+
+def test_lora_workspace_apart_from_every_operand():
+    used = lib.moe_lora_workspace_bytes(4, 3, 64, 16, 16)
+    assert used % 256 == 0 and used > 0
+    for name, at, size in LORA_OPERANDS + [("x", A, 1024), ("y", J, 1024), ("out", K, 1024)]:
+        for ws in {at, at - used + 256, at + (size - 1) // 256 * 256}:
+            assert lora(ws=ws) == UNSUP, (name, hex(ws - at))
+    # in place, and in a row of a strided operand other than the first
+    assert lora(ws=J, y=J, out=J) == UNSUP
+    for name, ld in (("x", "ldx"), ("y", "ldy"), ("out", "ldo")):
+        at = {"x": A, "y": J, "out": K}[name]
+        assert lora(ws=at + 3 * 4096, **{ld: 1024}) == UNSUP, name
