@@ -515,8 +515,7 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                It holds for every smaller S too. Calls that share one must
  *                not overlap in time (two graphs captured with it included).
  *  The rank-r intermediate is kept in fp32 and enters the second product
- *  exactly for fp32 y, to 2^-16 of its values for bf16 y (whose own rounding
- *  is 2^-8); products are summed in fp32. fp32 x and intermediates from 3.39e38
+ *  exactly; products are summed in fp32. fp32 x and intermediates from 3.39e38
  *  on count as infinities. The result is deterministic, and a row's depends on
  *  its own x, y and adapter alone.
  *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8 below 2^24, r a

@@ -152,18 +152,15 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
 // rows, 16 bytes of y, and 16 lanes 256 bytes of a row.
 // STEPS: MFMAs over the rank, 32 of it each.
 
-// z enters the matrix cores as bf16 planes: exactly (3) for fp32 rows of y, to
-// 2^-16 (2) for bf16 rows, whose own rounding is 2^-8.
-template <typename YT>
-constexpr int z_planes() {
-  return sizeof(YT) == 2 ? 2 : 3;
-}
+// z enters the matrix cores exactly, as three bf16 planes. (Two, 16 bits, would take 25.5 us
+// instead of 26.1 for the prompts above, and show 2^-16 of b z where y cancels it.)
+constexpr int kZPlanes = 3;
 
 // z of rows 16 t .. of a group: 8 ranks from q of row lane & 15 in each step (any
 // values past the rank, where b is zero).
-template <int STEPS, typename YT>
+template <int STEPS>
 struct Z16 {
-  bf16x8 f[STEPS][z_planes<YT>()];
+  bf16x8 f[STEPS][kZPlanes];
 
   __device__ __forceinline__ void load(const LoraProblem& p, const Plan& c, const Group& g, int t,
                                        int q) {
@@ -179,7 +176,7 @@ struct Z16 {
         add<kTogether>(v, zp + k * slice, slice, q, p.r);
     }
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s) skinny::split8<z_planes<YT>()>(v[s], f[s]);
+    for (int s = 0; s < STEPS; ++s) skinny::split8<kZPlanes>(v[s], f[s]);
   }
   // N slices, their loads together
   template <int N>
@@ -238,8 +235,8 @@ struct Y4 {
 // Two of the J tiles at a time: their sums go into y's registers.
 template <int J, int STEPS, typename YT, typename F>
 __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, int t,
-                                         const Z16<STEPS, YT>& z, Y4<J, YT>& y, float scale,
-                                         int n, F frag) {
+                                         const Z16<STEPS>& z, Y4<J, YT>& y, float scale, int n,
+                                         F frag) {
   constexpr int kWords = Y4<J, YT>::kWords;
 #pragma unroll
   for (int j = 0; j < J; j += 2) {
@@ -248,7 +245,7 @@ __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, i
     for (int s = 0; s < STEPS; ++s) {
       const bf16x8 b0 = frag(s, j), b1 = frag(s, j + 1);
 #pragma unroll
-      for (int q = z_planes<YT>() - 1; q >= 0; --q) {
+      for (int q = kZPlanes - 1; q >= 0; --q) {
         lo = mfma_bf16(z.f[s][q], b0, lo);
         hi = mfma_bf16(z.f[s][q], b1, hi);
       }
@@ -304,7 +301,7 @@ __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int 
 #pragma unroll
         for (int j = 0; j < J; ++j)
           bq[s][j] = *(const u32x4*)(b + (size_t)j * p.r + min(s * 32 + g4 * 8, p.r - 8));
-      Z16<STEPS, YT> z;
+      Z16<STEPS> z;
       Y4<J, YT> y;
       y.load(p, g, 0, n);
       z.load(p, c, g, 0, g4 * 8);
@@ -472,12 +469,11 @@ __global__ __launch_bounds__(kOneWaves * 64) void one_launch_kernel(LoraProblem 
 // columns to the next (it is as large as y's columns from a rank of 64 on), and
 // the next ones' b and y are in flight while these are worked on. The prompts
 // above: 16 us, 10 of them for y and out at the rate of a copy.
-// (Held to 128 registers a rank of 16 took 26.8 us instead of 29.0, 4096 rows of
-// 64 adapters; from a rank of 64 on the registers are needed: 39 instead of 27.)
+// The registers are what it needs: held to 128 a rank of 16 spills four and takes
+// 28.7 us instead of 27.8 (4096 rows of 64 adapters), and so does a rank of 64 held
+// to 168, three waves a SIMD instead of two: 14, the prompts above 28.3 instead of 26.1.
 template <int J, int STEPS, typename YT>
-__global__ __launch_bounds__(256, STEPS == 1 ? 4 : 1) void expand_tiles_kernel(LoraProblem p,
-                                                                               Plan c,
-                                                                               int groups) {
+__global__ __launch_bounds__(256, 1) void expand_tiles_kernel(LoraProblem p, Plan c, int groups) {
   // rows of b at (n % J) * 16 + n / J, so that a tile's are together; 16 bytes
   // of padding spread a column of them over the banks
   constexpr int kStride = STEPS * 64 + 16;
@@ -507,7 +503,7 @@ __global__ __launch_bounds__(256, STEPS == 1 ? 4 : 1) void expand_tiles_kernel(L
       for (int i = 0; i < kLoads; ++i) bq[i] = from[min((int)threadIdx.x + i * 256, last)];
     };
     const bool mine = wave * 16 < g.count;
-    Z16<STEPS, YT> z;
+    Z16<STEPS> z;
     Y4<J, YT> even, odd;
     load_b(blockIdx.x);
     if (mine) {

@@ -25,8 +25,7 @@ namespace skinny {
 
 constexpr int kChunk = 64;  // k per step of a wave
 
-// 8 floats -> PLANES bf16 fragments whose sum is the floats (3 planes: exactly,
-// 2 planes: to 2^-16).
+// 8 floats -> PLANES bf16 fragments whose sum is the floats (3 planes: exactly).
 template <int PLANES>
 __device__ __forceinline__ void split8(const float (&v)[8], bf16x8 (&out)[PLANES]) {
   u32x4 w[PLANES];
