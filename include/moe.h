@@ -400,7 +400,10 @@ moe_status moe_forward_small_static(const float* logits, const uint16_t* x, cons
  * Around the FFN: the norms before and after it, the router projection and
  * low-rank adapters. These steps are not in the pages; their formulas are
  * stated here in full. Arithmetic and sums are fp32; each output is rounded
- * once (RNE) from the fp32 value.
+ * once (RNE) from the fp32 value. Results are deterministic: equal calls give
+ * equal bits, and no row's values or ids enter another row's result. The order
+ * of a row's sums depends on the call's sizes, though: the same row may differ
+ * in the last bits of the fp32 sums between batches of different sizes.
  */
 
 /*
@@ -476,10 +479,10 @@ moe_status moe_norm_out(const void* y, int y_dtype, const int32_t* topk_ids,
  *  logits        [T, E] float32, written; apart from x, w and bias
  *                (MOE_ERR_UNSUPPORTED).
  *  Limits: 0 <= T < 2^24, 1 <= E <= 1024, T * E < 2^31, H a multiple of 8 below
- *  2^24; x and w 16-byte, bias and logits 4-byte aligned. The result is
- *  deterministic. Infinities and NaN in x or w make the logits that read them
- *  non-finite, and no others; fp32 values from 3.39e38 on (which round to a bf16
- *  infinity) count as infinities.
+ *  2^24; x and w 16-byte, bias and logits 4-byte aligned. Infinities and NaN in
+ *  x or w make the logits that read them non-finite, and no others; fp32 values
+ *  from 3.39e38 on (which round to a bf16 infinity) count as infinities, and
+ *  bits of one below 2^-133 (the smallest bf16) are rounded to that.
  */
 moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dtype,
                              const float* bias, int T, int E, int H, float* logits,
@@ -516,8 +519,8 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *                not overlap in time (two graphs captured with it included).
  *  The rank-r intermediate is kept in fp32 and enters the second product
  *  exactly; products are summed in fp32. fp32 x and intermediates from 3.39e38
- *  on count as infinities. The result is deterministic, and a row's depends on
- *  its own x, y and adapter alone.
+ *  on count as infinities. Bits are fixed for given S, n, K, N, r, block_m and
+ *  types; a batch of another S may add a row's products in another order.
  *  Limits: 0 <= S < 2^24, 1 <= n <= 1024, K and N multiples of 8 below 2^24, r a
  *  multiple of 8 in [8, 256], block_m a power of two in [1, 256]; ldx >= K, ldy
  *  and ldo >= N, each a multiple of 8 (of 4 for fp32); x, a, b, y and out

@@ -15,7 +15,8 @@
 // fp32 operands enter exactly, as three bf16 planes each (round to nearest, the
 // remainder again, and what is left: 8 + 8 + 8 bits). The products of planes
 // p + q <= 2 are summed; the dropped ones are below 2^-23 of the product. (A value
-// that rounds to a bf16 infinity, 3.39e38 or more, gives one less itself: NaN.)
+// that rounds to a bf16 infinity, 3.39e38 or more, gives one less itself: NaN. The
+// planes end at 2^-133, the smallest bf16; the matrix cores keep subnormal ones.)
 #pragma once
 
 #include "moe_common.h"

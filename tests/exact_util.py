@@ -99,9 +99,9 @@ def lora_emulated(t, y_dtype, x_planes=3, z_planes=3):
 
 
 def router_exact(g, T, E, H, x_dtype, kind):
-    """x, w (fp32), the exact logits and how far a result may be off them. `w`: one-hot rows of x pick 24-bit values of w; `x`:
-    the other way round (fp32 x); `rest`: rows of x take the first two planes of a value of
-    w away from it."""
+    """x, w (fp32), the exact logits and how far a result may be off them. `w`: one-hot rows of
+    x pick 24-bit values of w; `x`: the other way round (fp32 x); `rest`: rows of x take the
+    first two planes of a value of w away from it."""
     x, w = torch.zeros(T, H), torch.zeros(E, H)
     if kind == "w":
         w = full_floats(g, E, H)
