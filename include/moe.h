@@ -495,7 +495,9 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  * projection gave, for instance any dense projection of S tokens (k = 1
  * alignment of the tokens' adapter ids), or the experts' down projection
  * inside an FFN workspace between MOE_FFN_STAGE_FC2 and the combine (x = h,
- * ids = adapter * E + expert of every slot; moe_ffn_intermediates).
+ * ids = adapter * E + expert of every slot; moe_ffn_intermediates). A slot
+ * whose expert id is outside [0, E) has no row of h or y here: its id is -1,
+ * where the formula would name another adapter's expert.
  *
  *  x             [S, K] of x_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row
  *                stride ldx elements.

@@ -730,8 +730,8 @@ def lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m: int, sc
              out=None, workspace=None, stream=None, prepare: bool = False):
     """moe_lora_add: out[s] = y[s] + scale[g] * b[g] (a[g] x[s]) for the rows s of
     adapter g in the lists (align_block of the rows' adapter ids [S, 1], or of
-    any ids whose flat slots are the rows); the other rows of ``out`` are left as
-    they are. x [S, K], y [S, N] bfloat16 or float32, a [n, r, K], b [n, N, r]
+    any ids whose flat slots are the rows; -1 for slots of experts that another
+    shard serves); the other rows of ``out`` are left as they are. x [S, K], y [S, N] bfloat16 or float32, a [n, r, K], b [n, N, r]
     bfloat16, scale [n] float32. ``out`` defaults to y (in place). x, y and out
     may be column slices of wider matrices."""
     S, K = _dims(x, "x", 2)
