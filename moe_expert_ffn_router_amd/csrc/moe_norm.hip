@@ -316,21 +316,23 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_out_kernel(NormOut
 constexpr size_t kStreamBytes = (size_t)128 << 20;
 
 // Calls f(W, NV) as compile-time constants for rows of H elements: the fewest
-// waves that hold a row with one vector per thread, where they are at most 16.
-// `pairs`: two vectors per thread, half the waves (a row of 513..1024 vectors).
+// waves that hold a row with one vector per thread, where they are at most 8, then
+// two vectors per thread: half the waves of a row leave room for twice the rows on
+// a CU. Rows of 513 .. 1024 vectors with two instead of one: norm_in 8192 x 7168
+// bf16 84 us instead of 90, 16 x 4096 fp32 2.97 instead of 2.87; norm_out 4096 x
+// top-8 x 7168 bf16 119 instead of 137, 16 x top-8 5.6 instead of 6.0.
 template <int V>
 struct Int {
   static constexpr int value = V;
 };
 template <int VEC, typename F>
-static void by_row_length(int H, bool pairs, F f) {
+static void by_row_length(int H, F f) {
   const int vecs = H / VEC;
   if (vecs <= 64) f(Int<1>{}, Int<1>{});
   else if (vecs <= 128) f(Int<1>{}, Int<2>{});
   else if (vecs <= 256) f(Int<4>{}, Int<1>{});
   else if (vecs <= 512) f(Int<8>{}, Int<1>{});
-  else if (vecs <= 1024 && pairs) f(Int<8>{}, Int<2>{});
-  else if (vecs <= 1024) f(Int<16>{}, Int<1>{});
+  else if (vecs <= 1024) f(Int<8>{}, Int<2>{});
   else if (VEC == 8 || vecs <= 2048) f(Int<16>{}, Int<2>{});
   else if constexpr (VEC == 4) f(Int<16>{}, Int<4>{});
 }
@@ -343,10 +345,7 @@ static dim3 grid_of(int T) {
 
 template <int VEC, typename IO>
 static void run_in(const NormInProblem& p, hipStream_t stream) {
-  // with many rows half the waves per row leave room for twice the rows on a CU:
-  // 1024 x 7168 bf16 12.7 -> 11.4 us, 8192 x 7168 95 -> 85 us (256 rows: the same;
-  // norm_out, which has the experts' rows in flight, 35.3 -> 37.2 us)
-  by_row_length<VEC>(p.H, p.T >= 512, [&](auto w, auto nv) {
+  by_row_length<VEC>(p.H, [&](auto w, auto nv) {
     constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
     norm_in_kernel<W, NV, VEC, IO>
         <<<grid_of<W>(p.T), W == 1 ? 256 : W * 64, 0, stream>>>(p);
@@ -355,7 +354,7 @@ static void run_in(const NormInProblem& p, hipStream_t stream) {
 
 template <int VEC, typename YT, typename IO>
 static void run_out(const NormOutProblem& p, hipStream_t stream) {
-  by_row_length<VEC>(p.H, false, [&](auto w, auto nv) {
+  by_row_length<VEC>(p.H, [&](auto w, auto nv) {
     constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
     const dim3 grid = grid_of<W>(p.T);
     const int threads = W == 1 ? 256 : W * 64;
