@@ -149,7 +149,8 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(LoraProblem p
 // ---------------------------------------------------------------- expand ---
 // D = z (rows) x b (columns), 16 rows and 16 J columns at a time, with column
 // J cc + j in column cc of tile j: a lane then holds J consecutive columns of 4
-// rows, 16 bytes of y, and 16 lanes 256 bytes of a row.
+// rows, 16 bytes of y, and 16 lanes 256 bytes of a row. (J 4 and half of that for
+// bf16 rows and ranks past 64, whose b takes the registers.)
 // STEPS: MFMAs over the rank, 32 of it each.
 
 // z enters the matrix cores exactly, as three bf16 planes. (Two, 16 bits, would take 25.5 us

@@ -309,10 +309,13 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void norm_out_kernel(NormOut
   }
 }
 
-// y rows that together pass this are read around the caches: 256 MB of them
+// y rows that together pass this are read around the caches: 268 MB of them
 // leave nothing in the 256 MB cache that a later kernel would find, and read so
-// they took 64.5 us instead of 75.9 (4096 x 8 rows of 4096 bf16, everything on);
-// 15 MB that FC2 has just written are still there, and took 9.9 us against 8.4.
+// they take 61.2 us instead of 75.7 (4096 x 8 rows of 4096 bf16, everything on; 64.2
+// instead of 79.5 right after another kernel has written them). 15 MB that FC2 has
+// just written are still there, and take 12.1 us instead of 10.1; 59 MB 16.9 instead
+// of 15.7. From 92 to 161 MB the better side depends on the shape and on what ran
+// before: 134 MB in turn with others 33.6 instead of 37.4, just written 43.7 and 42.4.
 constexpr size_t kStreamBytes = (size_t)128 << 20;
 
 // Calls f(W, NV) as compile-time constants for rows of H elements: the fewest
