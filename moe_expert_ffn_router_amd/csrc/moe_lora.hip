@@ -595,12 +595,13 @@ static void shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
 template <typename XT>
 static void run_shrink(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   const bool pairs = c.many && c.rows_a == 32;
-  // 16 ranks to a workgroup while those are few (the same 28 rows 8.4 us instead of
-  // 9.9; 80 rows of 6 adapters of r 64, 1520 -> 5936, 9.3 and 10.7; with 176 of them,
-  // 32 rows of 16 adapters of r 64, 2048 x 2048, 9.8 and 9.0)
+  // 16 ranks to a workgroup while those are one a CU at most (the same 28 rows 8.6 us
+  // instead of 10.0; with 208 of them, 96 rows of 12 adapters of r 64, 2048 -> 8192,
+  // 13.5 and 14.3; with 272, 128 rows of 16 of r 24, 4096 x 4096, 8.7 both; with 288,
+  // 100 rows of 4 of r 128, 2048 x 2048, 11.2 and 10.9)
   const long narrow =
       (p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1) * (long)c.slices * ((p.r + 15) / 16);
-  if (c.tiles && !pairs && p.r > 16 && narrow <= 128) shrink<1, 1, 16, XT>(p, c, stream);
+  if (c.tiles && !pairs && p.r > 16 && narrow <= 256) shrink<1, 1, 16, XT>(p, c, stream);
   else if (p.r > 32)
     pairs ? shrink<2, 4, 16, XT>(p, c, stream) : shrink<1, 4, 16, XT>(p, c, stream);
   else if (p.r > 16)

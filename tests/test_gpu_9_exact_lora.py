@@ -23,6 +23,7 @@ LORA = [  # S, n, r, K, N, block_m
     (64, 3, 8, 136, 136, 64), (64, 3, 16, 136, 136, 16), (64, 3, 24, 4104, 264, 64),
     (64, 3, 64, 136, 136, 64), (64, 3, 128, 264, 136, 64), (64, 3, 256, 1032, 136, 64),
     (1000, 9, 96, 200, 136, 64), (300, 3, 248, 520, 264, 32),
+    (64, 4, 64, 4096, 136, 64), (128, 16, 24, 4096, 136, 64), (100, 4, 128, 2048, 136, 64),
     # 32 rows at a time in the shrink
     (4100, 2, 64, 136, 136, 64), (4100, 3, 16, 200, 136, 32), (4100, 2, 24, 136, 72, 256),
     (4200, 1, 160, 264, 72, 64)]
