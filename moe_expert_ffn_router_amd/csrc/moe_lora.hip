@@ -282,8 +282,8 @@ __device__ __forceinline__ void add_rows(const LoraProblem& p, const Group& g, i
 
 // Few rows of an adapter and a rank above 32: b is most of the traffic and each
 // of its rows is used once or little more. A wave keeps the b of 16 J columns in
-// registers and takes the group's rows 16 at a time (16 requests of r 64 beside
-// 2048 -> 8192: 11 us with the shrink, 12.5 with b shared through LDS).
+// registers and takes the group's rows 16 at a time (16 requests of r 64, an adapter
+// each, beside 2048 -> 8192: 12.3 us with the shrink, 14.6 with b shared through LDS).
 template <int J, int STEPS, typename YT>
 __global__ __launch_bounds__(256) void expand_kernel(LoraProblem p, Plan c, int groups) {
   const int g4 = (threadIdx.x >> 4) & 3;
@@ -559,22 +559,24 @@ static Plan plan_of(const LoraProblem& p) {
   while ((1 << c.log2m) < p.block_m) ++c.log2m;
   c.rows = p.block_m < 64 ? p.block_m : 64;
   c.many = p.block_m >= 32 && (long)p.S >= 32L * p.n;
-  // b shared between rows from 8 rows an adapter on (N 4096, r 16: 512 adapters x
-  // 4 rows 44.5 us so, 41.6 row by row; 16 adapters x 8 the same); with so few
-  // adapters that their groups do not fill the chip, from 2 (16 adapters x 2 rows
-  // 7.8 us, 8.3 row by row; r 8 x 6 rows, 2048 -> 7168, 8.5, 11.5; a rank of 128 x 4
-  // rows 16.7, 14.2)
+  // b shared between rows from 8 rows an adapter on (4096 x 4096, r 16, a quarter of
+  // the rows without an adapter and some adapters popular: 512 adapters x 4 rows 59
+  // us so, 46.8 row by row; 16 adapters x 8 8.0, 13.6); with so few adapters that
+  // their groups do not fill the chip, from 2 and up to a rank of 64 (16 adapters x 2
+  // rows 7.6, 7.7, x 6 8.0, 10.0; r 64 x 2 11.3, 12.2; a rank of 128 x 4 22.7, 17.8).
+  // Of how the rows are spread the host knows nothing: with two for every adapter a
+  // rank of 16 takes 7.8 and 6.5.
   c.tiles = (long)p.S >= 8L * p.n || (p.n <= 16 && p.S >= 2 * p.n && p.r <= 64);
   // 16 rows to a group of the shrink until 32 of them are 256 groups
   if (c.many) c.rows_a = p.S >= 4096 ? 32 : 16;
   // and 16 where fewer than 8 groups cannot share out their pieces (28 rows of an
-  // adapter of r 128, 936 -> 360, 9.9 us instead of 12.9)
+  // adapter of r 128, 936 -> 360, 8.6 us instead of 9.7)
   else c.rows_a = c.tiles && c.rows > 16 && groups_of(p, c.rows) < 8 ? 16 : c.rows;
   // slices of K until some 256 workgroups (of much-used adapters) or 512 have work;
   // fewer past a rank of 64, since the expansion reads the rows' z of every slice
   // once per 128 columns (512 rows of 8 adapters, 4096 x 4096: r 128 18.9 us, 32 with
-  // as many as for r 64; r 256 31, 60), and past 32 where it takes rows 16 at a time
-  // of which few are there (64 rows of 64 adapters, r 64: 16.9 us, 20.1)
+  // as many as for r 64; r 256 32, 62), and past 32 where it takes rows 16 at a time
+  // of which few are there (64 rows of 64 adapters, r 64: 17.2 us, 20.2)
   const long groups = c.many ? p.S / c.rows_a + 1 : p.S / 16 + (p.n < p.S ? p.n : p.S) / 2 + 1;
   const long weight = p.r > 64 || (p.r > 32 && !c.tiles) ? (p.r + 31) / 32 : 1;
   const long most = max_slices(p.K), want = c.many ? 320 : 512;
@@ -616,7 +618,7 @@ template <int J, int STEPS, typename YT>
 static void expand(const LoraProblem& p, const Plan& c, hipStream_t stream) {
   const int groups = groups_of(p, c.rows), units = (p.N + 16 * J - 1) / (16 * J);
   // some 1024 workgroups at work; beyond, one takes several sets of columns, all
-  // of them as many (4096 rows r 128: 43 us; 2048 workgroups 46, 4096 54)
+  // of them as many (4096 rows r 128: 36.8 us; 2048 workgroups 37.6, 4096 46)
   const long live = p.S / c.rows + (p.n < p.S ? p.n : p.S) / 2 + 1;
   const int want = (int)((1024 + live - 1) / live), each = units > want ? units / want : 1;
   if (c.tiles)
