@@ -506,7 +506,10 @@ moe_status moe_router_logits(const void* x, int x_dtype, const void* w, int w_dt
  *  sorted_ids, block_adapter, num_padded   from moe_align_block on the rows'
  *                adapter ids with E = n and the same block_m; an id outside
  *                [0, n) marks a row without an adapter. One alignment serves
- *                every projection of a step.
+ *                every projection of a step. More than 1024 adapters: a call
+ *                for each 1024, with -1 for the rows of the others'. block_m 64
+ *                or more where adapters have many rows: b is read again for
+ *                every block of fewer.
  *  y             [S, N] of y_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row
  *                stride ldy elements; out likewise with stride ldo. out = y
  *                with equal strides updates in place; otherwise out shares no

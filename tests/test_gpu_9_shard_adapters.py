@@ -9,7 +9,7 @@ import oracle
 from oracle import layer_oracle as lo
 from synth import make_inputs
 from tests.gpu_util import TOL, moe, say
-from tests.layer_util import f64, gen, rand
+from tests.layer_util import U, close, f64, gen, rand
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-6
@@ -66,3 +66,27 @@ def test_adapters_on_an_expert_parallel_rank(dtype, block_m, rank):
                                     next_weight=f64(nw), eps=EPS)
     assert oracle.normwise_rel_err(f64(out), ref_out) <= TOL["bf16"]
     assert oracle.normwise_rel_err(f64(nxt), ref_next) <= TOL["bf16"]
+
+
+@pytest.mark.parametrize("r", [8, 40])
+def test_more_adapters_than_a_call_takes(r):
+    say(f"adapters split over two calls, r={r}")
+    m, g = moe(), gen(r)
+    S, n, K, N, M = 200, 1500, 72, 136, 64
+    ids = torch.randint(-1, n, (S, 1), generator=g).int().cuda()
+    x, y = rand(g, S, K, dtype="bf16"), rand(g, S, N, dtype="bf16")
+    a, b = rand(g, n, r, K, dtype="bf16"), rand(g, n, N, r, dtype="bf16")
+    with pytest.raises(m.MoEError):
+        m.align_block(ids, n, M)
+    out = y.clone()
+    for first in (0, 1024):
+        part = slice(first, min(first + 1024, n))
+        count = part.stop - first
+        mine = (ids >= first) & (ids < part.stop)
+        lists = m.align_block(torch.where(mine, ids - first, -1).int(), count, M)
+        m.lora_add(out, x, a[part], b[part], *lists, M)
+    torch.cuda.synchronize()
+    ref = lo.lora_add(f64(y), f64(x), f64(a), f64(b), ids.view(-1).cpu().numpy())
+    mag = lo.lora_add(np.zeros((S, N)), np.abs(f64(x)), np.abs(f64(a)), np.abs(f64(b)),
+                      ids.view(-1).cpu().numpy())
+    close(out, ref, (K + r + 8) * U * mag + U * np.abs(f64(y)), "bf16", "out")
