@@ -9,7 +9,7 @@
 // Measured (captured into a graph): 16 requests with r 16 beside 4096 x 4096 6.8
 // us, one 4.3 us; 512 slots of 8 adapters x 128 experts, r 8, 2048
 // -> 7168, 16.9 us = 3.5 TB/s; 4096 rows of prompts, 8 adapters of r 64, 4096 x
-// 4096, 26.0 us = 3.1 TB/s.
+// 4096, 26.2 us = 3.1 TB/s.
 #include "../../include/moe.h"
 #include "moe_common.h"
 #include "moe_launch.h"
@@ -107,7 +107,7 @@ struct Pieces {
 // ---------------------------------------------------------------- shrink ---
 // A workgroup: R NT ranks of a group's adapter, one slice of K, R MT rows at a
 // time. Bound by reading x and, for few rows, a; every 16 or 32 rows read a again,
-// from L2 (the prompts above: 10.0 us, 5 of them for x at the rate of a copy).
+// from L2 (the prompts above: 9.3 us, 5 of them for x at the rate of a copy).
 constexpr int kShrinkWaves = 8;
 
 template <int MT, int NT, int R, typename XT>
