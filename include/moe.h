@@ -6,6 +6,8 @@
  *       FC1 (gate|up) + SiLU-and-mul  ->  FC2 (down)  ->  top-k weighted combine.
  * Around it: the norms before and after the block (residual add, shared
  * expert, combine), the router projection, low-rank adapters of many requests.
+ * Beside it: tokens in expert order and back with their gradients, layer norm and
+ * its gradients, the matrix product with bias, activation and residual.
  *
  * Sources (web pages; cited by title and section):
  *  - "vLLM support for NVIDIA Vera Rubin NVL72" (Chinese summary), section
@@ -549,6 +551,192 @@ moe_status moe_lora_add(const void* x, int x_dtype, size_t ldx, const uint16_t* 
  */
 moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, int block_m, int dtype,
                                  size_t* h_offset, int* h_dtype, size_t* y_offset, int* y_dtype);
+
+/*
+ * Beside the FFN: tokens in expert order and back, layer norm, and the matrix
+ * product of a shared expert or a dense block; the first two with their
+ * gradients. These steps are not in the pages; their formulas are stated here in
+ * full. Arithmetic and sums are fp32; each output is rounded once (RNE) from the
+ * fp32 value, and sums run in a fixed order: equal calls give equal bits. Vectors
+ * of 16 bytes are used where rows start at multiples of 16; other lengths and
+ * alignments (of an element at least, MOE_ERR_ALIGN below that) run element by
+ * element.
+ */
+
+/*
+ * Tokens in expert order, for expert products of the caller's own: the row of
+ * every (token, slot) pair at its place in the lists of moe_align_block,
+ *   rows[p] = x[sorted_ids[p] / k]   (a copy, bit for bit)
+ *   rows[p] = 0                      where sorted_ids[p] is no slot: padding
+ * for p < *num_padded; later rows are left as they are. Beside them every slot's
+ * place, which the calls below take:
+ *   slot_rows[t, j] = p with sorted_ids[p] == t * k + j, or -1 for a slot whose
+ *   id is outside [0, E) (another shard's: it is in no list).
+ *
+ *  x             [T, H] of `dtype` (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *  topk_ids      [T, k] int32, the ids that the lists were made from.
+ *  sorted_ids, num_padded   from moe_align_block with this E, any block_m;
+ *                R entries of sorted_ids (moe_align_capacity, or more).
+ *  rows          [R, H] of `dtype`, written. slot_rows [T, k] int32, written.
+ *  The outputs overlap no operand and not each other (MOE_ERR_UNSUPPORTED).
+ *  Limits: 0 <= T, 1 <= E, 1 <= k (k may exceed E: a small shard), T * k < 2^24,
+ *  1 <= R < 2^25, 1 <= H <= 2^20 and T * k * H and R * H below 2^37. T == 0
+ *  launches nothing.
+ */
+moe_status moe_dispatch(const void* x, const int32_t* topk_ids, const int32_t* sorted_ids,
+                        const int32_t* num_padded, int T, int E, int H, int k, int R, int dtype,
+                        void* rows, int32_t* slot_rows, moe_stream_t stream);
+
+/*
+ * Gradient of moe_dispatch: dx[t] = sum_j drows[slot_rows[t, j]], in ascending j;
+ * slots without a place (slot_rows outside [0, R)) add nothing.
+ *
+ *  drows         [R, H] and dx [T, H], written, of `dtype`; rows that are no
+ *                slot's are not read. dx overlaps neither drows nor slot_rows.
+ *  Limits: as moe_dispatch.
+ */
+moe_status moe_dispatch_backward(const void* drows, const int32_t* slot_rows, int T, int H, int k,
+                                 int R, int dtype, void* dx, moe_stream_t stream);
+
+/*
+ * Back from expert order with the routing weights:
+ *   out[t] = sum_j topk_weights[t, j] * rows[slot_rows[t, j]], in ascending j;
+ * slots without a place add nothing and their weights are not used, whatever
+ * they are: a token without any gives zeros.
+ *
+ *  rows          [R, H] of rows_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *  topk_weights  [T, k] float32, or NULL: 1.
+ *  out           [T, H] of `dtype` (either), written; overlaps no operand.
+ *  Limits: as moe_dispatch.
+ */
+moe_status moe_combine(const void* rows, int rows_dtype, const int32_t* slot_rows,
+                       const float* topk_weights, int T, int H, int k, int R, int dtype, void* out,
+                       moe_stream_t stream);
+
+/*
+ * Gradients of moe_combine:
+ *   drows[slot_rows[t, j]] = topk_weights[t, j] * dout[t]
+ *   drows[p] = 0 for p < *num_padded where sorted_ids[p] is no slot; later rows
+ *   are left as they are
+ *   dweights[t, j] = sum_c dout[t, c] * rows[slot_rows[t, j], c], 0 for a slot
+ *   without a place
+ *
+ *  dout          [T, H] of `dtype`; rows, drows [R, H] of rows_dtype.
+ *  topk_weights  [T, k] float32, or NULL: 1.
+ *  drows         written; may be the buffer of rows (each element is read before
+ *                it is written), otherwise apart from it.
+ *  dweights      [T, k] float32, written, or NULL: not computed, and rows may be
+ *                NULL.
+ *  sorted_ids, num_padded, R   as moe_dispatch.
+ *  The outputs overlap no other operand. Limits: as moe_dispatch.
+ */
+moe_status moe_combine_backward(const void* dout, int dtype, const void* rows, int rows_dtype,
+                                const int32_t* slot_rows, const float* topk_weights,
+                                const int32_t* sorted_ids, const int32_t* num_padded, int T, int H,
+                                int k, int R, void* drows, float* dweights, moe_stream_t stream);
+
+/*
+ * Layer norm, with the residual add of moe_norm_in in front of it:
+ *   s[t]   = residual[t] + alpha * x[t]        (alpha * x[t] without residual)
+ *   out[t] = (s[t] - mean(s[t])) / sqrt(var(s[t]) + eps) * weight + bias
+ *   residual_out[t] = s[t]
+ * var is the mean square about the mean; the norm takes the unrounded s.
+ *
+ *  x, residual, residual_out, out   [T, H] of `dtype` (MOE_DTYPE_BF16 or
+ *                MOE_DTYPE_F32); residual and residual_out may be NULL. out or
+ *                residual_out may be the buffer of x or of residual, not each
+ *                other's, not part of one and not over weight or bias
+ *                (MOE_ERR_UNSUPPORTED).
+ *  weight, bias  [H] float32, either NULL: 1 and 0.
+ *  Limits: 0 <= T < 2^24, 1 <= H <= MOE_NORM_MAX_H, eps finite and >= 0
+ *  (MOE_ERR_UNSUPPORTED otherwise; with eps = 0 a row of equal values gives NaN).
+ *  A row whose sum or sum of squares leaves the fp32 range is outside the contract.
+ */
+moe_status moe_layer_norm(const void* x, const void* residual, const float* weight,
+                          const float* bias, float alpha, float eps, int T, int H, int dtype,
+                          void* residual_out, void* out, moe_stream_t stream);
+
+/*
+ * Gradients of moe_layer_norm. With u = (s - mean(s)) / sqrt(var(s) + eps), the
+ * statistics computed again from s, and g = dout * weight:
+ *   ds[t]  = (g - mean(g) - u * mean(g * u)) / sqrt(var + eps) + dresidual_out[t]
+ *   dresidual[t] = ds[t],  dx[t] = alpha * ds[t]
+ *   dweight = sum_t dout[t] * u[t],  dbias = sum_t dout[t]
+ *
+ *  dout          [T, H] of `dtype`: the gradient of out.
+ *  s             [T, H] of `dtype`: the residual_out of the forward call, or its x
+ *                where that had neither residual nor an alpha other than 1.
+ *  weight        [H] float32 or NULL: 1.
+ *  dresidual_out [T, H] of `dtype`: the gradient that arrives at residual_out, or
+ *                NULL: none.
+ *  dx            [T, H], written; dresidual [T, H], written, or NULL. Each may be
+ *                the buffer of dout, s or dresidual_out, not part of one nor each
+ *                other's.
+ *  dweight, dbias   [H] float32, written, or NULL. With T == 0 they are zeros.
+ *  workspace     moe_layer_norm_backward_workspace_bytes(T, H) bytes (or more),
+ *                16-byte aligned, no initialisation needed; NULL where neither
+ *                dweight nor dbias is asked for. It holds for every smaller T.
+ *                Calls that share one must not overlap in time (two graphs
+ *                captured with it included).
+ *  dweight, dbias and the workspace overlap no operand (MOE_ERR_UNSUPPORTED).
+ *  Limits: as moe_layer_norm.
+ */
+size_t moe_layer_norm_backward_workspace_bytes(int T, int H);
+moe_status moe_layer_norm_backward(const void* dout, const void* s, const float* weight,
+                                   const void* dresidual_out, float alpha, float eps, int T, int H,
+                                   int dtype, void* dx, void* dresidual, float* dweight,
+                                   float* dbias, void* workspace, size_t workspace_bytes,
+                                   moe_stream_t stream);
+
+/* Activations of moe_linear. */
+enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+  MOE_ACT_GELU = 3,      /* v (1 + erf(v / sqrt 2)) / 2 */
+  MOE_ACT_GELU_TANH = 4  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+};
+
+/*
+ * Matrix product with bias, activation and residual in its epilogue, for instance
+ * the two products of a shared expert (whose output moe_norm_out takes) or of a
+ * dense block:
+ *   gated == 0:  out[t, n] = residual[t, n] + act(x[t] . w[n] + bias[n])
+ *   gated != 0:  out[t, n] = residual[t, n] + act(x[t] . w[n] + bias[n])
+ *                                             * (x[t] . w[N + n] + bias[N + n])
+ * (gate rows, then up rows, as FC1's). Sums are fp32, nothing is rounded before
+ * out; of the products of fp32 operands what lies below 2^-23 of one is left out,
+ * as in moe_router_logits.
+ *
+ *  x             [T, K] of `dtype` (MOE_DTYPE_BF16 or MOE_DTYPE_F32), row stride
+ *                ldx elements.
+ *  w             [N, K] (gated: [2 N, K]) of `dtype`; bias [N] (gated: [2 N])
+ *                float32 or NULL.
+ *  residual      [T, N] of out_dtype, row stride ldr, or NULL (ldr is ignored).
+ *  out           [T, N] of out_dtype (either), row stride ldo, written. It may be
+ *                residual with equal strides; otherwise it shares no element with
+ *                any operand (MOE_ERR_UNSUPPORTED; also where rows of different
+ *                strides lie between each other). Column slices of one matrix are
+ *                apart.
+ *  workspace     moe_linear_workspace_bytes(T, N, K, gated, dtype) bytes (or
+ *                more), 256-byte aligned, no initialisation needed, apart from
+ *                every operand; NULL where that is 0. Calls that share one must
+ *                not overlap in time (two graphs captured with it included).
+ *  Bits are fixed for given sizes and types; a batch of another T may add a row's
+ *  products in another order.
+ *  Limits: 0 <= T < 2^24, 1 <= N < 2^24, K a multiple of 8 below 2^22, ldx a
+ *  multiple of 8 (fp32: 4) in [K, 2^22), ldo and ldr at least N and below 2^31; x
+ *  and w 16-byte aligned, bias, out and residual by their elements. Infinities and
+ *  NaN in a row of x or w make the outputs that read it non-finite, and no
+ *  others; fp32 values from 3.39e38 on (which round to a bf16 infinity) count as
+ *  infinities, and bits of one below 2^-133 are rounded to that. T == 0 launches
+ *  nothing.
+ */
+size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
+moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias, int activation,
+                      int gated, const void* residual, size_t ldr, int T, int N, int K, int dtype,
+                      int out_dtype, void* workspace, size_t workspace_bytes, void* out,
+                      size_t ldo, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -22,6 +22,13 @@ The names mirror the C ABI in include/moe.h:
     lora_add(y, x, a, b, sorted_ids, block_adapter, num_padded, block_m, ...) -> out   adapters of many requests
     norm_out(y, topk_weights, ...)         -> (out, next)              combine + shared expert + norms + residual
     ffn_intermediates(workspace, ...)      -> (h, y)                   an FFN workspace's tensors, for the two above
+    dispatch(x, topk_ids, E, sorted_ids, num_padded, ...) -> (rows, slot_rows)   tokens in expert order
+    dispatch_backward(drows, slot_rows, ...)              -> dx
+    combine(rows, slot_rows, topk_weights, ...)           -> out                 and back, weighted
+    combine_backward(dout, rows, slot_rows, topk_weights, sorted_ids, num_padded, ...) -> (drows, dweights)
+    layer_norm(x, weight, bias, residual=None, ...)       -> (out, residual_out)
+    layer_norm_backward(dout, s, weight, ...)             -> (dx, dresidual, dweight, dbias)
+    linear(x, w, bias=None, activation=ACT_NONE, gated=False, residual=None, ...) -> out
 """
 from __future__ import annotations
 
@@ -40,6 +47,7 @@ STAGE_FC1, STAGE_FC2, STAGE_COMBINE, STAGE_PREP = 1 << 0, 1 << 1, 1 << 2, 1 << 3
 PREPARED = 1 << 11  # with STAGE_FC1: an earlier call ran STAGE_PREP (see include/moe.h)
 NO_XCD_REMAP = 1 << 8
 FORWARD_ONE_KERNEL = 1 << 9  # forward_small: the whole layer as one cooperative launch
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4  # activations of linear
 RANGE_GEMM = 1 << 10  # bf16 prefill blocks: 256 x 256 tiles over per-expert token ranges
 ABI_VERSION = 1
 
@@ -49,7 +57,10 @@ EXPORTS = ("moe_status_str", "moe_abi_version", "moe_route_topk", "moe_align_cap
            "moe_ffn_fp8_block", "moe_ffn_f32", "moe_small_max_tokens",
            "moe_forward_small_workspace_bytes", "moe_forward_small", "moe_forward_small_static",
            "moe_norm_in", "moe_norm_out", "moe_router_logits", "moe_lora_workspace_bytes",
-           "moe_lora_add", "moe_ffn_intermediates")
+           "moe_lora_add", "moe_ffn_intermediates", "moe_dispatch", "moe_dispatch_backward",
+           "moe_combine", "moe_combine_backward", "moe_layer_norm",
+           "moe_layer_norm_backward_workspace_bytes", "moe_layer_norm_backward",
+           "moe_linear_workspace_bytes", "moe_linear")
 STATIC_SCRATCH_BYTES = 32 << 20  # MOE_STATIC_SCRATCH_BYTES
 
 
@@ -116,6 +127,24 @@ def _load() -> ctypes.CDLL:
                                  P]
     lib.moe_ffn_intermediates.restype = I
     lib.moe_ffn_intermediates.argtypes = [I, I, I, I, I, I, I, P, P, P, P]
+    lib.moe_dispatch.restype = I
+    lib.moe_dispatch.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, P]
+    lib.moe_dispatch_backward.restype = I
+    lib.moe_dispatch_backward.argtypes = [P, P, I, I, I, I, I, P, P]
+    lib.moe_combine.restype = I
+    lib.moe_combine.argtypes = [P, I, P, P, I, I, I, I, I, P, P]
+    lib.moe_combine_backward.restype = I
+    lib.moe_combine_backward.argtypes = [P, I, P, I, P, P, P, P, I, I, I, I, P, P, P]
+    lib.moe_layer_norm.restype = I
+    lib.moe_layer_norm.argtypes = [P, P, P, P, F, F, I, I, I, P, P, P]
+    lib.moe_layer_norm_backward_workspace_bytes.restype = Z
+    lib.moe_layer_norm_backward_workspace_bytes.argtypes = [I, I]
+    lib.moe_layer_norm_backward.restype = I
+    lib.moe_layer_norm_backward.argtypes = [P, P, P, P, F, F, I, I, I, P, P, P, P, P, Z, P]
+    lib.moe_linear_workspace_bytes.restype = Z
+    lib.moe_linear_workspace_bytes.argtypes = [I, I, I, I, I]
+    lib.moe_linear.restype = I
+    lib.moe_linear.argtypes = [P, Z, P, P, I, I, P, Z, I, I, I, I, I, P, Z, P, Z, P]
     if lib.moe_abi_version() != ABI_VERSION:
         raise ImportError(f"libmoe ABI {lib.moe_abi_version()} != binding ABI {ABI_VERSION}")
     return lib
@@ -790,3 +819,247 @@ def ffn_intermediates(workspace, T: int, E: int, H: int, I: int, k: int, block_m
         return workspace[at.value:at.value + T * k * cols * size].view(t).view(T * k, cols)
 
     return view(h_at, h_dt, I), view(y_at, y_dt, H)
+
+
+# ------------------------------------------------------- beside the FFN ---
+
+def _rows_lists(sorted_ids, num_padded, dev: int) -> int:
+    """The lists of an alignment as the rows in expert order take them; their length R."""
+    if not (isinstance(num_padded, torch.Tensor) and num_padded.dtype is torch.int32
+            and num_padded.get_device() == dev >= 0 and num_padded.numel() >= 1):
+        _need(num_padded, "num_padded", _I32, torch.device("cuda", max(dev, 0)), min_numel=1)
+    R = _dims(sorted_ids, "sorted_ids", 1)[0]
+    _same(sorted_ids, "sorted_ids", _I32, dev, (R,))
+    return R
+
+
+def dispatch(x, topk_ids, E: int, sorted_ids, num_padded, out=None, slot_rows=None, stream=None,
+             prepare: bool = False):
+    """moe_dispatch: the rows of x [T, H] (bfloat16 or float32) in expert order, and every slot's
+    place among them. topk_ids [T, k] and E as given to align_block, sorted_ids [R] and num_padded
+    as it returned them. Returns (rows [R, H], slot_rows [T, k] int32): rows that pad an expert's
+    run are zeros, those from num_padded on are not written; slot_rows is -1 for a slot whose id is
+    outside [0, E)."""
+    T, H = _dims(x, "x", 2)
+    code = _act(x, "x")
+    dev = x.get_device()
+    _same(x, "x", (x.dtype,), dev, (T, H))
+    k = _dims(topk_ids, "topk_ids", 2)[1]
+    _same(topk_ids, "topk_ids", _I32, dev, (T, k))
+    R = _rows_lists(sorted_ids, num_padded, dev)
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out = _empty(x, (R, H), x.dtype, stream)
+    else:
+        _same(out, "out", (x.dtype,), dev, (R, H))
+    if slot_rows is None:
+        slot_rows = _empty(topk_ids, (T, k), torch.int32, stream)
+    else:
+        _same(slot_rows, "slot_rows", _I32, dev, (T, k))
+    keep = (x, topk_ids, sorted_ids, num_padded, out, slot_rows)
+    args = (x.data_ptr(), topk_ids.data_ptr(), sorted_ids.data_ptr(), num_padded.data_ptr(), T, E,
+            H, k, R, code, out.data_ptr(), slot_rows.data_ptr(), raw)
+    return _run(lib.moe_dispatch, args, keep, prepare, (out, slot_rows))
+
+
+def dispatch_backward(drows, slot_rows, out=None, stream=None, prepare: bool = False):
+    """moe_dispatch_backward: dx [T, H] from the gradient drows [R, H] of the rows and the slots'
+    places slot_rows [T, k]; the rows of no slot are not read."""
+    R, H = _dims(drows, "drows", 2)
+    code = _act(drows, "drows")
+    dev, like = drows.get_device(), (drows.dtype,)
+    _same(drows, "drows", like, dev, (R, H))
+    T, k = _dims(slot_rows, "slot_rows", 2)
+    _same(slot_rows, "slot_rows", _I32, dev, (T, k))
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out = _empty(drows, (T, H), drows.dtype, stream)
+    else:
+        _same(out, "out", like, dev, (T, H))
+    args = (drows.data_ptr(), slot_rows.data_ptr(), T, H, k, R, code, out.data_ptr(), raw)
+    return _run(lib.moe_dispatch_backward, args, (drows, slot_rows, out), prepare, out)
+
+
+def combine(rows, slot_rows, topk_weights=None, dtype=None, out=None, stream=None,
+            prepare: bool = False):
+    """moe_combine: out[t] = sum_j topk_weights[t, j] * rows[slot_rows[t, j]] (weight 1 without
+    topk_weights); slots without a place add nothing. rows [R, H] bfloat16 or float32, out [T, H]
+    of ``dtype`` (by default the rows')."""
+    R, H = _dims(rows, "rows", 2)
+    code_r = _act(rows, "rows")
+    dev = rows.get_device()
+    _same(rows, "rows", (rows.dtype,), dev, (R, H))
+    T, k = _dims(slot_rows, "slot_rows", 2)
+    _same(slot_rows, "slot_rows", _I32, dev, (T, k))
+    if topk_weights is not None:
+        _same(topk_weights, "topk_weights", _F32, dev, (T, k))
+    if dtype is None:
+        dtype = rows.dtype if out is None else out.dtype
+    if dtype not in _ACT:
+        raise TypeError(f"dtype is {dtype}, expected one of {tuple(_ACT)}")
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out = _empty(rows, (T, H), dtype, stream)
+    else:
+        _same(out, "out", (dtype,), dev, (T, H))
+    args = (rows.data_ptr(), code_r, slot_rows.data_ptr(), _ptr(topk_weights), T, H, k, R,
+            _ACT[dtype], out.data_ptr(), raw)
+    return _run(lib.moe_combine, args, (rows, slot_rows, topk_weights, out), prepare, out)
+
+
+def combine_backward(dout, rows, slot_rows, topk_weights, sorted_ids, num_padded, drows=None,
+                     dweights=None, stream=None, prepare: bool = False):
+    """moe_combine_backward: the gradients of combine's rows and weights from dout [T, H]. Returns
+    (drows [R, H] of the rows' type, dweights [T, k] float32); topk_weights None: weight 1. Rows of
+    drows that pad a run are zeros, those from num_padded on are not written; drows may be rows
+    itself."""
+    T, H = _dims(dout, "dout", 2)
+    code, code_r = _act(dout, "dout"), _act(rows, "rows")
+    dev = dout.get_device()
+    _same(dout, "dout", (dout.dtype,), dev, (T, H))
+    k = _dims(slot_rows, "slot_rows", 2)[1]
+    _same(slot_rows, "slot_rows", _I32, dev, (T, k))
+    R = _rows_lists(sorted_ids, num_padded, dev)
+    _same(rows, "rows", (rows.dtype,), dev, (R, H))
+    if topk_weights is not None:
+        _same(topk_weights, "topk_weights", _F32, dev, (T, k))
+    raw = _launch_stream(dev, stream)
+    if drows is None:
+        drows = _empty(rows, (R, H), rows.dtype, stream)
+    else:
+        _same(drows, "drows", (rows.dtype,), dev, (R, H))
+    if dweights is None:
+        dweights = _empty(slot_rows, (T, k), torch.float32, stream)
+    else:
+        _same(dweights, "dweights", _F32, dev, (T, k))
+    keep = (dout, rows, slot_rows, topk_weights, sorted_ids, num_padded, drows, dweights)
+    args = (dout.data_ptr(), code, rows.data_ptr(), code_r, slot_rows.data_ptr(),
+            _ptr(topk_weights), sorted_ids.data_ptr(), num_padded.data_ptr(), T, H, k, R,
+            drows.data_ptr(), dweights.data_ptr(), raw)
+    return _run(lib.moe_combine_backward, args, keep, prepare, (drows, dweights))
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, alpha: float = 1.0, eps: float = 1e-5,
+               out=None, residual_out=None, stream=None, prepare: bool = False):
+    """moe_layer_norm: s = residual + alpha * x; out = layer norm of s times ``weight`` plus
+    ``bias`` (either None: 1 and 0); residual_out = s. x, residual [T, H] bfloat16 or float32,
+    weight, bias [H] float32. Returns (out, residual_out); residual_out is None (and s not stored)
+    without a residual unless a buffer is given. out or residual_out may be x or residual itself."""
+    T, H = shape = _dims(x, "x", 2)
+    code = _act(x, "x")
+    dev, like = x.get_device(), (x.dtype,)
+    _same(x, "x", like, dev, shape)
+    if weight is not None:
+        _same(weight, "weight", _F32, dev, (H,))
+    if bias is not None:
+        _same(bias, "bias", _F32, dev, (H,))
+    if residual is not None:
+        _same(residual, "residual", like, dev, shape)
+    raw = _launch_stream(dev, stream)
+    if residual_out is not None:
+        _same(residual_out, "residual_out", like, dev, shape)
+    elif residual is not None:
+        residual_out = _empty(x, shape, x.dtype, stream)
+    if out is None:
+        out = _empty(x, shape, x.dtype, stream)
+    else:
+        _same(out, "out", like, dev, shape)
+    keep = (x, residual, weight, bias, out, residual_out)
+    args = (x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(bias), alpha, eps, T, H, code,
+            _ptr(residual_out), out.data_ptr(), raw)
+    return _run(lib.moe_layer_norm, args, keep, prepare, (out, residual_out))
+
+
+def layer_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(lib.moe_layer_norm_backward_workspace_bytes(T, H))
+
+
+def layer_norm_backward(dout, s, weight=None, dresidual_out=None, alpha: float = 1.0,
+                        eps: float = 1e-5, dx=None, dresidual=None, dweight=None, dbias=None,
+                        workspace=None, stream=None, prepare: bool = False):
+    """moe_layer_norm_backward: the gradients of layer_norm from dout [T, H], the sum s [T, H] it
+    normalised (its residual_out, or x) and what arrives at residual_out. Returns (dx, dresidual,
+    dweight, dbias): dx = alpha * ds; dresidual = ds, None without dresidual_out unless a buffer is
+    given; dweight [H] float32, None without a weight unless a buffer is given; dbias [H] float32.
+    dx or dresidual may be dout, s or dresidual_out itself."""
+    T, H = shape = _dims(dout, "dout", 2)
+    code = _act(dout, "dout")
+    dev, like = dout.get_device(), (dout.dtype,)
+    _same(dout, "dout", like, dev, shape)
+    _same(s, "s", like, dev, shape)
+    if weight is not None:
+        _same(weight, "weight", _F32, dev, (H,))
+    if dresidual_out is not None:
+        _same(dresidual_out, "dresidual_out", like, dev, shape)
+    raw = _launch_stream(dev, stream)
+    if dresidual is not None:
+        _same(dresidual, "dresidual", like, dev, shape)
+    elif dresidual_out is not None:
+        dresidual = _empty(dout, shape, dout.dtype, stream)
+    if dx is None:
+        dx = _empty(dout, shape, dout.dtype, stream)
+    else:
+        _same(dx, "dx", like, dev, shape)
+    if dweight is not None:
+        _same(dweight, "dweight", _F32, dev, (H,))
+    elif weight is not None:
+        dweight = _empty(dout, (H,), torch.float32, stream)
+    if dbias is None:
+        dbias = _empty(dout, (H,), torch.float32, stream)
+    else:
+        _same(dbias, "dbias", _F32, dev, (H,))
+    need = layer_norm_backward_workspace_bytes(T, H)
+    if workspace is None:
+        workspace = _empty(dout, (max(need, 256),), torch.uint8, stream)
+    else:
+        _need(workspace, "workspace", (torch.uint8,), dout.device, min_numel=need)
+    keep = (dout, s, weight, dresidual_out, dx, dresidual, dweight, dbias, workspace)
+    args = (dout.data_ptr(), s.data_ptr(), _ptr(weight), _ptr(dresidual_out), alpha, eps, T, H,
+            code, dx.data_ptr(), _ptr(dresidual), _ptr(dweight), dbias.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), raw)
+    return _run(lib.moe_layer_norm_backward, args, keep, prepare, (dx, dresidual, dweight, dbias))
+
+
+def linear_workspace_bytes(T: int, N: int, K: int, gated: bool, dtype: int) -> int:
+    return int(lib.moe_linear_workspace_bytes(T, N, K, int(bool(gated)), dtype))
+
+
+def linear(x, w, bias=None, activation: int = ACT_NONE, gated: bool = False, residual=None,
+           dtype=None, out=None, workspace=None, stream=None, prepare: bool = False):
+    """moe_linear: out [T, N] = residual + act(x w^T + bias), or gated residual + act(x wg^T + bg)
+    * (x wu^T + bu) with w [2 N, K] and bias [2 N] holding the gate rows, then the up rows. x [T, K]
+    and w bfloat16 or float32 (the same), bias float32, activation ACT_*; residual and out of
+    ``dtype`` (by default the residual's, else x's). x, residual and out may be column slices of
+    wider matrices; out may be residual itself."""
+    T, K = _dims(x, "x", 2)
+    n = _dims(w, "w", 2)[0]
+    code = _act(x, "x")
+    dev = x.get_device()
+    ldx = _need_rows(x, "x", (x.dtype,))
+    _same(w, "w", (x.dtype,), dev, (n, K))
+    if gated and n % 2:
+        raise ValueError(f"w has shape {tuple(w.shape)}, expected [2 N, K={K}]")
+    N = n // 2 if gated else n
+    if bias is not None:
+        _same(bias, "bias", _F32, dev, (n,))
+    if dtype is None:
+        like = residual if residual is not None else x if out is None else out
+        dtype = like.dtype
+    if dtype not in _ACT:
+        raise TypeError(f"dtype is {dtype}, expected one of {tuple(_ACT)}")
+    ldr = 0 if residual is None else _need_rows(residual, "residual", (dtype,), dev, (T, N))
+    raw = _launch_stream(dev, stream)
+    if out is None:
+        out, ldo = _empty(x, (T, N), dtype, stream), N
+    else:
+        ldo = _need_rows(out, "out", (dtype,), dev, (T, N))
+    need = linear_workspace_bytes(T, N, K, gated, code)
+    if workspace is not None:
+        _need(workspace, "workspace", (torch.uint8,), x.device, min_numel=need)
+    elif need:
+        workspace = _empty(x, (need,), torch.uint8, stream)
+    keep = (x, w, bias, residual, out, workspace)
+    args = (x.data_ptr(), ldx, w.data_ptr(), _ptr(bias), activation, int(bool(gated)),
+            _ptr(residual), ldr, T, N, K, code, _ACT[dtype], _ptr(workspace),
+            0 if workspace is None else workspace.numel(), out.data_ptr(), ldo, raw)
+    return _run(lib.moe_linear, args, keep, prepare, out)

@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe.so")
 SOURCES = ["moe_api.hip", "moe_route.hip", "moe_align.hip", "moe_ffn.hip", "moe_gemm.hip",
-           "moe_norm.hip", "moe_router.hip", "moe_lora.hip"]
+           "moe_norm.hip", "moe_router.hip", "moe_lora.hip", "moe_dispatch.hip",
+           "moe_layer_norm.hip", "moe_linear.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 CFLAGS = [

@@ -556,3 +556,212 @@ MOE_EXPORT moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, i
   *h_dtype = *y_dtype = bf16 ? MOE_DTYPE_BF16 : MOE_DTYPE_F32;
   return MOE_OK;
 }
+
+// ---------------------------------------------------- beside the FFN ---
+
+// Sizes of rows in expert order (of a backward or a way back: without E).
+static moe_status check_rows(int T, int E, int H, int k, int R) {
+  if (T < 0 || E < 1 || k < 1 || (long)T * k >= kMaxSlots) return MOE_ERR_SHAPE;
+  if (H < 1 || H > 1 << 20 || R < (T > 0 ? 1 : 0) || R >= 1 << 25) return MOE_ERR_SHAPE;
+  if ((long)T * k * H >= 1L << 37 || (long)R * H >= 1L << 37) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+MOE_EXPORT moe_status moe_dispatch(const void* x, const int32_t* topk_ids,
+                                   const int32_t* sorted_ids, const int32_t* num_padded, int T,
+                                   int E, int H, int k, int R, int dtype, void* rows,
+                                   int32_t* slot_rows, moe_stream_t stream) {
+  if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_rows(T, E, H, k, R);
+  if (s != MOE_OK || T == 0) return s;
+  if (!x || !topk_ids || !sorted_ids || !num_padded || !rows || !slot_rows) return MOE_ERR_NULL;
+  const size_t b = elem_bytes(dtype);
+  if (!aligned(x, b) || !aligned(rows, b) || !aligned(topk_ids, 4) || !aligned(sorted_ids, 4) ||
+      !aligned(num_padded, 4) || !aligned(slot_rows, 4))
+    return MOE_ERR_ALIGN;
+  const size_t slots = (size_t)T * k * 4, row_bytes = (size_t)R * H * b;
+  const Span in[] = {{x, (size_t)T * H * b}, {topk_ids, slots}, {sorted_ids, (size_t)R * 4},
+                     {num_padded, 4}};
+  if (overlap(rows, row_bytes, slot_rows, slots)) return MOE_ERR_UNSUPPORTED;
+  for (const Span& o : in)
+    if (meets(rows, row_bytes, {o}) || meets(slot_rows, slots, {o})) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_dispatch(
+      moe::DispatchProblem{x, topk_ids, sorted_ids, num_padded, T, E, H, k, R, dtype, rows,
+                           slot_rows},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_combine(const void* rows, int rows_dtype, const int32_t* slot_rows,
+                                  const float* topk_weights, int T, int H, int k, int R, int dtype,
+                                  void* out, moe_stream_t stream) {
+  if (!bf16_or_f32(dtype) || !bf16_or_f32(rows_dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_rows(T, 1, H, k, R);
+  if (s != MOE_OK || T == 0) return s;
+  if (!rows || !slot_rows || !out) return MOE_ERR_NULL;
+  const size_t b = elem_bytes(dtype), rb = elem_bytes(rows_dtype);
+  if (!aligned(rows, rb) || !aligned(out, b) || !aligned(slot_rows, 4) ||
+      !aligned(topk_weights, 4))
+    return MOE_ERR_ALIGN;
+  const size_t slots = (size_t)T * k * 4;
+  if (meets(out, (size_t)T * H * b,
+            {{rows, (size_t)R * H * rb}, {slot_rows, slots}, {topk_weights, slots}}))
+    return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_combine(
+      moe::CombineProblem{rows, rows_dtype, slot_rows, topk_weights, T, H, k, R, dtype, out},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_dispatch_backward(const void* drows, const int32_t* slot_rows, int T,
+                                            int H, int k, int R, int dtype, void* dx,
+                                            moe_stream_t stream) {
+  return moe_combine(drows, dtype, slot_rows, nullptr, T, H, k, R, dtype, dx, stream);
+}
+
+MOE_EXPORT moe_status moe_combine_backward(const void* dout, int dtype, const void* rows,
+                                           int rows_dtype, const int32_t* slot_rows,
+                                           const float* topk_weights, const int32_t* sorted_ids,
+                                           const int32_t* num_padded, int T, int H, int k, int R,
+                                           void* drows, float* dweights, moe_stream_t stream) {
+  if (!bf16_or_f32(dtype) || !bf16_or_f32(rows_dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_rows(T, 1, H, k, R);
+  if (s != MOE_OK || T == 0) return s;
+  if (!dout || (!rows && dweights) || !slot_rows || !sorted_ids || !num_padded || !drows)
+    return MOE_ERR_NULL;
+  const size_t b = elem_bytes(dtype), rb = elem_bytes(rows_dtype);
+  if (!aligned(dout, b) || !aligned(rows, rb) || !aligned(drows, rb) || !aligned(slot_rows, 4) ||
+      !aligned(topk_weights, 4) || !aligned(sorted_ids, 4) || !aligned(num_padded, 4) ||
+      !aligned(dweights, 4))
+    return MOE_ERR_ALIGN;
+  const size_t slots = (size_t)T * k * 4, row_bytes = (size_t)R * H * rb;
+  const Span in[] = {{dout, (size_t)T * H * b}, {slot_rows, slots}, {topk_weights, slots},
+                     {sorted_ids, (size_t)R * 4}, {num_padded, 4}};
+  if (shifted(drows, rows, row_bytes) || overlap(drows, row_bytes, dweights, slots) ||
+      overlap(dweights, slots, rows, row_bytes))
+    return MOE_ERR_UNSUPPORTED;
+  for (const Span& o : in)
+    if (meets(drows, row_bytes, {o}) || meets(dweights, slots, {o})) return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_combine_backward(
+      moe::CombineBackwardProblem{dout, dtype, rows, rows_dtype, slot_rows, topk_weights,
+                                  sorted_ids, num_padded, T, H, k, R, drows, dweights},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT moe_status moe_layer_norm(const void* x, const void* residual, const float* weight,
+                                     const float* bias, float alpha, float eps, int T, int H,
+                                     int dtype, void* residual_out, void* out,
+                                     moe_stream_t stream) {
+  if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_norm(T, H, 1, eps);
+  if (s != MOE_OK || T == 0) return s;
+  if (!x || !out) return MOE_ERR_NULL;
+  const size_t b = elem_bytes(dtype), bytes = (size_t)T * H * b;
+  if (!aligned(x, b) || !aligned(residual, b) || !aligned(residual_out, b) || !aligned(out, b) ||
+      !aligned(weight, 4) || !aligned(bias, 4))
+    return MOE_ERR_ALIGN;
+  if (overlap(out, bytes, residual_out, bytes) || shifted(out, x, bytes) ||
+      shifted(out, residual, bytes) || shifted(residual_out, x, bytes) ||
+      shifted(residual_out, residual, bytes))
+    return MOE_ERR_UNSUPPORTED;
+  const Span w{weight, H * sizeof(float)}, bi{bias, H * sizeof(float)};
+  if (meets(out, bytes, {w, bi}) || meets(residual_out, bytes, {w, bi}))
+    return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_layer_norm(
+      moe::LayerNormProblem{x, residual, weight, bias, alpha, eps, T, H, dtype, residual_out, out},
+      (hipStream_t)stream));
+}
+
+MOE_EXPORT size_t moe_layer_norm_backward_workspace_bytes(int T, int H) {
+  if (check_norm(T, H, 1, 0.f) != MOE_OK) return 0;
+  return moe::layer_norm_backward_workspace_bytes(T, H);
+}
+
+MOE_EXPORT moe_status moe_layer_norm_backward(const void* dout, const void* s,
+                                              const float* weight, const void* dresidual_out,
+                                              float alpha, float eps, int T, int H, int dtype,
+                                              void* dx, void* dresidual, float* dweight,
+                                              float* dbias, void* workspace,
+                                              size_t workspace_bytes, moe_stream_t stream) {
+  if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
+  moe_status st = check_norm(T, H, 1, eps);
+  if (st != MOE_OK) return st;
+  const bool sums = dweight || dbias;
+  const size_t used = sums ? moe::layer_norm_backward_workspace_bytes(T, H) : 0;
+  if ((T > 0 && (!dout || !s || !dx)) || (used && !workspace)) return MOE_ERR_NULL;
+  const size_t b = elem_bytes(dtype), bytes = (size_t)T * H * b, vec = H * sizeof(float);
+  if (!aligned(dout, b) || !aligned(s, b) || !aligned(dresidual_out, b) || !aligned(dx, b) ||
+      !aligned(dresidual, b) || !aligned(weight, 4) || !aligned(dweight, 4) ||
+      !aligned(dbias, 4) || (used && !aligned(workspace, 16)))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes < used) return MOE_ERR_WORKSPACE;
+  const Span w{weight, vec};
+  const void* in[] = {dout, s, dresidual_out};
+  if (overlap(dx, bytes, dresidual, bytes) || meets(dx, bytes, {w}) || meets(dresidual, bytes, {w}))
+    return MOE_ERR_UNSUPPORTED;
+  for (const void* p : in)
+    if (shifted(dx, p, bytes) || shifted(dresidual, p, bytes)) return MOE_ERR_UNSUPPORTED;
+  const Span rows[] = {{dout, bytes}, {s, bytes}, {dresidual_out, bytes}, {dx, bytes},
+                       {dresidual, bytes}, w};
+  for (const Span& o : rows)
+    if (meets(dweight, vec, {o}) || meets(dbias, vec, {o}) || (used && meets(workspace, used, {o})))
+      return MOE_ERR_UNSUPPORTED;
+  if (overlap(dweight, vec, dbias, vec) ||
+      (used && meets(workspace, used, {{dweight, vec}, {dbias, vec}})))
+    return MOE_ERR_UNSUPPORTED;
+  return hip_status(moe::launch_layer_norm_backward(
+      moe::LayerNormBackwardProblem{dout, s, weight, dresidual_out, alpha, eps, T, H, dtype, dx,
+                                    dresidual, dweight, dbias, (float*)workspace},
+      (hipStream_t)stream));
+}
+
+static moe_status check_linear(int T, int N, int K, int dtype) {
+  if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || (long)T >= kMaxSlots || N < 1 || N >= kMaxLength) return MOE_ERR_SHAPE;
+  if (K < 8 || K % 8 != 0 || K >= 1 << 22) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+MOE_EXPORT size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype) {
+  if (check_linear(T, N, K, dtype) != MOE_OK) return 0;
+  return moe::linear_workspace_bytes(T, N, K, gated != 0, dtype);
+}
+
+MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias,
+                                 int activation, int gated, const void* residual, size_t ldr,
+                                 int T, int N, int K, int dtype, int out_dtype, void* workspace,
+                                 size_t workspace_bytes, void* out, size_t ldo,
+                                 moe_stream_t stream) {
+  if (!bf16_or_f32(out_dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_GELU_TANH)
+    return MOE_ERR_UNSUPPORTED;
+  moe_status s = check_linear(T, N, K, dtype);
+  if (s != MOE_OK) return s;
+  const size_t b = elem_bytes(dtype), ob = elem_bytes(out_dtype);
+  if (ldx < (size_t)K || ldx >= 1 << 22 || ldx % (16 / b) != 0) return MOE_ERR_SHAPE;
+  if (ldo < (size_t)N || ldo > INT_MAX || (residual && (ldr < (size_t)N || ldr > INT_MAX)))
+    return MOE_ERR_SHAPE;
+  if (T == 0) return MOE_OK;
+  const size_t used = moe::linear_workspace_bytes(T, N, K, gated != 0, dtype);
+  if (!x || !w || !out || (used && !workspace)) return MOE_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(residual, ob) ||
+      !aligned(out, ob) || (used && !aligned(workspace, 256)))
+    return MOE_ERR_ALIGN;
+  if (workspace_bytes < used) return MOE_ERR_WORKSPACE;
+  const size_t n = gated ? 2 * (size_t)N : N, ldrb = ldr * ob;
+  const Span ws{used ? workspace : nullptr, used};
+  const Span vecs[] = {{w, n * K * b}, {bias, n * sizeof(float)}, ws};
+  for (const Span& o : vecs)
+    if (o.p && rows_meet(out, ldo * ob, N * ob, T, o)) return MOE_ERR_UNSUPPORTED;
+  if (rows_overlap(x, ldx * b, K * b, out, ldo * ob, N * ob, T) ||
+      (residual && (residual != out || ldr != ldo) &&
+       rows_overlap(residual, ldrb, N * ob, out, ldo * ob, N * ob, T)))
+    return MOE_ERR_UNSUPPORTED;
+  if (used && (meets(ws.p, ws.n, {vecs[0], vecs[1]}) || rows_meet(x, ldx * b, K * b, T, ws) ||
+               (residual && rows_meet(residual, ldrb, N * ob, T, ws))))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t four = 4 * ob;
+  const bool by_four = N % 4 == 0 && ldo % 4 == 0 && aligned(out, four) &&
+                       (!residual || (ldr % 4 == 0 && aligned(residual, four)));
+  return hip_status(moe::launch_linear(
+      moe::LinearProblem{x, ldx, w, bias, activation, gated != 0, residual, ldr, T, N, K, dtype,
+                         out_dtype, workspace, out, ldo, by_four},
+      (hipStream_t)stream));
+}

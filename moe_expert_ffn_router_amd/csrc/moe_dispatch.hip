@@ -1,0 +1,271 @@
+// Tokens in expert order and back: dispatch copies every token's row to the places
+// that the alignment gave its slots, combine sums the rows of a token's slots with the
+// routing weights, and each has its gradient. With at[s] the place of slot s (-1: none)
+//   dispatch           rows[at[t,j]] = x[t], zeros in the places that pad a run
+//   its gradient       dx[t] = sum_j drows[at[t,j]]: the combine without weights
+//   combine            out[t] = sum_j w[t,j] rows[at[t,j]]
+//   its gradient       drows[at[t,j]] = w[t,j] dout[t], dw[t,j] = dout[t] . rows[at[t,j]]
+//
+// Bound by HBM: each kernel reads and writes a row once. A wave takes a row (or a
+// piece of it), lanes along it, sums in a fixed order in fp32.
+#include <algorithm>
+#include <type_traits>
+
+#include "../../include/moe.h"
+#include "moe_common.h"
+#include "moe_launch.h"
+#include "moe_rows.h"
+
+namespace moe {
+namespace dispatch {
+
+using namespace rows;
+
+// Waves of a launch in workgroups of four, these in a grid of kGridX columns (a launch
+// counts its threads in 32 bits along a dimension).
+constexpr int kGridX = 1 << 20;
+__device__ __forceinline__ int my_wave() {
+  const int group = blockIdx.y * kGridX + blockIdx.x;
+  return __builtin_amdgcn_readfirstlane(group * 4 + (threadIdx.x >> 6));
+}
+static dim3 grid_of(long waves, int pieces = 1) {
+  const long groups = (waves + 3) / 4;
+  return dim3((unsigned)std::min<long>(groups, kGridX), (unsigned)((groups + kGridX - 1) / kGridX),
+              pieces);
+}
+
+// The rows of a call are copied in words of 16 bytes where every row starts at one,
+// else by elements.
+template <typename U>
+__device__ __forceinline__ void fill_row(U* to, int units, U value) {
+  for (int c = threadIdx.x & 63; c < units; c += 64) to[c] = value;
+}
+
+// N words of 64 lanes each from `from`, those past the row's end its last one.
+constexpr int kCopy = 8;
+template <typename U>
+__device__ __forceinline__ void load_piece(const U* from, int c0, int units, U (&v)[kCopy]) {
+#pragma unroll
+  for (int i = 0; i < kCopy; ++i) v[i] = from[min(c0 + i * 64, units - 1)];
+}
+template <typename U>
+__device__ __forceinline__ void store_piece(U* to, int c0, int units, const U (&v)[kCopy]) {
+#pragma unroll
+  for (int i = 0; i < kCopy; ++i)
+    if (c0 + i * 64 < units) to[c0 + i * 64] = v[i];
+}
+
+struct Lists {
+  const int32_t* topk_ids;    // [S]
+  const int32_t* sorted_ids;  // [R]
+  const int32_t* num_padded;
+  int32_t* slot_rows;  // [S]
+  int S, E, R;
+};
+
+// One wave per place (the first R waves): its token's row, or zeros where it pads a
+// run; then a wave for every 64 slots: -1 for those of another shard's experts. Places
+// at and past num_padded are left alone.
+template <typename U>
+__global__ __launch_bounds__(256) void places_kernel(const U* __restrict__ x, Lists l, int units,
+                                                     int k, U* __restrict__ rows) {
+  const int w = my_wave(), lane = threadIdx.x & 63;
+  if (w >= l.R) {
+    const long s = (long)(w - l.R) * 64 + lane;
+    if (s < l.S && (unsigned)l.topk_ids[s] >= (unsigned)l.E) l.slot_rows[s] = -1;
+    return;
+  }
+  if (w >= l.num_padded[0]) return;
+  const int slot = __builtin_amdgcn_readfirstlane(l.sorted_ids[w]);
+  U* to = rows + (size_t)w * units;
+  if ((unsigned)slot >= (unsigned)l.S) {
+    fill_row(to, units, U{});
+    return;
+  }
+  if (lane == 0) l.slot_rows[slot] = w;
+  const U* from = x + (size_t)(slot / k) * units;
+  for (int c = lane; c < units; c += 64 * kCopy) {
+    U v[kCopy];
+    load_piece(from, c, units, v);
+    store_piece(to, c, units, v);
+  }
+}
+
+// The sum over a token's slots, 64 at a time: lane l holds slot l's place and weight.
+// A wave takes 64 vectors of a token's row; slots without a place are not read.
+constexpr int kBatch = 8;
+template <int VEC, bool WEIGHTED, typename YT, typename IO>
+__global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
+                                                      const int32_t* __restrict__ slot_rows,
+                                                      const float* __restrict__ weights, int T,
+                                                      int H, int k, int R, int pieces,
+                                                      IO* __restrict__ out) {
+  const int w = my_wave(), lane = threadIdx.x & 63;
+  const int t = w / pieces, c = (w - t * pieces) * 64 + lane, vecs = H / VEC;
+  if (t >= T) return;
+  const int col = min(c, vecs - 1) * VEC;
+  float v[VEC] = {};
+  for (int j0 = 0; j0 < k; j0 += 64) {
+    const int j = j0 + lane;
+    int at = -1;
+    float wl = 1.f;
+    if (j < k) {
+      at = slot_rows[(size_t)t * k + j];
+      if (WEIGHTED) wl = weights[(size_t)t * k + j];
+    }
+    uint64_t left = __ballot((unsigned)at < (unsigned)R);
+    while (left) {
+      // where fewer than kBatch are left the last one again, its values and weight as zeros
+      int row[kBatch], some = 0;
+      uint32_t keep[kBatch];
+      float wj[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        keep[q] = left ? ~0u : 0u;
+        if (left) some = __builtin_ctzll(left);
+        left &= left - 1;
+        row[q] = __builtin_amdgcn_readlane(at, some);
+        wj[q] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_int(wl), some) & keep[q]);
+      }
+      Vec<YT, VEC> r[kBatch];
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) r[q] = load_vec<YT, VEC>(y + (size_t)row[q] * H + col);
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        keep_vec<YT, VEC>(r[q], keep[q]);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) v[e] += wj[q] * elem<YT, VEC>(r[q], e);
+      }
+    }
+  }
+  if (c < vecs) store_vec<IO, VEC>(out + (size_t)t * H + col, v);
+}
+
+// One wave per slot (the first S waves): its row of the gradient and its weight's, the
+// dot product of the token's gradient with the row; then a wave for every 8 places:
+// zeros in those that pad a run.
+template <int VEC, typename YT, typename IO>
+__global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardProblem p) {
+  const int w = my_wave(), lane = threadIdx.x & 63, vecs = p.H / VEC, S = p.T * p.k;
+  if (w >= S) {
+    const long p0 = (long)(w - S) * 8;
+    const int n = (int)min((long)min(p.num_padded[0], p.R) - p0, 8L);
+    for (int i = 0; i < n; ++i) {
+      const int slot = __builtin_amdgcn_readfirstlane(p.sorted_ids[p0 + i]);
+      if ((unsigned)slot < (unsigned)S) continue;
+      const float zero[VEC] = {};
+      YT* to = (YT*)p.drows + (size_t)(p0 + i) * p.H;
+      for (int c = lane; c < vecs; c += 64) store_vec<YT, VEC>(to + c * VEC, zero);
+    }
+    return;
+  }
+  const int at = __builtin_amdgcn_readfirstlane(p.slot_rows[w]);
+  if ((unsigned)at >= (unsigned)p.R) {
+    if (lane == 0 && p.dweights) p.dweights[w] = 0.f;
+    return;
+  }
+  const float wt = p.topk_weights ? p.topk_weights[w] : 1.f;
+  const IO* g = (const IO*)p.dout + (size_t)(w / p.k) * p.H;
+  const YT* y = (const YT*)p.rows + (size_t)at * p.H;
+  YT* dy = (YT*)p.drows + (size_t)at * p.H;
+  float dot = 0.f;
+  for (int c = lane; c < vecs; c += 64) {
+    const Vec<IO, VEC> gv = load_vec<IO, VEC>(g + c * VEC);
+    float d[VEC];
+    if (p.dweights) {
+      const Vec<YT, VEC> yv = load_vec<YT, VEC>(y + c * VEC);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) dot += elem<IO, VEC>(gv, e) * elem<YT, VEC>(yv, e);
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d[e] = wt * elem<IO, VEC>(gv, e);
+    store_vec<YT, VEC>(dy + c * VEC, d);
+  }
+  dot = wave_sum(dot);
+  if (lane == 0 && p.dweights) p.dweights[w] = dot;
+}
+
+template <int VEC, typename YT, typename IO>
+static void run_combine(const CombineProblem& p, hipStream_t stream) {
+  const int pieces = (p.H / VEC + 63) / 64;
+  const dim3 grid = grid_of((long)p.T * pieces);
+  if (p.topk_weights)
+    combine_kernel<VEC, true><<<grid, 256, 0, stream>>>((const YT*)p.rows, p.slot_rows,
+                                                        p.topk_weights, p.T, p.H, p.k, p.R,
+                                                        pieces, (IO*)p.out);
+  else
+    combine_kernel<VEC, false><<<grid, 256, 0, stream>>>((const YT*)p.rows, p.slot_rows,
+                                                         p.topk_weights, p.T, p.H, p.k, p.R,
+                                                         pieces, (IO*)p.out);
+}
+
+template <int VEC, typename YT, typename IO>
+static void run_combine_backward(const CombineBackwardProblem& p, hipStream_t stream) {
+  const dim3 grid = grid_of((long)p.T * p.k + (p.R + 7) / 8);
+  combine_backward_kernel<VEC, YT, IO><<<grid, 256, 0, stream>>>(p);
+}
+
+// Calls f(VEC, rows' type, tokens' type) for the types of a call: 16 bytes of the wider
+// type to a lane where every row of both starts at a multiple of 16, else one element.
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+template <typename F>
+static void by_type(int rows_dtype, int dtype, int H, bool aligned, F f) {
+  const uint16_t b = 0;
+  const float s = 0;
+  const bool b2 = rows_dtype == MOE_DTYPE_BF16 && dtype == MOE_DTYPE_BF16;
+  const bool wide = aligned && H % 8 == 0;
+  if (b2)
+    wide ? f(Int<8>{}, b, b) : f(Int<1>{}, b, b);
+  else if (rows_dtype == MOE_DTYPE_BF16)
+    wide ? f(Int<8>{}, b, s) : f(Int<1>{}, b, s);
+  else if (dtype == MOE_DTYPE_BF16)
+    wide ? f(Int<8>{}, s, b) : f(Int<1>{}, s, b);
+  else
+    aligned && H % 4 == 0 ? f(Int<4>{}, s, s) : f(Int<1>{}, s, s);
+}
+
+static bool aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if ((uintptr_t)p % 16) return false;
+  return true;
+}
+
+}  // namespace dispatch
+
+hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
+  using namespace dispatch;
+  const int bytes = p.dtype == MOE_DTYPE_BF16 ? 2 : 4;
+  const Lists l{p.topk_ids, p.sorted_ids, p.num_padded, p.slot_rows, p.T * p.k, p.E, p.R};
+  const dim3 grid = grid_of((long)p.R + (l.S + 63) / 64);
+  auto run = [&](auto unit) {
+    typedef decltype(unit) U;
+    places_kernel<U><<<grid, 256, 0, stream>>>((const U*)p.x, l, p.H * bytes / (int)sizeof(U),
+                                               p.k, (U*)p.rows);
+  };
+  if ((size_t)p.H * bytes % 16 == 0 && aligned16({p.x, p.rows})) run(u32x4{});
+  else if (bytes == 4) run(uint32_t{});
+  else run(uint16_t{});
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineProblem& p, hipStream_t stream) {
+  using namespace dispatch;
+  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.rows, p.out}), [&](auto v, auto y, auto io) {
+    run_combine<decltype(v)::value, decltype(y), decltype(io)>(p, stream);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const CombineBackwardProblem& p, hipStream_t stream) {
+  using namespace dispatch;
+  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.dout, p.rows, p.drows}),
+          [&](auto v, auto y, auto io) {
+            run_combine_backward<decltype(v)::value, decltype(y), decltype(io)>(p, stream);
+          });
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -186,4 +186,85 @@ struct LoraProblem {
 size_t lora_workspace_bytes(int S, int n, int K, int r, int block_m);
 hipError_t launch_lora_add(const LoraProblem& p, hipStream_t stream);
 
+// Tokens in expert order and back (moe_dispatch.hip).
+struct DispatchProblem {
+  const void* x;
+  const int32_t* topk_ids;
+  const int32_t* sorted_ids;  // [R]
+  const int32_t* num_padded;
+  int T, E, H, k, R, dtype;
+  void* rows;          // [R, H]
+  int32_t* slot_rows;  // [T, k]
+};
+hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream);
+struct CombineProblem {
+  const void* rows;
+  int rows_dtype;
+  const int32_t* slot_rows;
+  const float* topk_weights;  // null: 1
+  int T, H, k, R, dtype;
+  void* out;
+};
+hipError_t launch_combine(const CombineProblem& p, hipStream_t stream);
+struct CombineBackwardProblem {
+  const void* dout;
+  int dtype;
+  const void* rows;  // may be null without dweights
+  int rows_dtype;
+  const int32_t* slot_rows;
+  const float* topk_weights;  // null: 1
+  const int32_t* sorted_ids;
+  const int32_t* num_padded;
+  int T, H, k, R;
+  void* drows;
+  float* dweights;  // may be null
+};
+hipError_t launch_combine_backward(const CombineBackwardProblem& p, hipStream_t stream);
+
+// Layer norm and its gradients (moe_layer_norm.hip).
+struct LayerNormProblem {
+  const void* x;
+  const void* residual;  // may be null
+  const float* weight;   // may be null: 1
+  const float* bias;     // may be null: 0
+  float alpha, eps;
+  int T, H, dtype;
+  void* residual_out;  // may be null
+  void* out;
+};
+hipError_t launch_layer_norm(const LayerNormProblem& p, hipStream_t stream);
+struct LayerNormBackwardProblem {
+  const void* dout;
+  const void* s;
+  const float* weight;         // may be null: 1
+  const void* dresidual_out;   // may be null
+  float alpha, eps;
+  int T, H, dtype;
+  void* dx;
+  void* dresidual;  // may be null
+  float* dweight;   // may be null
+  float* dbias;     // may be null
+  float* partial;   // workspace
+};
+size_t layer_norm_backward_workspace_bytes(int T, int H);
+hipError_t launch_layer_norm_backward(const LayerNormBackwardProblem& p, hipStream_t stream);
+
+// Matrix product with bias, activation and residual (moe_linear.hip).
+struct LinearProblem {
+  const void* x;
+  size_t ldx;
+  const void* w;
+  const float* bias;  // may be null
+  int activation, gated;
+  const void* residual;  // may be null
+  size_t ldr;
+  int T, N, K, dtype, out_dtype;
+  void* workspace;
+  void* out;
+  size_t ldo;
+  bool by_four;  // four columns of out and residual from a multiple of four on are aligned
+};
+size_t linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
+hipError_t launch_linear(const LinearProblem& p, hipStream_t stream);
+
 }  // namespace moe
