@@ -716,7 +716,7 @@ MOE_EXPORT moe_status moe_layer_norm_backward(const void* dout, const void* s,
 static moe_status check_linear(int T, int N, int K, int dtype) {
   if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
   if (T < 0 || (long)T >= kMaxSlots || N < 1 || N >= kMaxLength) return MOE_ERR_SHAPE;
-  if (K < 8 || K % 8 != 0 || K >= 1 << 22) return MOE_ERR_SHAPE;
+  if (K < 8 || K % 8 != 0 || K >= 1 << 21) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -735,7 +735,7 @@ MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const
   moe_status s = check_linear(T, N, K, dtype);
   if (s != MOE_OK) return s;
   const size_t b = elem_bytes(dtype), ob = elem_bytes(out_dtype);
-  if (ldx < (size_t)K || ldx >= 1 << 22 || ldx % (16 / b) != 0) return MOE_ERR_SHAPE;
+  if (ldx < (size_t)K || ldx >= 1 << 21 || ldx % (16 / b) != 0) return MOE_ERR_SHAPE;
   if (ldo < (size_t)N || ldo > INT_MAX || (residual && (ldr < (size_t)N || ldr > INT_MAX)))
     return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;

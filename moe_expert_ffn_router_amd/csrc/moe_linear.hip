@@ -4,8 +4,8 @@
 // (The fp32 matrix instructions run at a sixteenth of the bf16 rate, and are no closer: both
 // round as a chain of K additions does, 17 to 18 u rms at K = 4096.)
 //
-// Tile kernel: a workgroup of 8 waves (2 along the w rows, 4 along the x rows) makes
-// 32 NI w rows x 64 MI x rows, wave by wave 16 NI x 16 MI. 128 bytes of every row (a
+// Tile kernel: a workgroup of 2 waves along the w rows and WM along the x rows makes
+// 32 NI w rows x 16 WM MI x rows, wave by wave 16 NI x 16 MI. 128 bytes of every row (a
 // chunk: 64 bf16, 32 fp32) are a stage of a ring in LDS that direct-to-LDS loads fill
 // ahead of the chunk in work, one barrier a chunk. Past the operands' ends (rows, and
 // the last chunk's columns past K) a load's offset lies outside its buffer and gives
@@ -22,19 +22,23 @@ namespace linear {
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 constexpr int kRsrcWord3 = 0x00020000;     // raw buffer, 32-bit data format
-// Offsets of a tile's rows stay below kBufferBytes (255 rows of less than 2^24 bytes); one
-// past it, kOOB, gives zeros and reads no memory.
-constexpr uint32_t kBufferBytes = 0xFF800000u, kOOB = 0xFFFF0000u;
-constexpr int kRowBytes = 128;             // of a row in a stage
-constexpr int kWaves = 8, kWavesN = 2, kWavesM = 4;
+// A tile's rows lie within 2^31 bytes (256 rows of less than 2^23); a lane whose offset
+// starts at kOOB is past them whatever row of the tile is added: zeros, no memory read.
+constexpr uint32_t kOOB = 0x80000000u;
 constexpr int kLds = 160 * 1024;
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const uint8_t* uni_ptr(const uint8_t* v) {
+  const uint64_t a = (uint64_t)v;
+  return (const uint8_t*)(((uint64_t)(uint32_t)uni((int)(a >> 32)) << 32) |
+                          (uint32_t)uni((int)(uint32_t)a));
+}
 
-template <int VM>
+// Waits until at most VM vector loads of this wave are in flight (and, LGKM = 0, no LDS read).
+template <int VM, int LGKM = 15>
 __device__ __forceinline__ void wait_loads() {
   static_assert(VM >= 0 && VM < 64, "vmcnt");
-  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (0x7 << 4) | (15 << 8));
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (0x7 << 4) | (LGKM << 8));
 }
 __device__ __forceinline__ void ring_barrier() {
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -44,60 +48,147 @@ __device__ __forceinline__ void ring_barrier() {
 
 // ---------------------------------------------------------- epilogue ---
 
-__device__ __forceinline__ float activate(int act, float v) {
-  switch (act) {
-    case MOE_ACT_RELU: return v < 0.f ? 0.f : v;  // a NaN stays
-    case MOE_ACT_SILU: return v / (1.0f + expf(-v));
-    case MOE_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case MOE_ACT_GELU_TANH: {
-      // (1 + tanh z) / 2 = 1 / (1 + exp(-2 z))
-      const float z = v * (0.79788456080286536f + 0.035677408136300125f * v * v);
-      return v / (1.0f + expf(-2.0f * z));
-    }
-    default: return v;
-  }
+// With the hardware's exp2 and reciprocal, an ulp each; the product in exp2's argument is
+// off by |v| u, which counts for nothing where v is large: v exp(-|v|) is small there.
+__device__ __forceinline__ float exp_of(float v) {
+  return __builtin_amdgcn_exp2f(v * 1.44269504088896341f);
+}
+__device__ __forceinline__ float logistic(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_of(-v));
+}
+// v times the normal distribution at v. Its upper tail by Abramowitz and Stegun's 7.1.26,
+// erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2) with t = 1 / (1 + 0.3275911 x), x >= 0, off by
+// 1.5e-7 at most (2.5 u, half of that in the result): a tenth of the library function's code.
+__device__ __forceinline__ float gelu(float v) {
+  const float x = fabsf(v) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
+  const float p =
+      t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f +
+                                                    t * (-1.453152027f + t * 1.061405429f))));
+  const float tail = 0.5f * p * exp_of(-x * x);
+  return v * (v < 0.f ? tail : 1.0f - tail);
+}
+// The activation of all of a lane's values in one branch, not one a value: what is executed
+// of the epilogue is straight code of a few lines (jumps from value to value, each to a line
+// that the instruction cache does not hold yet, took 14 us of every workgroup).
+template <int N>
+__device__ __forceinline__ void activate(int act, f32x4 (&v)[N]) {
+  auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[i][q] = f(v[i][q]);
+  };
+  if (act == MOE_ACT_NONE) return;
+  if (act == MOE_ACT_RELU)
+    each([](float x) { return x < 0.f ? 0.f : x; });  // a NaN stays
+  else if (act == MOE_ACT_SILU)
+    each([](float x) { return x * logistic(x); });
+  else if (act == MOE_ACT_GELU)
+    each([](float x) { return gelu(x); });
+  else  // (1 + tanh z) / 2 is the logistic function of 2 z
+    each([](float x) {
+      return x * logistic(x * (1.5957691216057307f + 0.071354816272600251f * x * x));
+    });
 }
 
-__device__ __forceinline__ float load_one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ void store_one(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, v); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
-__device__ __forceinline__ f32x4 load_four(const uint16_t* p) {
-  const u32x2 r = *(const u32x2*)p;
+// Four consecutive values of out or residual as they are in memory.
+template <typename OT>
+struct Four {
+  typedef u32x2 type;
+};
+template <>
+struct Four<float> {
+  typedef f32x4 type;
+};
+__device__ __forceinline__ f32x4 value(const u32x2& r) {
   return f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
                __uint_as_float(r[1] << 16), __uint_as_float(r[1] & 0xffff0000u)};
 }
-__device__ __forceinline__ f32x4 load_four(const float* p) { return *(const f32x4*)p; }
+__device__ __forceinline__ f32x4 value(const f32x4& r) { return r; }
 __device__ __forceinline__ void store_four(uint16_t* p, f32x4 v) {
   *(u32x2*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 __device__ __forceinline__ void store_four(float* p, f32x4 v) { *(f32x4*)p = v; }
+__device__ __forceinline__ float load_one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+__device__ __forceinline__ float load_one(const float* p) { return *p; }
+__device__ __forceinline__ void store_one(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, v); }
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 
-// Four columns n .. n + 3 of row m from their sums (and, gated, those of the up rows).
+// Four columns n .. n + 3 < N of some rows: their biases once, then row by row.
 template <bool GATED, typename OT>
-__device__ __forceinline__ void finish(const LinearProblem& p, int m, int n, f32x4 v, f32x4 up) {
-  if (m >= p.T || n >= p.N) return;
-  OT* out = (OT*)p.out + (size_t)m * p.ldo + n;
-  const OT* res = p.residual ? (const OT*)p.residual + (size_t)m * p.ldr + n : nullptr;
+struct Columns {
+  int n;
+  f32x4 bias, up_bias;
+
+  __device__ __forceinline__ Columns(const LinearProblem& p, int n) : n(n), bias{}, up_bias{} {
+    if (!p.bias || n >= p.N) return;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int c = min(n + q, p.N - 1);
-    if (p.bias) {
-      v[q] += p.bias[c];
-      if (GATED) up[q] += p.bias[p.N + c];
+    for (int q = 0; q < 4; ++q) {
+      const int c = min(n + q, p.N - 1);
+      bias[q] = p.bias[c];
+      if (GATED) up_bias[q] = p.bias[p.N + c];
     }
-    v[q] = activate(p.activation, v[q]);
-    if (GATED) v[q] *= up[q];
   }
-  if (p.by_four) {
-    if (res) v += load_four(res);
-    store_four(out, v);
-  } else {
+  // The sums of a part of K as they are: [part, T, columns of w rounded up to fours] fp32.
+  template <int R, typename F>
+  __device__ __forceinline__ void store_sums(const LinearProblem& p, F m, const f32x4 (&v)[R],
+                                             const f32x4 (&up)[R]) const {
+    const size_t fours = (p.N + 3) / 4 * (GATED ? 2 : 1);
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (n + q < p.N) store_one(out + q, res ? load_one(res + q) + v[q] : v[q]);
+    for (int i = 0; i < R; ++i) {
+      if (m(i) >= p.T || n >= p.N) continue;
+      f32x4* to = (f32x4*)p.workspace + ((size_t)blockIdx.y * p.T + m(i)) * fours + n / 4;
+      *to = v[i];
+      if (GATED) to[fours / 2] = up[i];
+    }
   }
-}
+  // What residual holds of rows m(i), ahead of their sums: loads that nothing waits for yet
+  // (those past the ends from inside, never used). Only where p.by_four.
+  template <int R, typename F>
+  __device__ __forceinline__ void fetch(const LinearProblem& p, F m,
+                                        typename Four<OT>::type (&raw)[R]) const {
+    if (!p.residual || !p.by_four) return;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      raw[i] = *(const typename Four<OT>::type*)((const OT*)p.residual +
+                                                 (size_t)min(m(i), p.T - 1) * p.ldr +
+                                                 min(n, p.N - 4));
+  }
+  // Rows m(i) of them from their sums (and, gated, those of the up rows) and what fetch has
+  // brought. m(i) >= T: none.
+  template <int R, typename F>
+  __device__ __forceinline__ void store(const LinearProblem& p, F m, f32x4 (&v)[R],
+                                        const f32x4 (&up)[R],
+                                        const typename Four<OT>::type (&raw)[R]) const {
+#pragma unroll
+    for (int i = 0; i < R; ++i) v[i] += bias;
+    activate(p.activation, v);
+    if (GATED) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) v[i] *= up[i] + up_bias;
+    }
+    if (p.by_four) {
+      if (p.residual) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) v[i] += value(raw[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (m(i) < p.T && n < p.N) store_four((OT*)p.out + (size_t)m(i) * p.ldo + n, v[i]);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (m(i) >= p.T) continue;
+      OT* out = (OT*)p.out + (size_t)m(i) * p.ldo + n;
+      const OT* res = (const OT*)p.residual + (size_t)m(i) * p.ldr + n;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (n + q < p.N) store_one(out + q, p.residual ? load_one(res + q) + v[i][q] : v[i][q]);
+    }
+  }
+};
 
 // -------------------------------------------------------------- tiles ---
 
@@ -108,7 +199,7 @@ struct Frag {
   static constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
   bf16x8 plane[kPlanes];
 
-  // step: which 32 of the chunk's k; row, key: the row in LDS and its columns' key
+  // step: which 32 of the stage's k; row, key: the row in LDS and its columns' key
   __device__ __forceinline__ void read(const uint8_t* row, int key, int step) {
     const int g = (threadIdx.x >> 4) & 3;
     if constexpr (sizeof(T) == 2) {
@@ -131,84 +222,130 @@ __device__ __forceinline__ void multiply(f32x4& acc, const Frag<T>& w, const Fra
       if (a + b <= 2) acc = mfma_bf16(w.plane[a], x.plane[b], acc);
 }
 
-// Rows of a wave's NI w tiles in LDS. Gated: tile after tile, gate rows in the even ones
-// and their up rows in the odd. Else row r of tile i of a pair lies at (r / 4) 8 + 4 (i
-// odd) + r % 4 of the pair's 32, so that a lane's eight sums of a pair are those of eight
-// consecutive rows (16 bytes of bf16); a last tile without a partner keeps its order.
-template <int NI, bool GATED>
-__device__ __forceinline__ int w_row(int i, int r) {
-  if (GATED || (NI % 2 && i == NI - 1)) return i * 16 + r;
-  return (i >> 1) * 32 + (r >> 2) * 8 + (i & 1) * 4 + (r & 3);
+// A product added in place, where it stands: the reads and loads of the loop are placed
+// among the products by hand. (As a builtin the compiler moved them together, and gave sums
+// new registers, 184 copies a step with 256 of them to a wave: 1249 TFLOP/s for 8192^3
+// instead of 1331.) It knows nothing of the matrix instruction in here: what writes the sums
+// before the first and reads them after the last goes through settle().
+__device__ __forceinline__ void mfma_in_place(f32x4& acc, const bf16x8& a, const bf16x8& b) {
+  asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
-// Column (16 bytes) c of a row lies at column c ^ key in LDS, so that eight lanes of a
-// read, one column of eight rows, meet eight columns.
-template <int NI, bool GATED>
-__device__ __forceinline__ int w_key(int row) {
-  if (GATED) return row & 7;
-  const int r = row % (16 * NI);
-  if (NI % 2 && r >= 16 * (NI - 1)) return r & 7;
-  return (r & 3) | ((r >> 1) & 4);
+// Orders everything else that touches the sums before or after the products, by more than
+// the 16 wait states that a product's registers may need.
+template <int I, int NI, int MI>
+__device__ __forceinline__ void settle(f32x4 (&acc)[NI][MI]) {
+  if constexpr (I == 0) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+  if constexpr (I < NI) {
+#pragma unroll
+    for (int j = 0; j < MI; ++j) asm volatile("" : "+a"(acc[I][j]));
+    settle<I + 1>(acc);
+  }
 }
 
-template <int MI, int NI>
+// Row in LDS of row r of w tile i of the waves wn. Gated: tile after tile, gate rows in the
+// even ones and their up rows in the odd. Else row r of tile i of a pair lies at (r / 4) 8 +
+// 4 (i odd) + r % 4 of the pair's 32, so that a lane's eight sums of a pair are those of
+// eight consecutive rows.
+template <int NI, bool GATED>
+__device__ __forceinline__ int w_row(int wn, int i, int r) {
+  if (GATED) return (wn * NI + i) * 16 + r;
+  return (wn * (NI / 2) + (i >> 1)) * 32 + (r >> 2) * 8 + (i & 1) * 4 + (r & 3);
+}
+// Column (16 bytes) c of a row lies at column c ^ key in LDS, so that eight lanes of a read,
+// one column of eight rows (of x, and gated of w, in a row; else two times four, eight
+// apart), meet the eight columns of 128 bytes: one row, or two of 64.
+template <int B, bool PAIRS>
+__device__ __forceinline__ int key_of(int row) {
+  const int r = PAIRS ? (row & 3) | ((row >> 1) & 4) : row & 7;
+  return B == 128 ? r : r >> 1;
+}
+
+// A workgroup of 2 x WM waves, each 16 NI w rows x 16 MI x rows; B bytes of every row are a
+// stage.
+template <int MI, int NI, int WM, int B>
 struct Shape {
-  static constexpr int kRowsW = 16 * NI * kWavesN, kRowsX = 16 * MI * kWavesM;
-  // loads (8 rows) of a wave and stage; the same for every wave, so that what is in
-  // flight is known: loads past the last row fill the stage's padding with zeros
-  static constexpr int kLoads = (kRowsW + kRowsX + 8 * kWaves - 1) / (8 * kWaves);
-  static constexpr int kStage = kLoads * kWaves * 1024;
-  static constexpr int kStages = kLds / kStage < 4 ? kLds / kStage : 4;
+  static constexpr int kWaves = 2 * WM;
+  static constexpr int kRowsW = 32 * NI, kRowsX = 16 * MI * WM;
+  // a load takes kPer rows; the waves' loads take kStep, and every wave has the same number
+  // of them, so that what is in flight is known
+  static constexpr int kPer = 1024 / B, kStep = kPer * kWaves;
+  static constexpr int kLoadsW = kRowsW / kStep, kLoadsX = kRowsX / kStep;
+  static constexpr int kLoads = kLoadsW + kLoadsX;
+  static_assert(NI % 2 == 0 && kRowsW % kStep == 0 && kRowsX % kStep == 0, "whole loads");
+  static constexpr int kStage = (kRowsW + kRowsX) * B;
+  static constexpr int kStages = kLds / kStage < 5 ? kLds / kStage : 5;
 };
 
-template <int MI, int NI, bool GATED, typename T, typename OT>
-__global__ __launch_bounds__(kWaves * 64, 2) void tile_kernel(LinearProblem p, int n_tiles) {
-  typedef Shape<MI, NI> S;
-  static_assert(!GATED || NI % 2 == 0, "pairs of tiles");
+// Workgroups go round the 8 XCDs: the b-th gets a tile of its XCD's share, a run of
+// consecutive tiles (shares differ by one at most).
+__device__ __forceinline__ int xcd_order(int b, int tiles) {
+  const int per = tiles >> 3, rest = tiles & 7, q = b & 7;
+  return q * per + min(q, rest) + (b >> 3);
+}
+// Tiles run down panels of kPanel columns, row by row: consecutive tiles share the rows
+// of w and x that an XCD's L2 then holds.
+constexpr int kPanel = 8;
+__device__ __forceinline__ void panel(int t, int m_tiles, int n_tiles, int& m, int& n) {
+  const int q = t / (kPanel * m_tiles), in = t - q * kPanel * m_tiles;
+  const int wide = min(kPanel, n_tiles - q * kPanel);
+  m = in / wide;
+  n = q * kPanel + in - m * wide;
+}
+
+template <int MI, int NI, int WM, int B, bool GATED, typename T, typename OT>
+__global__ __launch_bounds__(2 * WM * 64, WM / 2) void tile_kernel(LinearProblem p,
+                                                                         int n_tiles) {
+  typedef Shape<MI, NI, WM, B> S;
+  constexpr int kWaves = S::kWaves;
   __shared__ __attribute__((aligned(16))) uint8_t lds[S::kStages * S::kStage];
   const int wave = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wn = wave & 1, wm = wave >> 1;
-  const int tile_m = blockIdx.x / n_tiles, tile_n = blockIdx.x - tile_m * n_tiles;
+  const int tile = xcd_order(blockIdx.x, gridDim.x);
+  int tile_m, tile_n;
+  panel(tile, gridDim.x / n_tiles, n_tiles, tile_m, tile_n);
   constexpr int kCols = GATED ? S::kRowsW / 2 : S::kRowsW;  // outputs of a row
   const int m0 = tile_m * S::kRowsX, n0 = tile_n * kCols;
 
-  // this wave's loads, 8 rows each, the w rows first: lane l the 16 bytes that belong at
-  // column l % 8 of row l / 8
-  const size_t wstep = (size_t)p.K * sizeof(T), xstep = p.ldx * sizeof(T);
-  const uint8_t* wbase = (const uint8_t*)p.w + n0 * wstep;
-  const uint8_t* ubase = wbase + p.N * wstep;  // gated: the up rows
-  const uint8_t* xbase = (const uint8_t*)p.x + m0 * xstep;
-  uint32_t off[S::kLoads];
-  int col[S::kLoads];
-#pragma unroll
-  for (int i = 0; i < S::kLoads; ++i) {
-    const int row = (i * kWaves + wave) * 8 + (lane >> 3);
-    int key = row & 7;
-    off[i] = kOOB;
-    if (row < S::kRowsW) {
-      key = w_key<NI, GATED>(row);
-      const int n = GATED ? (row >> 5) * 16 + (row & 15) : row;
-      if (n0 + n < p.N) off[i] = (uint32_t)n * (uint32_t)wstep;
-    } else if (row < S::kRowsW + S::kRowsX) {
-      const int m = row - S::kRowsW;
-      if (m0 + m < p.T) off[i] = (uint32_t)m * (uint32_t)xstep;
-    }
-    col[i] = ((lane & 7) ^ key) * 16;
-    if (off[i] != kOOB) off[i] += col[i];
-  }
-  const int bytes = p.K * (int)sizeof(T);
-  const int chunks = (bytes + kRowBytes - 1) / kRowBytes;
-  auto issue = [&](int c, int slot) {
-    const int left = bytes - c * kRowBytes;  // bytes of K from this chunk on
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) {
-      const int first = (i * kWaves + wave) * 8;
-      const uint8_t* base = first >= S::kRowsW ? xbase : GATED && (first & 16) ? ubase : wbase;
-      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + (size_t)c * kRowBytes), (short)0, (int)kBufferBytes, kRsrcWord3);
-      const uint32_t o = left >= kRowBytes || col[i] < left ? off[i] : kOOB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, (lds_ptr_t)(lds + slot * S::kStage + first * kRowBytes), 16, (int)o, 0, 0, 0);
-    }
+  // This wave's loads, kPer rows each: every lane 16 bytes, which the rows' order in memory
+  // and the key of their place in LDS decide, from the rows of the tile that are there (a
+  // buffer of that size). Few registers for them: the sums and two steps' operands take
+  // nearly all of a wave's 512.
+  constexpr int kLanes = B / 16;  // of a row
+  const uint32_t wstep = (uint32_t)p.K * sizeof(T), xstep = (uint32_t)p.ldx * sizeof(T);
+  const int row = wave * S::kPer + lane / kLanes;  // of the first load of w and of x
+  // gated: 16 gate rows, 16 up rows, ...: of which the later loads' are a multiple of 32 on
+  static_assert(!GATED || S::kStep % 32 == 0, "gate and up rows");
+  const bool up = GATED && ((wave * S::kPer) & 16);
+  const uint8_t* wbase = uni_ptr((const uint8_t*)p.w + (size_t)(n0 + (up ? p.N : 0)) * wstep);
+  const uint8_t* xbase = uni_ptr((const uint8_t*)p.x + (size_t)m0 * xstep);
+  const uint32_t wsize = uni((min(kCols, p.N - n0) - 1) * wstep + B);
+  const uint32_t xsize = uni((min(S::kRowsX, p.T - m0) - 1) * xstep + B);
+  const int wcol = ((lane % kLanes) ^ key_of<B, !GATED>(row)) * 16;
+  const int xcol = ((lane % kLanes) ^ key_of<B, false>(row)) * 16;
+  const uint32_t woff = (GATED ? (row >> 5) * 16 + (row & 15) : row) * wstep + wcol;
+  const uint32_t xoff = row * xstep + xcol;
+  const uint32_t wnext = (GATED ? S::kStep / 2 : S::kStep) * wstep, xnext = S::kStep * xstep;
+  // this workgroup's part of K (blockIdx.y of gridDim.y)
+  const int all = (p.K * (int)sizeof(T) + B - 1) / B;
+  const int first = (int)((long)all * blockIdx.y / gridDim.y);
+  const int stages = (int)((long)all * (blockIdx.y + 1) / gridDim.y) - first;
+  const int bytes = min(p.K * (int)sizeof(T) - first * B, stages * B);
+  wbase += (size_t)first * B;
+  xbase += (size_t)first * B;
+  // the i-th load of stage c; past the last stage all zeros
+  auto issue = [&](int i, int c, int slot) __attribute__((always_inline)) {
+    const int left = bytes - c * B;  // bytes of K from this stage on
+    const bool is_w = i < S::kLoadsW;
+    const int q = is_w ? i : i - S::kLoadsW;
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)((is_w ? wbase : xbase) + (size_t)c * B), (short)0, (int)(is_w ? wsize : xsize),
+        kRsrcWord3);
+    const uint32_t o = (is_w ? wcol : xcol) < left ? (is_w ? woff : xoff) : kOOB;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rs,
+        (lds_ptr_t)(lds + slot * S::kStage +
+                    ((is_w ? 0 : S::kRowsW) + q * S::kStep + wave * S::kPer) * B),
+        16, (int)(o + q * (is_w ? wnext : xnext)), 0, 0, 0);
   };
 
   f32x4 acc[NI][MI];
@@ -216,71 +353,327 @@ __global__ __launch_bounds__(kWaves * 64, 2) void tile_kernel(LinearProblem p, i
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  int fill = 0, slot = 0;  // slots of the next chunk to load and of the one in work
-  for (; fill < S::kStages - 1; ++fill) issue(fill, fill);
-  for (int c = 0; c < chunks; ++c) {
-    // this wave's loads of chunk c have landed, then all waves': and all have read what
-    // lay in the slot that the next loads fill
-    wait_loads<(S::kStages - 2) * S::kLoads>();
-    ring_barrier();
-    issue(c + S::kStages - 1, fill);
-    fill = fill == S::kStages - 1 ? 0 : fill + 1;
-    const uint8_t* w = lds + slot * S::kStage + wn * 16 * NI * kRowBytes;
-    const uint8_t* x = lds + slot * S::kStage + (S::kRowsW + wm * 16 * MI) * kRowBytes;
-    slot = slot == S::kStages - 1 ? 0 : slot + 1;
+  const int r = lane & 15;
+  // operand q of a step: the x tiles', then the w tiles'
+  auto read = [&](Frag<T>(&wf)[NI], Frag<T>(&xf)[MI], int q, int slot, int step)
+      __attribute__((always_inline)) {
+    const uint8_t* at = lds + slot * S::kStage;
+    if (q < MI) {
+      xf[q].read(at + (S::kRowsW + (wm * MI + q) * 16 + r) * B, key_of<B, false>(r), step);
+    } else {
+      const int row = w_row<NI, GATED>(wn, q - MI, r);
+      wf[q - MI].read(at + row * B, key_of<B, !GATED>(row), step);
+    }
+  };
 #pragma unroll
-    for (int step = 0; step < (sizeof(T) == 2 ? 2 : 1); ++step) {
-      Frag<T> wf[NI], xf[MI];
-      const int r = lane & 15;
+  for (int c = 0; c < S::kStages; ++c)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int row = w_row<NI, GATED>(i, r);
-        wf[i].read(w + row * kRowBytes, w_key<NI, GATED>(row), step);
+    for (int i = 0; i < S::kLoads; ++i) issue(i, c, c);
+  int slot = 0;
+  if constexpr (sizeof(T) == 2) {
+    constexpr int kSteps = B / 64;  // of a stage
+    Frag<T> w0[NI], x0[MI], w1[NI], x1[MI];
+    // A step's products, with the reads of the next one's operands among the first of them
+    // and, in a stage's last step, the loads that fill its slot again. The stage's own
+    // operands are all read by then, and the next stage's loads have landed: in this wave
+    // where it waits, in all past the barrier.
+    auto step = [&](const Frag<T>(&wa)[NI], const Frag<T>(&xa)[MI], Frag<T>(&wb)[NI],
+                    Frag<T>(&xb)[MI], int h, int c) __attribute__((always_inline)) {
+      const bool last = h == kSteps - 1;
+      const int here = slot;
+      if (last) {
+        wait_loads<(S::kStages - 2) * S::kLoads, 0>();
+        ring_barrier();
+        slot = slot == S::kStages - 1 ? 0 : slot + 1;
       }
+      constexpr int kReads = NI + MI, kMma = NI * MI;
+      constexpr int kPer = kMma >= 2 * kReads ? 2 : 1;
+      constexpr int kGap = kMma >= 2 * S::kLoads ? 2 : 1;
 #pragma unroll
-      for (int j = 0; j < MI; ++j) xf[j].read(x + (j * 16 + r) * kRowBytes, r & 7, step);
+      for (int n = 0; n < kMma || n / kPer < kReads || n / kGap < S::kLoads; ++n) {
+        if (n < kMma) mfma_in_place(acc[n / MI][n % MI], wa[n / MI].plane[0], xa[n % MI].plane[0]);
+        if (n % kPer == 0 && n / kPer < kReads)
+          read(wb, xb, n / kPer, slot, last ? 0 : h + 1);
+        if (last && n % kGap == kGap - 1 && n / kGap < S::kLoads)
+          issue(n / kGap, c + S::kStages, here);
+      }
+    };
+    wait_loads<(S::kStages - 1) * S::kLoads>();
+    ring_barrier();
+#pragma unroll
+    for (int q = 0; q < NI + MI; ++q) read(w0, x0, q, 0, 0);
+    settle<0>(acc);
+    for (int c = 0; c < stages; c += 3 - kSteps) {  // (a stage more than there are: zeros)
+      step(w0, x0, w1, x1, 0, c);
+      step(w1, x1, w0, x0, kSteps - 1, kSteps == 2 ? c : c + 1);
+    }
+    settle<0>(acc);
+  } else {
+    for (int c = 0; c < stages; ++c) {
+      wait_loads<(S::kStages - 1) * S::kLoads>();
+      ring_barrier();
+      Frag<T> wf[NI], xf[MI];
+#pragma unroll
+      for (int q = 0; q < NI + MI; ++q) read(wf, xf, q, slot, 0);
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < MI; ++j) multiply<T>(acc[i][j], wf[i], xf[j]);
+      wait_loads<63, 0>();
+      ring_barrier();  // all waves have read the slot
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) issue(i, c + S::kStages, slot);
+      slot = slot == S::kStages - 1 ? 0 : slot + 1;
     }
   }
-  wait_loads<0>();  // no load may still write this workgroup's LDS at its end
-  const int g = lane >> 4;
+  // A wave's sums, as many of its 16-row tiles at a time as its piece of LDS holds, and back
+  // along rows: whole lines of out and residual, and one copy of the epilogue's code.
+  constexpr int kCell = 16 * NI * 4 + 16;  // bytes of a row, a column of banks apart
+  constexpr int kAt = S::kStages * S::kStage / kWaves / (16 * kCell);
+  constexpr int kGroup = kAt < MI ? kAt : MI;
+  constexpr int kFours = GATED ? 2 * NI : 4 * NI;  // of a row's outputs
+  constexpr int kRows = 64 / kFours;               // rows at a time, a lane to four columns
+  constexpr int kTurns = (kGroup * 16 + kRows - 1) / kRows;
+  static_assert(kGroup >= 1 && MI % kGroup == 0, "LDS of a wave");
+  uint8_t* mine = lds + wave * kGroup * 16 * kCell;
+  const int row0 = lane / kFours, q = lane - row0 * kFours;
+  const Columns<GATED, OT> cols(p,
+                                row0 < kRows ? n0 + wn * (GATED ? 8 : 16) * NI + q * 4 : p.N);
+  const uint8_t* cell = mine + (GATED ? (q >> 2) * 128 + (q & 3) * 16 : q * 16);
+  const int m1 = m0 + wm * MI * 16 + row0;
+  typename Four<OT>::type raw[2][kTurns];
+  auto at = [&](int j0, int a) __attribute__((always_inline)) {
+    return kGroup * 16 % kRows == 0 || row0 + a * kRows < kGroup * 16 ? m1 + j0 * 16 + a * kRows
+                                                                      : p.T;
+  };
+  const bool whole = gridDim.y == 1;
+  wait_loads<0, 0>();  // no load may still write the ring, which the sums go through now
+  if (whole) cols.fetch(p, [&](int a) { return at(0, a); }, raw[0]);
+  ring_barrier();
 #pragma unroll
-  for (int j = 0; j < MI; ++j) {
-    const int m = m0 + (wm * MI + j) * 16 + (lane & 15);
-    if constexpr (GATED) {
+  for (int j0 = 0; j0 < MI; j0 += kGroup) {
+    skinny::wave_lds_order();
 #pragma unroll
-      for (int i = 0; i < NI; i += 2)
-        finish<true, OT>(p, m, n0 + wn * 8 * NI + i * 8 + g * 4, acc[i][j], acc[i + 1][j]);
-    } else {
+    for (int j = j0; j < j0 + kGroup; ++j)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        finish<false, OT>(p, m, n0 + wn * 16 * NI + w_row<NI, GATED>(i, g * 4), acc[i][j],
-                          f32x4{});
+        *(f32x4*)(mine + ((j - j0) * 16 + r) * kCell +
+                  w_row<NI, GATED>(0, i, (lane >> 4) * 4) * 4) = acc[i][j];
+    if (whole && j0 + kGroup < MI)
+      cols.fetch(p, [&](int a) { return at(j0 + kGroup, a); }, raw[(j0 / kGroup + 1) & 1]);
+    skinny::wave_lds_order();
+    f32x4 v[kTurns], up[kTurns];
+#pragma unroll
+    for (int a = 0; a < kTurns; ++a) {
+      const uint8_t* from = cell + min(row0 + a * kRows, kGroup * 16 - 1) * kCell;
+      v[a] = *(const f32x4*)from;
+      up[a] = GATED ? *(const f32x4*)(from + 64) : f32x4{};
     }
+    if (whole)
+      cols.store(p, [&](int a) { return at(j0, a); }, v, up, raw[(j0 / kGroup) & 1]);
+    else
+      cols.store_sums(p, [&](int a) { return at(j0, a); }, v, up);
   }
 }
 
-template <int MI, int NI, bool GATED, typename T, typename OT>
-static void run_tiles(const LinearProblem& p, hipStream_t stream) {
-  typedef Shape<MI, NI> S;
+// The parts' sums added in order, and the epilogue: a thread for four columns of a row.
+template <bool GATED, typename OT>
+__global__ __launch_bounds__(256) void join_kernel(LinearProblem p, int parts) {
+  const int fours = (p.N + 3) / 4;
+  const long u = (long)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(u / fours), q = (int)(u - (long)m * fours);
+  if (m >= p.T) return;
+  const size_t step = (size_t)p.T * fours * (GATED ? 2 : 1);
+  const f32x4* from = (const f32x4*)p.workspace + (size_t)m * fours * (GATED ? 2 : 1) + q;
+  const Columns<GATED, OT> cols(p, q * 4);
+  typename Four<OT>::type raw[1];
+  cols.fetch(p, [&](int) { return m; }, raw);
+  f32x4 v[1] = {}, up[1] = {};
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    v[0] += from[i * step];
+    if (GATED) up[0] += from[i * step + fours];
+  }
+  cols.store(p, [&](int) { return m; }, v, up, raw);
+}
+
+// -------------------------------------------------------------- few rows ---
+
+// Up to R MT rows of x: K over the waves of a workgroup (moe_skinny.h), R NT rows of w each:
+// gated half of them gate rows, half their up rows. No second launch, no padding to a tile.
+template <int MT, int NT, int R, int NW, int D, bool GATED, typename T, typename OT>
+__global__ __launch_bounds__(NW * 64) void few_kernel(LinearProblem p) {
+  constexpr int kSums = R * MT * R * NT * 4;
+  constexpr int kPieces = skinny::lds_bytes<MT, NT, R, NW, T, T>();
+  __shared__ __attribute__((aligned(16))) char lds[kPieces + kSums];
+  constexpr int kCols = R * NT / (GATED ? 2 : 1);
+  const int n0 = blockIdx.x * kCols;
+  const int wave = uni(threadIdx.x >> 6);
+  skinny::Product<MT, NT, R, T, T> product;
+  product.lds = lds + wave * product.kLdsBytes;
+  product.x.set([&](int i) { return (const T*)p.x + (size_t)min(i, p.T - 1) * p.ldx; });
+  product.w.set([&](int i) {
+    const int n = min(n0 + (GATED ? i % kCols : i), p.N - 1);
+    return (const T*)p.w + (size_t)(n + (GATED && i >= kCols ? p.N : 0)) * p.K;
+  });
+  product.clear();
+  product.template accumulate<D>(p.K, wave, (p.K + skinny::kChunk - 1) / skinny::kChunk, NW);
+  float* sums = (float*)(lds + kPieces);  // [x row][w row]
+  skinny::reduce_waves<MT, NT, R, NW>(product.acc, lds, [&](int wr, int xr, auto s) {
+    if constexpr (sizeof(s) == 4) sums[xr * R * NT + wr] = s;
+    else *(f32x4*)(sums + xr * R * NT + wr) = s;
+  });
+  __syncthreads();
+  for (int u = threadIdx.x; u < R * MT * kCols / 4; u += NW * 64) {
+    const int m = u / (kCols / 4), q = u - m * (kCols / 4);
+    const float* at = sums + m * R * NT + q * 4;
+    f32x4 v[1] = {*(const f32x4*)at}, up[1] = {GATED ? *(const f32x4*)(at + kCols) : f32x4{}};
+    const Columns<GATED, OT> cols(p, n0 + q * 4);
+    typename Four<OT>::type raw[1];
+    cols.fetch(p, [&](int) { return m; }, raw);
+    cols.store(p, [&](int) { return m; }, v, up, raw);
+  }
+}
+
+// ------------------------------------------------------------------ plan ---
+
+template <int MI, int NI, int WM, int B, bool GATED, typename T, typename OT>
+static void run_tiles(const LinearProblem& p, int parts, hipStream_t stream) {
+  typedef Shape<MI, NI, WM, B> S;
   const int mt = (p.T + S::kRowsX - 1) / S::kRowsX;
   const int cols = GATED ? S::kRowsW / 2 : S::kRowsW;
   const int nt = (p.N + cols - 1) / cols;
-  tile_kernel<MI, NI, GATED, T, OT><<<mt * nt, kWaves * 64, 0, stream>>>(p, nt);
+  tile_kernel<MI, NI, WM, B, GATED, T, OT>
+      <<<dim3(mt * nt, parts), S::kWaves * 64, 0, stream>>>(p, nt);
+  if (parts > 1) {
+    const long fours = (long)p.T * ((p.N + 3) / 4);
+    join_kernel<GATED, OT><<<(unsigned)((fours + 255) / 256), 256, 0, stream>>>(p, parts);
+  }
+}
+
+template <int MT, int NT, int R, int NW, int D, bool GATED, typename T, typename OT>
+static void run_few(const LinearProblem& p, hipStream_t stream) {
+  const int cols = R * NT / (GATED ? 2 : 1);
+  few_kernel<MT, NT, R, NW, D, GATED, T, OT>
+      <<<(p.N + cols - 1) / cols, NW * 64, 0, stream>>>(p);
+}
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+// Which kernel a call runs: the few-rows kernel with mt x nt tiles of r rows, or the tile
+// kernel with mi x ni and K in `parts`.
+struct Plan {
+  bool few;
+  int a, b, r;  // few: mt, nt, r; tiles: mi, ni
+  int parts;
+};
+struct TileCost {
+  int mi, ni;
+  float fixed, alone, full;  // us: of a tile beside its stages; of a stage, one tile and all CUs
+};
+// The least of these estimates, in us. Tiles: measured with K 2048 and 4096 on 32 .. 256
+// tiles (alone and full), e.g. 512 x 4096 x 4096 1 x 4 23.9 (1 x 2 30.3, 2 x 4 27.3), 1024 rows
+// 2 x 4 35.5 (2 x 8 43.8, 1 x 4 46.8), 2048 rows 2 x 8 60.6 (4 x 8 76.1), 4096 rows 4 x 8 102.7
+// (2 x 8 117.7), 3000 x 1500 x 2000 2 x 6 28.9 (2 x 8 32.2, 2 x 4 43.0). Parts of K where
+// tiles are few: 64 x gated 2048 x 7168 in 4 15.8 (whole 27.0), 700 x 700 x 8192 in 2 21.5 (30.8);
+// the joining kernel takes 3.2 and its bytes. Few rows: w streams at 90 GB/s a CU and 7.5 TB/s
+// in all, x comes from L2 at 140: 16 x gated 2048 x 7168 11.5 (tiles 14.5), 16 x 4096 x 4096 7.7
+// (10.9), 64 x 512 x 512 3.3 (4.7), but 64 x 7168 x 2048 14.5 (10.0).
+static const TileCost kTiles[] = {{1, 2, 3.3f, 0.21f, 0.255f}, {1, 4, 3.8f, 0.24f, 0.31f},
+                                  {2, 4, 4.5f, 0.34f, 0.48f},  {2, 6, 5.0f, 0.46f, 0.68f},
+                                  {2, 8, 5.5f, 0.57f, 0.86f},  {4, 8, 8.0f, 1.05f, 1.5f}};
+static const TileCost kTilesF32[] = {{1, 2, 3.3f, 0.85f, 1.0f}, {2, 4, 4.5f, 1.4f, 1.75f},
+                                     {4, 4, 5.5f, 2.2f, 2.8f}};
+static const int kFew[][3] = {{1, 1, 8}, {1, 1, 16}, {1, 2, 16}, {2, 1, 16}, {2, 2, 16}, {4, 1, 16}};
+constexpr int kCus = 256;
+
+static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
+  const bool f32 = dtype == MOE_DTYPE_F32;
+  const int size = f32 ? 4 : 2, half = gated ? 2 : 1;
+  Plan best{};
+  float least = 3.0e38f;
+  auto take = [&](float t, const Plan& p) {
+    if (t < least) {
+      least = t;
+      best = p;
+    }
+  };
+  for (const auto& f : kFew) {
+    if (T > f[0] * f[2]) continue;
+    const int cols = f[1] * f[2] / half;
+    const long tiles = ((long)N + cols - 1) / cols;
+    const float w = 1e-3f * f[1] * f[2] * K * size, x = 1e-3f * f[0] * f[2] * K * size;  // KB
+    const float all = w * std::min<long>(tiles, kCus) / (f32 ? 6000.f : 7500.f);
+    take(2.5f + (float)((tiles + kCus - 1) / kCus) * (std::max(w / 90.f, all) + x / 140.f),
+         Plan{true, f[0], f[1], f[2], 1});
+  }
+  const int stages = (K * size + 127) / 128;
+  auto price = [&](const TileCost& c) {
+    const int rows = 64 * c.mi, cols = 32 * c.ni / half;
+    const long tiles = ((long)T + rows - 1) / rows * (((long)N + cols - 1) / cols);
+    for (int parts = 1; parts <= 16; parts += parts < 4 ? 1 : parts / 2) {
+      if (parts > 1 && 2 * parts > stages) break;
+      const long groups = tiles * parts, whole = groups / kCus;
+      const float part = (float)(groups - whole * kCus) / kCus, n = (stages + parts - 1) / parts;
+      float t = 2.5f + whole * (c.fixed - 2.5f + n * c.full);
+      if (part > 0) t += c.fixed - 2.5f + n * (c.alone + (c.full - c.alone) * part);
+      if (parts > 1) t += 3.2f + 2e-6f * parts * T * ((float)N * half);  // 8 bytes at 4 TB/s
+      take(t, Plan{false, c.mi, c.ni, 0, parts});
+      if (groups > 2 * kCus) break;  // more parts: more rounds
+    }
+  };
+  if (f32) {
+    for (const TileCost& c : kTilesF32) price(c);
+  } else {
+    for (const TileCost& c : kTiles) price(c);
+  }
+  return best;
 }
 
 template <bool GATED, typename T, typename OT>
 static void dispatch(const LinearProblem& p, hipStream_t stream) {
-  if (p.T > 512) run_tiles<4, 8, GATED, T, OT>(p, stream);
-  else run_tiles<1, 2, GATED, T, OT>(p, stream);
+  constexpr bool kF32 = sizeof(T) == 4;
+  const Plan plan = plan_of(p.T, p.N, p.K, GATED, kF32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16);
+  auto tiles = [&](auto mi, auto ni) {
+    constexpr int MI = decltype(mi)::value, NI = decltype(ni)::value;
+    if (!plan.few && plan.a == MI && plan.b == NI)
+      run_tiles<MI, NI, 4, 128, GATED, T, OT>(p, plan.parts, stream);
+  };
+  // NW waves with D chunks in flight each (fp32: less, for registers and LDS)
+  auto few = [&](auto mt, auto nt, auto r, auto nw, auto d) {
+    constexpr int MT = decltype(mt)::value, NT = decltype(nt)::value, R = decltype(r)::value;
+    if (plan.few && plan.a == MT && plan.b == NT && plan.r == R)
+      run_few<MT, NT, R, decltype(nw)::value, decltype(d)::value, GATED, T, OT>(p, stream);
+  };
+  few(Int<1>{}, Int<1>{}, Int<8>{}, Int<16>{}, Int<kF32 ? 2 : 4>{});
+  few(Int<1>{}, Int<1>{}, Int<16>{}, Int<16>{}, Int<kF32 ? 1 : 4>{});
+  few(Int<1>{}, Int<2>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
+  few(Int<2>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
+  few(Int<2>{}, Int<2>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
+  few(Int<4>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 4 : 8>{}, Int<kF32 ? 1 : 2>{});
+  tiles(Int<1>{}, Int<2>{});
+  tiles(Int<2>{}, Int<4>{});
+  if constexpr (kF32) {
+    tiles(Int<4>{}, Int<4>{});
+  } else {
+    tiles(Int<1>{}, Int<4>{});
+    tiles(Int<2>{}, Int<6>{});
+    tiles(Int<2>{}, Int<8>{});
+    tiles(Int<4>{}, Int<8>{});
+  }
 }
 
 }  // namespace linear
 
-size_t linear_workspace_bytes(int, int, int, int, int) { return 0; }
+size_t linear_workspace_bytes(int T, int N, int K, int gated, int dtype) {
+  const linear::Plan plan = linear::plan_of(T, N, K, gated, dtype);
+  if (plan.few || plan.parts == 1) return 0;
+  const size_t n = (size_t)(N + 3) / 4 * 4 * (gated ? 2 : 1);
+  return (plan.parts * T * n * sizeof(float) + 255) / 256 * 256;
+}
 
 hipError_t launch_linear(const LinearProblem& p, hipStream_t stream) {
   using namespace linear;
