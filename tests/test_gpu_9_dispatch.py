@@ -224,6 +224,63 @@ def test_no_tokens():
     assert m.combine(rows, at).shape == (0, 24)
 
 
+# rows of 60 to 170 MB: both sides of the rules on what all rows together hold, and such rows off
+# the 16-byte grid
+LARGE = [(2000, 8, 64, 64, 16, 1880, "bf16"), (2100, 8, 64, 64, 16, 2000, "bf16"),
+         (2100, 8, 64, 16, 64, 2000, "bf16"), (4200, 8, 128, 128, 1, 2000, "bf16"),
+         (4200, 8, 128, 100, 128, 2001, "bf16"), (2100, 4, 8, 8, 128, 2004, "f32"),
+         (4300, 4, 8, 8, 1, 2004, "f32"), (4300, 4, 8, 6, 16, 2003, "f32"),
+         (300, 66, 80, 80, 1, 4096, "bf16")]
+
+
+@pytest.mark.parametrize("T,k,E,local,block_m,H,dtype", LARGE)
+def test_large(T, k, E, local, block_m, H, dtype):
+    """Against torch on the GPU: the copies and places bit for bit, the sums in 64 bits."""
+    say(f"rows T={T} k={k} E={E}/{local} block_m={block_m} H={H} {dtype}")
+    r, m = Routed(T, k, E, local, block_m, 3), moe()
+    x = torch.randn((T, H), generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(
+        DT[dtype])
+    out, ok = sentinel((r.R, H), dtype)
+    rows, at = m.dispatch(x, r.ids, r.E, r.sid, r.npad, out=out)
+    ok()
+    assert torch.equal(at, r.slot_rows)
+    slot = r.sid[:r.n].long()
+    ref = x[slot.clamp(max=r.S - 1) // k]
+    ref[slot >= r.S] = 0
+    assert torch.equal(rows[:r.n], ref) and bool((rows[r.n:] == 12345.0).all())
+    del ref
+    here, place = (at >= 0), at.long().clamp(min=0)
+    w = torch.where(here, r.w, 0.0)
+
+    def total(weights, src):
+        v = torch.zeros((T, H), dtype=torch.float64, device="cuda")
+        mag = torch.zeros_like(v)
+        for j in range(k):
+            term = src[place[:, j]].double() * weights[:, j, None].double()
+            v += term
+            mag += term.abs()
+        return v.cpu().numpy(), mag.cpu().numpy()
+
+    v, mag = total(w, rows)
+    close(m.combine(rows, at, r.w), v, (2 * k + 1) * U * mag, dtype, "out")
+    v, mag = total(here.float(), rows)
+    close(m.dispatch_backward(rows, at), v, (k + 1) * U * mag, dtype, "dx")
+    drows, ok = sentinel((r.R, H), dtype)
+    _, dw = m.combine_backward(x, rows, at, r.w, r.sid, r.npad, drows=drows)
+    ok()
+    live = slot < r.S
+    wt = torch.where(live, r.w.view(-1)[slot.clamp(max=r.S - 1)], 0.0)
+    ref = (x[slot.clamp(max=r.S - 1) // k].float() * wt[:, None]).to(DT[dtype])
+    assert torch.equal(drows[:r.n].float() + 0.0, ref.float() + 0.0)
+    assert bool((drows[r.n:] == 12345.0).all())
+    dots = torch.zeros((T, k), dtype=torch.float64, device="cuda")
+    mags = torch.zeros_like(dots)
+    for j in range(k):
+        term = x.double() * rows[place[:, j]].double() * here[:, j, None]
+        dots[:, j], mags[:, j] = term.sum(1), term.abs().sum(1)
+    close(dw, dots.cpu().numpy(), (H + 2) * U * mags.cpu().numpy(), "f32", "dweights")
+
+
 def test_offsets_past_32_bits():
     """2^21 + 3 slots of rows of 2056 bf16: more than 2^32 elements; the last rows are checked."""
     T, k, H = (1 << 21) + 3, 1, 2056
