@@ -37,33 +37,31 @@ static dim3 grid_of(int workers) {
   return dim3(std::min(groups, kGridX), (groups + kGridX - 1) / kGridX);
 }
 
-template <int W, int NV, int VEC, typename IO>
+template <int W, int NV, int VEC, bool ANY, typename IO>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void forward_kernel(LayerNormProblem p) {
   __shared__ float red[2][W];
   const int row = my_worker<W>();
   if (row >= p.T) return;  // whole waves, and W = 1 has no barrier
-  const Place<W, NV> c(p.H / VEC);
+  const Span<W, NV, VEC, ANY> c(p.H, W == 1 ? threadIdx.x & 63 : threadIdx.x);
   const size_t base = (size_t)row * p.H;
   Vec<IO, VEC> xr[NV], rr[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) xr[i] = load_vec<IO, VEC>((const IO*)p.x + base + c.at[i] * VEC);
+  for (int i = 0; i < NV; ++i)
+    xr[i] = load_vec<IO, VEC, false, ANY>((const IO*)p.x + base + c.at[i]);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     rr[i] = Vec<IO, VEC>{};
-    if (p.residual) rr[i] = load_vec<IO, VEC>((const IO*)p.residual + base + c.at[i] * VEC);
+    if (p.residual) rr[i] = load_vec<IO, VEC, false, ANY>((const IO*)p.residual + base + c.at[i]);
   }
   float s[NV][VEC], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    keep_vec<IO, VEC>(xr[i], c.mask[i]);
-    keep_vec<IO, VEC>(rr[i], c.mask[i]);
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
       s[i][q] = p.alpha * elem<IO, VEC>(xr[i], q) + elem<IO, VEC>(rr[i], q);
-      sum += s[i][q];
+      sum += c.has(i, q) ? s[i][q] : 0.f;
     }
-    if (c.mask[i] && p.residual_out)
-      store_vec<IO, VEC>((IO*)p.residual_out + base + c.at[i] * VEC, s[i]);
+    if (p.residual_out) c.store(i, (IO*)p.residual_out + base, s[i]);
   }
   const float mean = row_sum<W>(sum, red[0]) / (float)p.H;
   float ss = 0.f;
@@ -72,15 +70,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void forward_kernel(LayerNor
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
       s[i][q] -= mean;
-      ss += c.mask[i] ? s[i][q] * s[i][q] : 0.f;
+      ss += c.has(i, q) ? s[i][q] * s[i][q] : 0.f;
     }
   const float inv = 1.0f / sqrtf(row_sum<W>(ss, red[1]) / (float)p.H + p.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    if (!c.mask[i]) continue;
     Vec<float, VEC> w, b{};
-    if (p.weight) w = load_vec<float, VEC>(p.weight + c.at[i] * VEC);
-    if (p.bias) b = load_vec<float, VEC>(p.bias + c.at[i] * VEC);
+    if (p.weight) w = load_vec<float, VEC, false, ANY>(p.weight + c.at[i]);
+    if (p.bias) b = load_vec<float, VEC, false, ANY>(p.bias + c.at[i]);
     float o[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
@@ -88,7 +85,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void forward_kernel(LayerNor
       if (p.weight) o[q] *= elem<float, VEC>(w, q);
       o[q] += elem<float, VEC>(b, q);
     }
-    store_vec<IO, VEC>((IO*)p.out + base + c.at[i] * VEC, o);
+    c.store(i, (IO*)p.out + base, o);
   }
 }
 
@@ -109,45 +106,54 @@ __device__ __forceinline__ void row_sums(float& a, float& b, f32x2* slot) {
   }
 }
 
-// Worker w takes the rows w, w + workers, ... and writes its sums for the weight and
-// the bias to partial[w] ([2, H]). The slots of the two sums are each written again
-// only past the other's barrier, when all have read them.
-template <int W, int NV, int VEC, typename IO>
-__global__ __launch_bounds__(W == 1 ? 256 : W * 64) void backward_kernel(
-    LayerNormBackwardProblem p, int workers) {
+// A worker of W waves takes the rows w, w + workers, ... . W > 1: it is a workgroup; W = 1:
+// 16 of them are one. At the end a workgroup's sums for the weight and the bias (16 workers'
+// added up in LDS, in order) go to partial[workgroup] ([2, H]). The slots of the two sums over
+// a row are each written again only past the other's barrier, when all have read them. (Two
+// workers of 8 waves to a workgroup, for half the partials, hold each other up at the
+// barriers: 41.4 us instead of 38.8 for 4096 x 4096 bf16.)
+template <int W>
+constexpr int group_waves() {
+  return W == 1 ? 16 : W;
+}
+template <int W, int NV, int VEC, bool ANY, typename IO>
+__global__ __launch_bounds__(group_waves<W>() * 64) void backward_kernel(
+    LayerNormBackwardProblem p) {
+  constexpr int kWorkers = group_waves<W>() / W, kLength = W * 64 * NV * VEC;
   __shared__ f32x2 red[2][W];
-  const int worker = my_worker<W>();
-  if (worker >= workers) return;  // whole waves, and W = 1 has no barrier
-  const Place<W, NV> c(p.H / VEC);
+  __shared__ float sums[2][kWorkers > 1 ? kLength : 1];
+  const int mine = kWorkers == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Span<W, NV, VEC, ANY> c(p.H, threadIdx.x - mine * 64);
   Vec<float, VEC> w[NV];
   float dw[NV][VEC] = {}, db[NV][VEC] = {};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (p.weight) w[i] = load_vec<float, VEC>(p.weight + c.at[i] * VEC);
+    if (p.weight) w[i] = load_vec<float, VEC, false, ANY>(p.weight + c.at[i]);
   const float n = 1.0f / (float)p.H;
-  for (int row = worker; row < p.T; row += workers) {
+  auto weighted = [&](float g, int i, int q) __attribute__((always_inline)) {
+    return p.weight ? g * elem<float, VEC>(w[i], q) : g;
+  };
+  for (int row = blockIdx.x * kWorkers + mine; row < p.T; row += gridDim.x * kWorkers) {
     const size_t base = (size_t)row * p.H;
     Vec<IO, VEC> sr[NV], gr[NV], rr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      sr[i] = load_vec<IO, VEC>((const IO*)p.s + base + c.at[i] * VEC);
-      gr[i] = load_vec<IO, VEC>((const IO*)p.dout + base + c.at[i] * VEC);
+      sr[i] = load_vec<IO, VEC, false, ANY>((const IO*)p.s + base + c.at[i]);
+      gr[i] = load_vec<IO, VEC, false, ANY>((const IO*)p.dout + base + c.at[i]);
       rr[i] = Vec<IO, VEC>{};
       if (p.dresidual_out)
-        rr[i] = load_vec<IO, VEC>((const IO*)p.dresidual_out + base + c.at[i] * VEC);
+        rr[i] = load_vec<IO, VEC, false, ANY>((const IO*)p.dresidual_out + base + c.at[i]);
     }
     float s[NV][VEC], g[NV][VEC], sum = 0.f, sg = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      keep_vec<IO, VEC>(sr[i], c.mask[i]);
-      keep_vec<IO, VEC>(gr[i], c.mask[i]);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
-        s[i][q] = elem<IO, VEC>(sr[i], q);
-        g[i][q] = elem<IO, VEC>(gr[i], q);
+        s[i][q] = c.has(i, q) ? elem<IO, VEC>(sr[i], q) : 0.f;
+        g[i][q] = c.has(i, q) ? elem<IO, VEC>(gr[i], q) : 0.f;
         db[i][q] += g[i][q];
         sum += s[i][q];
-        sg += p.weight ? g[i][q] * elem<float, VEC>(w[i], q) : g[i][q];
+        sg += weighted(g[i][q], i, q);
       }
     }
     row_sums<W>(sum, sg, red[0]);
@@ -157,9 +163,9 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void backward_kernel(
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int q = 0; q < VEC; ++q) {
-        s[i][q] = c.mask[i] ? s[i][q] - mean : 0.f;
+        s[i][q] = c.has(i, q) ? s[i][q] - mean : 0.f;
         ss += s[i][q] * s[i][q];
-        sgs += (p.weight ? g[i][q] * elem<float, VEC>(w[i], q) : g[i][q]) * s[i][q];
+        sgs += weighted(g[i][q], i, q) * s[i][q];
       }
     row_sums<W>(ss, sgs, red[1]);
     const float inv = 1.0f / sqrtf(ss * n + p.eps);
@@ -171,48 +177,63 @@ __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void backward_kernel(
       for (int q = 0; q < VEC; ++q) {
         const float u = s[i][q] * inv;
         dw[i][q] += g[i][q] * u;
-        const float gw = p.weight ? g[i][q] * elem<float, VEC>(w[i], q) : g[i][q];
-        d[q] = (gw - mg - u * mgu) * inv + elem<IO, VEC>(rr[i], q);
+        d[q] = (weighted(g[i][q], i, q) - mg - u * mgu) * inv + elem<IO, VEC>(rr[i], q);
       }
-      if (!c.mask[i]) continue;
-      const size_t at = base + c.at[i] * VEC;
-      if (p.dresidual) store_vec<IO, VEC>((IO*)p.dresidual + at, d);
+      if (p.dresidual) c.store(i, (IO*)p.dresidual + base, d);
 #pragma unroll
       for (int q = 0; q < VEC; ++q) d[q] *= p.alpha;
-      store_vec<IO, VEC>((IO*)p.dx + at, d);
+      c.store(i, (IO*)p.dx + base, d);
     }
   }
   if (!p.dweight && !p.dbias) return;
-  float* mine = p.partial + (size_t)worker * 2 * p.H;
+  float* to = p.partial + (size_t)blockIdx.x * 2 * p.H;
+  if constexpr (kWorkers > 1) {
+    for (int t = 0; t < kWorkers; ++t) {
+      __syncthreads();
+      if (t != mine) continue;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (!c.mask[i]) continue;
-    store_vec<float, VEC>(mine + c.at[i] * VEC, dw[i]);
-    store_vec<float, VEC>(mine + p.H + c.at[i] * VEC, db[i]);
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+          if (!c.has(i, q)) continue;
+          const int at = c.at[i] + q;
+          sums[0][at] = t ? sums[0][at] + dw[i][q] : dw[i][q];
+          sums[1][at] = t ? sums[1][at] + db[i][q] : db[i][q];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x)
+      to[i] = i < p.H ? sums[0][i] : sums[1][i - p.H];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      c.store(i, to, dw[i]);
+      c.store(i, to + p.H, db[i]);
+    }
   }
 }
 
-// The workers' sums added up: a workgroup takes 64 columns of one of the two, wave w
-// the workers w, w + 16, ...; then the waves' in order.
+// The workgroups' sums added up: 32 columns of one of the two to a workgroup here, whose 32
+// half waves take those of the workgroups h, h + 32, ...; then the halves' in order.
 __global__ __launch_bounds__(1024) void finish_kernel(const float* __restrict__ partial,
-                                                      int workers, int H,
+                                                      int partials, int H,
                                                       float* __restrict__ dweight,
                                                       float* __restrict__ dbias) {
-  __shared__ float part[16][64];
+  __shared__ float part[32][32];
   float* out = blockIdx.y ? dbias : dweight;
   if (!out) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 64 + lane;
+  const int at = threadIdx.x & 31, half = threadIdx.x >> 5;
+  const int col = blockIdx.x * 32 + at;
   const float* from = partial + (blockIdx.y ? H : 0) + min(col, H - 1);
   float v = 0.f;
-#pragma unroll 4
-  for (int i = wave; i < workers; i += 16) v += from[(size_t)i * 2 * H];
-  part[wave][lane] = v;
+#pragma unroll 8
+  for (int i = half; i < partials; i += 32) v += from[(size_t)i * 2 * H];
+  part[half][at] = v;
   __syncthreads();
-  if (wave == 0 && col < H) {
+  if (half == 0 && col < H) {
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += part[i][lane];
+    for (int i = 0; i < 32; ++i) v += part[i][at];
     out[col] = v;
   }
 }
@@ -224,74 +245,91 @@ struct Int {
 };
 template <int VEC, typename F>
 static void by_row_length(int H, F f) {
-  const int vecs = H / VEC;
-  if (vecs <= 64) f(Int<1>{}, Int<1>{});
-  else if (vecs <= 128) f(Int<1>{}, Int<2>{});
-  else if (vecs <= 256) f(Int<4>{}, Int<1>{});
-  else if (vecs <= 512) f(Int<8>{}, Int<1>{});
-  else if (vecs <= 1024) f(Int<8>{}, Int<2>{});
-  else if (VEC == 8 || vecs <= 2048) f(Int<16>{}, Int<2>{});
-  else if (VEC == 4 || vecs <= 4096) f(Int<16>{}, Int<4>{});
-  else if constexpr (VEC == 1) f(Int<16>{}, Int<16>{});
+  const int vecs = (H + VEC - 1) / VEC;
+  if (VEC == 1 || vecs <= 64) {
+    f(Int<1>{}, Int<1>{});
+  } else if constexpr (VEC > 1) {
+    if (vecs <= 128) f(Int<1>{}, Int<2>{});
+    else if (vecs <= 256) f(Int<4>{}, Int<1>{});
+    else if (vecs <= 512) f(Int<8>{}, Int<1>{});
+    else if (vecs <= 1024) f(Int<8>{}, Int<2>{});
+    else if (VEC == 8 || vecs <= 2048) f(Int<16>{}, Int<2>{});
+    else if constexpr (VEC == 4) f(Int<16>{}, Int<4>{});
+  }
 }
 
-static int workers_of(int T) { return std::min(T, 512); }
-
-template <int VEC, typename IO>
-static void run_forward(const LayerNormProblem& p, hipStream_t stream) {
-  by_row_length<VEC>(p.H, [&](auto w, auto nv) {
-    constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-    forward_kernel<W, NV, VEC, IO><<<grid_of<W>(p.T), W == 1 ? 256 : W * 64, 0, stream>>>(p);
-  });
+// Calls f(VEC, ANY, type): 16 bytes to a lane; ANY where rows do not start at multiples of
+// 16; rows shorter than that element by element.
+template <typename F>
+static void by_type(int H, int dtype, std::initializer_list<const void*> ptrs, F f) {
+  const int vec = dtype == MOE_DTYPE_BF16 ? 8 : 4;
+  bool any = H % vec != 0;
+  for (const void* p : ptrs) any = any || (uintptr_t)p % 16;
+  const uint16_t b = 0;
+  const float s = 0;
+  if (dtype == MOE_DTYPE_BF16) {
+    if (H < vec) f(Int<1>{}, Int<0>{}, b);
+    else if (any) f(Int<8>{}, Int<1>{}, b);
+    else f(Int<8>{}, Int<0>{}, b);
+  } else {
+    if (H < vec) f(Int<1>{}, Int<0>{}, s);
+    else if (any) f(Int<4>{}, Int<1>{}, s);
+    else f(Int<4>{}, Int<0>{}, s);
+  }
 }
 
-template <int VEC, typename IO>
-static void run_backward(const LayerNormBackwardProblem& p, hipStream_t stream) {
-  const int workers = workers_of(p.T);
-  by_row_length<VEC>(p.H, [&](auto w, auto nv) {
-    constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
-    backward_kernel<W, NV, VEC, IO>
-        <<<grid_of<W>(workers), W == 1 ? 256 : W * 64, 0, stream>>>(p, workers);
-  });
-}
-
-// 16 bytes to a lane where every row starts at a multiple of 16, else one element.
-static bool wide(int H, int dtype, std::initializer_list<const void*> ptrs) {
-  if (H % (dtype == MOE_DTYPE_BF16 ? 8 : 4)) return false;
-  for (const void* p : ptrs)
-    if ((uintptr_t)p % 16) return false;
-  return true;
+// Workgroups of the backward pass for rows of H elements.
+// More of them keep more rows in flight, fewer have fewer sums to write and add up (2 H floats
+// each): an eighth of the rows, at least 256 and at most what these measured (us, bf16): 8192
+// x 2048 256 36.9, 512 28.1, 768 27.4; 4096 x 4096 256 40.1, 512 38.8, 768 45.7; 1000 x 4096 256
+// 15.9, 512 19.6; 8192 x 7168 256 121, 512 129. Rows of one wave: 8192 x 1024 24.5 with 256.
+static int partials_of(int T, int H, int dtype) {
+  const int vec = dtype == MOE_DTYPE_BF16 ? 8 : 4, vecs = (H + vec - 1) / vec;
+  if (H < vec || vecs <= 128) return std::min((T + 15) / 16, 256);
+  const int most = vecs <= 256 ? 768 : vecs <= 512 ? 512 : 256;
+  return std::min(T, std::min(std::max(T / 8, 256), most));
 }
 
 }  // namespace layer_norm
 
 size_t layer_norm_backward_workspace_bytes(int T, int H) {
-  return ((size_t)layer_norm::workers_of(T) * 2 * H * sizeof(float) + 255) / 256 * 256;
+  const int most = std::max(layer_norm::partials_of(T, H, MOE_DTYPE_BF16),
+                            layer_norm::partials_of(T, H, MOE_DTYPE_F32));
+  return ((size_t)most * 2 * H * sizeof(float) + 255) / 256 * 256;
 }
 
 hipError_t launch_layer_norm(const LayerNormProblem& p, hipStream_t stream) {
   using namespace layer_norm;
-  const bool v = wide(p.H, p.dtype, {p.x, p.residual, p.weight, p.bias, p.residual_out, p.out});
-  if (p.dtype == MOE_DTYPE_BF16)
-    v ? run_forward<8, uint16_t>(p, stream) : run_forward<1, uint16_t>(p, stream);
-  else
-    v ? run_forward<4, float>(p, stream) : run_forward<1, float>(p, stream);
+  by_type(p.H, p.dtype, {p.x, p.residual, p.weight, p.bias, p.residual_out, p.out},
+          [&](auto v, auto any, auto io) {
+            constexpr int VEC = decltype(v)::value;
+            by_row_length<VEC>(p.H, [&](auto w, auto nv) {
+              constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
+              forward_kernel<W, NV, VEC, decltype(any)::value != 0, decltype(io)>
+                  <<<grid_of<W>(p.T), W == 1 ? 256 : W * 64, 0, stream>>>(p);
+            });
+          });
   return hipGetLastError();
 }
 
 hipError_t launch_layer_norm_backward(const LayerNormBackwardProblem& p, hipStream_t stream) {
   using namespace layer_norm;
-  const bool v = wide(p.H, p.dtype, {p.dout, p.s, p.weight, p.dresidual_out, p.dx, p.dresidual});
+  const int partials = partials_of(p.T, p.H, p.dtype);
   if (p.T > 0) {
-    if (p.dtype == MOE_DTYPE_BF16)
-      v ? run_backward<8, uint16_t>(p, stream) : run_backward<1, uint16_t>(p, stream);
-    else
-      v ? run_backward<4, float>(p, stream) : run_backward<1, float>(p, stream);
+    by_type(p.H, p.dtype, {p.dout, p.s, p.weight, p.dresidual_out, p.dx, p.dresidual},
+            [&](auto v, auto any, auto io) {
+              constexpr int VEC = decltype(v)::value;
+              by_row_length<VEC>(p.H, [&](auto w, auto nv) {
+                constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
+                backward_kernel<W, NV, VEC, decltype(any)::value != 0, decltype(io)>
+                    <<<partials, group_waves<W>() * 64, 0, stream>>>(p);
+              });
+            });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (p.dweight || p.dbias)
-    finish_kernel<<<dim3((p.H + 63) / 64, 2), 1024, 0, stream>>>(p.partial, workers_of(p.T), p.H,
+    finish_kernel<<<dim3((p.H + 31) / 32, 2), 1024, 0, stream>>>(p.partial, partials, p.H,
                                                                 p.dweight, p.dbias);
   return hipGetLastError();
 }

@@ -16,7 +16,13 @@ struct Vec {
   uint32_t w[kWords];
 };
 
-template <typename T, int VEC, bool NT = false>
+// Vectors that need not start at a multiple of their size (the hardware's loads and stores
+// need not either).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+// ANY: p is aligned to an element only.
+template <typename T, int VEC, bool NT = false, bool ANY = false>
 __device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
   constexpr int N = Vec<T, VEC>::kWords;
   Vec<T, VEC> v;
@@ -24,14 +30,16 @@ __device__ __forceinline__ Vec<T, VEC> load_vec(const T* p) {
     if constexpr (sizeof(T) == 2) v.w[0] = *p;
     else v.w[0] = __float_as_uint(*p);
   } else if constexpr (N == 2) {
-    const u32x2 r = *(const u32x2*)p;
+    const u32x2 r = ANY ? *(const u32x2_any*)p : *(const u32x2*)p;
     v.w[0] = r[0];
     v.w[1] = r[1];
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const u32x4* from = (const u32x4*)p + i / 4;
-      const u32x4 r = NT ? __builtin_nontemporal_load(from) : *from;
+      u32x4 r;
+      if constexpr (ANY) r = ((const u32x4_any*)p)[i / 4];
+      else if constexpr (NT) r = __builtin_nontemporal_load((const u32x4*)p + i / 4);
+      else r = ((const u32x4*)p)[i / 4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v.w[i + q] = r[q];
     }
@@ -49,7 +57,7 @@ __device__ __forceinline__ float elem(const Vec<T, VEC>& v, int i) {
   }
 }
 
-template <typename T, int VEC, bool NT = false>
+template <typename T, int VEC, bool NT = false, bool ANY = false>
 __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
   constexpr int N = Vec<T, VEC>::kWords;
   if constexpr (N == 1) {
@@ -65,12 +73,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
         o[i] = __float_as_uint(v[i]);
     }
     if constexpr (N == 2) {
-      *(u32x2*)p = u32x2{o[0], o[1]};
+      if constexpr (ANY) *(u32x2_any*)p = u32x2{o[0], o[1]};
+      else *(u32x2*)p = u32x2{o[0], o[1]};
     } else {
 #pragma unroll
       for (int i = 0; i < N; i += 4) {
         const u32x4 r{o[i], o[i + 1], o[i + 2], o[i + 3]};
-        if constexpr (NT) __builtin_nontemporal_store(r, (u32x4*)p + i / 4);
+        if constexpr (ANY) ((u32x4_any*)p)[i / 4] = r;
+        else if constexpr (NT) __builtin_nontemporal_store(r, (u32x4*)p + i / 4);
         else ((u32x4*)p)[i / 4] = r;
       }
     }
@@ -98,6 +108,35 @@ struct Place {
       const int c = me + i * W * 64;
       at[i] = min(c, vecs - 1);
       mask[i] = c < vecs ? ~0u : 0u;
+    }
+  }
+};
+
+// The same for rows of any H >= VEC elements: at[i] counts elements, and the vector that
+// would pass the row's end ends with it instead; its first skip[i] elements are the vector's
+// before it (all VEC of a vector past the end) and belong to that one's thread.
+template <int W, int NV, int VEC, bool ANY>
+struct Span {
+  int at[NV], skip[NV];
+  // me: the thread's place among the row's
+  __device__ __forceinline__ Span(int H, int me) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (me + i * W * 64) * VEC;
+      at[i] = min(c, H - VEC);
+      skip[i] = ANY ? min(c - at[i], VEC) : c < H ? 0 : VEC;
+    }
+  }
+  __device__ __forceinline__ bool has(int i, int e) const { return ANY ? e >= skip[i] : skip[i] == 0; }
+  // this thread's elements of vector i
+  template <typename T>
+  __device__ __forceinline__ void store(int i, T* row, const float (&v)[VEC]) const {
+    if (skip[i] == 0) {
+      store_vec<T, VEC, false, ANY>(row + at[i], v);
+    } else if (ANY && skip[i] < VEC) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (e >= skip[i]) store_vec<T, 1>(row + at[i] + e, {v[e]});
     }
   }
 };

@@ -149,7 +149,7 @@ def test_layer_norm_validation():
 
 def test_layer_norm_backward_validation():
     used = lib.moe_layer_norm_backward_workspace_bytes(4, 64)
-    assert used >= 4 * 2 * 64 * 4 and lib.moe_layer_norm_backward_workspace_bytes(0, 64) == 0
+    assert used >= 2 * 64 * 4 and lib.moe_layer_norm_backward_workspace_bytes(0, 64) == 0
     assert lib.moe_layer_norm_backward_workspace_bytes(-1, 64) == 0
     assert lib.moe_layer_norm_backward_workspace_bytes(4, 20000) == 0
     sizes = [lib.moe_layer_norm_backward_workspace_bytes(T, 640) for T in range(0, 20000, 7)]
