@@ -40,30 +40,53 @@ static dim3 grid_of(long waves, int pieces = 1) {
 // 140.
 constexpr size_t kStreamBytes = (size_t)128 << 20;
 
-// The rows of a call are copied in words of 16 bytes where every row starts at one,
-// else by elements.
-template <bool NT, typename U>
-__device__ __forceinline__ void put(U* to, U v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, to);
-  else *to = v;
-}
-template <bool NT, typename U>
-__device__ __forceinline__ void clear_row(U* to, int units) {
-  for (int c = threadIdx.x & 63; c < units; c += 64) put<NT>(to + c, U{});
+// How the rows of a call are copied: in words (U) of 16 bytes; where rows do not start at
+// multiples of 16 (ANY) the last of them ends with the row, and copies part of the one before
+// it again; rows shorter than that by elements.
+template <typename U, bool ANY>
+struct Words {
+  typedef U Word;
+  size_t row;  // bytes
+  int count;   // words of a row
+  template <typename P>
+  __device__ __forceinline__ P* at(P* rows, size_t r) const {
+    if constexpr (ANY) return rows + r * row;  // (P: a byte)
+    else return rows + r * count;
+  }
+  __device__ __forceinline__ U load(const U* from, int c) const { return from[c]; }
+  __device__ __forceinline__ U load(const uint8_t* from, int c) const {
+    return *(const u32x4_any*)(from + min((size_t)c * 16, row - 16));
+  }
+  template <bool NT>
+  __device__ __forceinline__ void store(U* to, int c, U v) const {
+    if constexpr (NT) __builtin_nontemporal_store(v, to + c);
+    else to[c] = v;
+  }
+  template <bool NT>
+  __device__ __forceinline__ void store(uint8_t* to, int c, U v) const {
+    *(u32x4_any*)(to + min((size_t)c * 16, row - 16)) = v;
+  }
+};
+template <bool NT, typename P, typename W>
+__device__ __forceinline__ void clear_row(P* to, const W& w) {
+  for (int c = threadIdx.x & 63; c < w.count; c += 64)
+    w.template store<NT>(to, c, typename W::Word{});
 }
 
-// kCopy words of 64 lanes each from `from`, those past the row's end its last one.
+// kCopy words of 64 lanes each, those past the row's end its last one.
 constexpr int kCopy = 8;
-template <typename U>
-__device__ __forceinline__ void load_piece(const U* from, int c0, int units, U (&v)[kCopy]) {
+template <typename P, typename W>
+__device__ __forceinline__ void load_piece(const P* from, int c0, const W& w,
+                                           typename W::Word (&v)[kCopy]) {
 #pragma unroll
-  for (int i = 0; i < kCopy; ++i) v[i] = from[min(c0 + i * 64, units - 1)];
+  for (int i = 0; i < kCopy; ++i) v[i] = w.load(from, min(c0 + i * 64, w.count - 1));
 }
-template <bool NT, typename U>
-__device__ __forceinline__ void store_piece(U* to, int c0, int units, const U (&v)[kCopy]) {
+template <bool NT, typename P, typename W>
+__device__ __forceinline__ void store_piece(P* to, int c0, const W& w,
+                                            const typename W::Word (&v)[kCopy]) {
 #pragma unroll
   for (int i = 0; i < kCopy; ++i)
-    if (c0 + i * 64 < units) put<NT>(to + c0 + i * 64, v[i]);
+    if (c0 + i * 64 < w.count) w.template store<NT>(to, c0 + i * 64, v[i]);
 }
 
 struct Lists {
@@ -77,9 +100,9 @@ struct Lists {
 // Dispatch in one launch, place by place: one wave per place (the first R waves), its
 // token's row or zeros where it pads a run; then a wave for every 64 slots: -1 for those of
 // another shard's experts. Places at and past num_padded are left alone.
-template <typename U>
-__global__ __launch_bounds__(256) void places_kernel(const U* __restrict__ x, Lists l, int units,
-                                                     int k, U* __restrict__ rows) {
+template <typename P, typename W>
+__global__ __launch_bounds__(256) void places_kernel(const P* __restrict__ x, Lists l, W words,
+                                                     int k, P* __restrict__ rows) {
   const int w = my_wave(), lane = threadIdx.x & 63;
   if (w >= l.R) {
     const long s = (long)(w - l.R) * 64 + lane;
@@ -88,17 +111,15 @@ __global__ __launch_bounds__(256) void places_kernel(const U* __restrict__ x, Li
   }
   if (w >= l.num_padded[0]) return;
   const int slot = __builtin_amdgcn_readfirstlane(l.sorted_ids[w]);
-  U* to = rows + (size_t)w * units;
   if ((unsigned)slot >= (unsigned)l.S) {
-    clear_row<false>(to, units);
+    clear_row<false>(words.at(rows, w), words);
     return;
   }
   if (lane == 0) l.slot_rows[slot] = w;
-  const U* from = x + (size_t)(slot / k) * units;
-  for (int c = lane; c < units; c += 64 * kCopy) {
-    U v[kCopy];
-    load_piece(from, c, units, v);
-    store_piece<false>(to, c, units, v);
+  for (int c = lane; c < words.count; c += 64 * kCopy) {
+    typename W::Word v[kCopy];
+    load_piece(words.at(x, slot / k), c, words, v);
+    store_piece<false>(words.at(rows, w), c, words, v);
   }
 }
 
@@ -114,46 +135,45 @@ __global__ __launch_bounds__(256) void slots_kernel(Lists l) {
     if ((unsigned)slot < (unsigned)l.S) l.slot_rows[slot] = (int)i;
   }
 }
-template <bool NT, typename U>
-__global__ __launch_bounds__(256) void tokens_kernel(const U* __restrict__ x, Lists l, int units,
-                                                     int T, int k, U* __restrict__ rows) {
+template <bool NT, typename P, typename W>
+__global__ __launch_bounds__(256) void tokens_kernel(const P* __restrict__ x, Lists l, W words,
+                                                     int T, int k, P* __restrict__ rows) {
   const int w = my_wave(), lane = threadIdx.x & 63;
   if (w >= T) {
     const long p0 = (long)(w - T) * 8;
     const int n = (int)min((long)min(l.num_padded[0], l.R) - p0, 8L);
     for (int i = 0; i < n; ++i) {
       const int slot = __builtin_amdgcn_readfirstlane(l.sorted_ids[p0 + i]);
-      if ((unsigned)slot >= (unsigned)l.S) clear_row<NT>(rows + (size_t)(p0 + i) * units, units);
+      if ((unsigned)slot >= (unsigned)l.S) clear_row<NT>(words.at(rows, p0 + i), words);
     }
     return;
   }
-  const U* from = x + (size_t)w * units;
-  for (int c = lane; c < units; c += 64 * kCopy) {
-    U v[kCopy];
-    load_piece(from, c, units, v);
+  for (int c = lane; c < words.count; c += 64 * kCopy) {
+    typename W::Word v[kCopy];
+    load_piece(words.at(x, w), c, words, v);
     for (int j0 = 0; j0 < k; j0 += 64) {
       const int at = j0 + lane < k ? l.slot_rows[(size_t)w * k + j0 + lane] : -1;
       for (uint64_t left = __ballot((unsigned)at < (unsigned)l.R); left; left &= left - 1) {
         const int row = __builtin_amdgcn_readlane(at, __builtin_ctzll(left));
-        store_piece<NT>(rows + (size_t)row * units, c, units, v);
+        store_piece<NT>(words.at(rows, row), c, words, v);
       }
     }
   }
 }
 
 // The sum over a token's slots, 64 at a time: lane l holds slot l's place and weight.
-// A wave takes 64 vectors of a token's row; slots without a place are not read.
+// A wave takes 64 vectors of a token's row, the last of which ends with the row (ANY: it may
+// sum some of the one before it again); slots without a place are not read.
 constexpr int kBatch = 8;
-template <int VEC, bool NT, bool WEIGHTED, typename YT, typename IO>
+template <int VEC, bool ANY, bool NT, bool WEIGHTED, typename YT, typename IO>
 __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
                                                       const int32_t* __restrict__ slot_rows,
                                                       const float* __restrict__ weights, int T,
                                                       int H, int k, int R, int pieces,
                                                       IO* __restrict__ out) {
   const int w = my_wave(), lane = threadIdx.x & 63;
-  const int t = w / pieces, c = (w - t * pieces) * 64 + lane, vecs = H / VEC;
+  const int t = w / pieces, c = ((w - t * pieces) * 64 + lane) * VEC, col = min(c, H - VEC);
   if (t >= T) return;
-  const int col = min(c, vecs - 1) * VEC;
   float v[VEC] = {};
   for (int j0 = 0; j0 < k; j0 += 64) {
     const int j = j0 + lane;
@@ -179,7 +199,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
       }
       Vec<YT, VEC> r[kBatch];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) r[q] = load_vec<YT, VEC, NT>(y + (size_t)row[q] * H + col);
+      for (int q = 0; q < kBatch; ++q) r[q] = load_vec<YT, VEC, NT, ANY>(y + (size_t)row[q] * H + col);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         keep_vec<YT, VEC>(r[q], keep[q]);
@@ -188,16 +208,16 @@ __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
       }
     }
   }
-  if (c < vecs) store_vec<IO, VEC>(out + (size_t)t * H + col, v);
+  if (c < H) store_vec<IO, VEC, false, ANY>(out + (size_t)t * H + col, v);
 }
 
 // One wave per slot (the first S waves): its row of the gradient and its weight's, the
 // dot product of the token's gradient with the row; then a wave for every 8 places:
 // zeros in those that pad a run.
 // kPiece: vectors of a lane in flight.
-template <int VEC, int kPiece, bool NT, typename YT, typename IO>
+template <int VEC, bool ANY, int kPiece, bool NT, typename YT, typename IO>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardProblem p) {
-  const int w = my_wave(), lane = threadIdx.x & 63, vecs = p.H / VEC, S = p.T * p.k;
+  const int w = my_wave(), lane = threadIdx.x & 63, S = p.T * p.k;
   if (w >= S) {
     const long p0 = (long)(w - S) * 8;
     const int n = (int)min((long)min(p.num_padded[0], p.R) - p0, 8L);
@@ -206,7 +226,8 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardPr
       if ((unsigned)slot < (unsigned)S) continue;
       const float zero[VEC] = {};
       YT* to = (YT*)p.drows + (size_t)(p0 + i) * p.H;
-      for (int c = lane; c < vecs; c += 64) store_vec<YT, VEC, NT>(to + c * VEC, zero);
+      for (int c = lane * VEC; c < p.H; c += 64 * VEC)
+        store_vec<YT, VEC, NT, ANY>(to + min(c, p.H - VEC), zero);
     }
     return;
   }
@@ -220,26 +241,30 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardPr
   const YT* y = (const YT*)p.rows + (size_t)at * p.H;
   YT* dy = (YT*)p.drows + (size_t)at * p.H;
   float dot = 0.f;
-  for (int c0 = lane; c0 < vecs; c0 += 64 * kPiece) {
+  for (int c0 = lane * VEC; c0 < p.H; c0 += 64 * VEC * kPiece) {
     Vec<IO, VEC> gv[kPiece];
     Vec<YT, VEC> yv[kPiece];
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      const int c = min(c0 + i * 64, vecs - 1);
-      gv[i] = load_vec<IO, VEC>(g + c * VEC);
-      if (p.dweights) yv[i] = load_vec<YT, VEC, NT>(y + c * VEC);
+      const int at = min(c0 + i * 64 * VEC, p.H - VEC);
+      gv[i] = load_vec<IO, VEC, false, ANY>(g + at);
+      if (p.dweights) yv[i] = load_vec<YT, VEC, NT, ANY>(y + at);
     }
 #pragma unroll
     for (int i = 0; i < kPiece; ++i) {
-      if (c0 + i * 64 >= vecs) break;
+      const int c = c0 + i * 64 * VEC, at = min(c, p.H - VEC);
+      if (c >= p.H) break;
       if (p.dweights) {
+        // the last vector's first elements may be those of the one before it, whose lane has
+        // counted them (and, in place, may have written their gradient by now)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dot += elem<IO, VEC>(gv[i], e) * elem<YT, VEC>(yv[i], e);
+        for (int e = 0; e < VEC; ++e)
+          if (!ANY || at + e >= c) dot += elem<IO, VEC>(gv[i], e) * elem<YT, VEC>(yv[i], e);
       }
       float d[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) d[e] = wt * elem<IO, VEC>(gv[i], e);
-      store_vec<YT, VEC, NT>(dy + (c0 + i * 64) * VEC, d);
+      store_vec<YT, VEC, NT, ANY>(dy + at, d);
     }
   }
   dot = wave_sum(dot);
@@ -251,51 +276,54 @@ struct Int {
   static constexpr int value = V;
 };
 
-template <int VEC, typename YT, typename IO>
+template <int VEC, bool ANY, typename YT, typename IO>
 static void run_combine(const CombineProblem& p, hipStream_t stream) {
-  const int pieces = (p.H / VEC + 63) / 64;
+  const int pieces = (p.H + 64 * VEC - 1) / (64 * VEC);
   const dim3 grid = grid_of((long)p.T * pieces);
+  constexpr bool kStream = VEC > 1 && !ANY;
   auto run = [&](auto nt, auto weighted) {
-    combine_kernel<VEC, decltype(nt)::value, decltype(weighted)::value>
+    combine_kernel<VEC, ANY, decltype(nt)::value, decltype(weighted)::value>
         <<<grid, 256, 0, stream>>>((const YT*)p.rows, p.slot_rows, p.topk_weights, p.T, p.H, p.k,
                                    p.R, pieces, (IO*)p.out);
   };
-  const bool nt = VEC > 1 && (size_t)p.T * p.k * p.H * sizeof(YT) > kStreamBytes;
-  if (p.topk_weights) nt ? run(Int<VEC != 1>{}, Int<1>{}) : run(Int<0>{}, Int<1>{});
-  else nt ? run(Int<VEC != 1>{}, Int<0>{}) : run(Int<0>{}, Int<0>{});
+  const bool nt = kStream && (size_t)p.T * p.k * p.H * sizeof(YT) > kStreamBytes;
+  if (p.topk_weights) nt ? run(Int<kStream>{}, Int<1>{}) : run(Int<0>{}, Int<1>{});
+  else nt ? run(Int<kStream>{}, Int<0>{}) : run(Int<0>{}, Int<0>{});
 }
 
-template <int VEC, typename YT, typename IO>
+template <int VEC, bool ANY, typename YT, typename IO>
 static void run_combine_backward(const CombineBackwardProblem& p, hipStream_t stream) {
   const dim3 grid = grid_of((long)p.T * p.k + (p.R + 7) / 8);
   // Eight vectors of a lane in flight for rows of more than four a lane: 32768 rows of 4096
-  // bf16 129.7 us instead of 135.4 with two, 1000 rows of 1030 fp32 3.8 instead of 4.9; 2250
-  // rows of 2048 bf16 8.9 instead of 8.4.
-  const bool nt = VEC > 1 && (size_t)p.T * p.k * p.H * sizeof(YT) > kStreamBytes;
-  if (p.H / VEC <= 256)
-    combine_backward_kernel<VEC, 2, false, YT, IO><<<grid, 256, 0, stream>>>(p);
+  // bf16 129.7 us instead of 135.4 with two; 2250 rows of 2048 bf16 8.9 instead of 8.4.
+  constexpr bool kStream = VEC > 1 && !ANY;
+  const bool nt = kStream && (size_t)p.T * p.k * p.H * sizeof(YT) > kStreamBytes;
+  if (p.H <= 256 * VEC)
+    combine_backward_kernel<VEC, ANY, 2, false, YT, IO><<<grid, 256, 0, stream>>>(p);
   else if (nt)
-    combine_backward_kernel<VEC, 8, VEC != 1, YT, IO><<<grid, 256, 0, stream>>>(p);
+    combine_backward_kernel<VEC, ANY, 8, kStream, YT, IO><<<grid, 256, 0, stream>>>(p);
   else
-    combine_backward_kernel<VEC, 8, false, YT, IO><<<grid, 256, 0, stream>>>(p);
+    combine_backward_kernel<VEC, ANY, 8, false, YT, IO><<<grid, 256, 0, stream>>>(p);
 }
 
-// Calls f(VEC, rows' type, tokens' type) for the types of a call: 16 bytes of the wider
-// type to a lane where every row of both starts at a multiple of 16, else one element.
+// Calls f(VEC, ANY, rows' type, tokens' type) for the types of a call: 16 bytes of the
+// narrower type to a lane, ANY where a row of either does not start at a multiple of 16; rows
+// shorter than that element by element.
 template <typename F>
 static void by_type(int rows_dtype, int dtype, int H, bool aligned, F f) {
   const uint16_t b = 0;
   const float s = 0;
-  const bool b2 = rows_dtype == MOE_DTYPE_BF16 && dtype == MOE_DTYPE_BF16;
-  const bool wide = aligned && H % 8 == 0;
-  if (b2)
-    wide ? f(Int<8>{}, b, b) : f(Int<1>{}, b, b);
-  else if (rows_dtype == MOE_DTYPE_BF16)
-    wide ? f(Int<8>{}, b, s) : f(Int<1>{}, b, s);
-  else if (dtype == MOE_DTYPE_BF16)
-    wide ? f(Int<8>{}, s, b) : f(Int<1>{}, s, b);
-  else
-    aligned && H % 4 == 0 ? f(Int<4>{}, s, s) : f(Int<1>{}, s, s);
+  const bool rb = rows_dtype == MOE_DTYPE_BF16, tb = dtype == MOE_DTYPE_BF16;
+  auto go = [&](auto vec, auto y, auto io) {
+    constexpr int VEC = decltype(vec)::value;
+    if (H < VEC) f(Int<1>{}, Int<0>{}, y, io);
+    else if (aligned && H % VEC == 0) f(vec, Int<0>{}, y, io);
+    else f(vec, Int<1>{}, y, io);
+  };
+  if (rb && tb) go(Int<8>{}, b, b);
+  else if (rb) go(Int<8>{}, b, s);
+  else if (tb) go(Int<8>{}, s, b);
+  else go(Int<4>{}, s, s);
 }
 
 static bool aligned16(std::initializer_list<const void*> ptrs) {
@@ -315,33 +343,38 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
   // instead of 7.1.
   constexpr size_t kTokenBytes = (size_t)64 << 20;
   const size_t all = (size_t)l.S * p.H * bytes;
-  auto run = [&](auto unit) {
-    typedef decltype(unit) U;
-    const int units = p.H * bytes / (int)sizeof(U);
+  // P: what the kernels count rows' addresses in
+  auto run = [&](auto* p0, auto words) {
+    typedef std::remove_pointer_t<decltype(p0)> P;
+    words.row = (size_t)p.H * bytes;
+    words.count = (int)((words.row + sizeof(typename decltype(words)::Word) - 1) /
+                        sizeof(typename decltype(words)::Word));
+    const P* x = (const P*)p.x;
+    P* rows = (P*)p.rows;
     if (all < kTokenBytes) {
-      places_kernel<U><<<grid_of((long)p.R + (l.S + 63) / 64), 256, 0, stream>>>(
-          (const U*)p.x, l, units, p.k, (U*)p.rows);
+      places_kernel<<<grid_of((long)p.R + (l.S + 63) / 64), 256, 0, stream>>>(x, l, words, p.k,
+                                                                             rows);
       return;
     }
     slots_kernel<<<(unsigned)((std::max(l.S, l.R) + 255L) / 256), 256, 0, stream>>>(l);
     const dim3 grid = grid_of((long)p.T + (p.R + 7) / 8);
     if (all > kStreamBytes)
-      tokens_kernel<true, U><<<grid, 256, 0, stream>>>((const U*)p.x, l, units, p.T, p.k,
-                                                       (U*)p.rows);
+      tokens_kernel<true><<<grid, 256, 0, stream>>>(x, l, words, p.T, p.k, rows);
     else
-      tokens_kernel<false, U><<<grid, 256, 0, stream>>>((const U*)p.x, l, units, p.T, p.k,
-                                                        (U*)p.rows);
+      tokens_kernel<false><<<grid, 256, 0, stream>>>(x, l, words, p.T, p.k, rows);
   };
-  if ((size_t)p.H * bytes % 16 == 0 && aligned16({p.x, p.rows})) run(u32x4{});
-  else if (bytes == 4) run(uint32_t{});
-  else run(uint16_t{});
+  if ((size_t)p.H * bytes % 16 == 0 && aligned16({p.x, p.rows}))
+    run((u32x4*)nullptr, Words<u32x4, false>{});
+  else if (p.H * bytes >= 16) run((uint8_t*)nullptr, Words<u32x4, true>{});
+  else if (bytes == 4) run((uint32_t*)nullptr, Words<uint32_t, false>{});
+  else run((uint16_t*)nullptr, Words<uint16_t, false>{});
   return hipGetLastError();
 }
 
 hipError_t launch_combine(const CombineProblem& p, hipStream_t stream) {
   using namespace dispatch;
-  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.rows, p.out}), [&](auto v, auto y, auto io) {
-    run_combine<decltype(v)::value, decltype(y), decltype(io)>(p, stream);
+  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.rows, p.out}), [&](auto v, auto any, auto y, auto io) {
+    run_combine<decltype(v)::value, decltype(any)::value != 0, decltype(y), decltype(io)>(p, stream);
   });
   return hipGetLastError();
 }
@@ -349,8 +382,9 @@ hipError_t launch_combine(const CombineProblem& p, hipStream_t stream) {
 hipError_t launch_combine_backward(const CombineBackwardProblem& p, hipStream_t stream) {
   using namespace dispatch;
   by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.dout, p.rows, p.drows}),
-          [&](auto v, auto y, auto io) {
-            run_combine_backward<decltype(v)::value, decltype(y), decltype(io)>(p, stream);
+          [&](auto v, auto any, auto y, auto io) {
+            run_combine_backward<decltype(v)::value, decltype(any)::value != 0, decltype(y), decltype(io)>(
+                p, stream);
           });
   return hipGetLastError();
 }
