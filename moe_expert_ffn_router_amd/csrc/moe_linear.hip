@@ -1,16 +1,15 @@
 // Matrix product with its epilogue: out = residual + act(x w^T + bias), or gated
 // residual + act(x wg^T + bg) (x wu^T + bu), on the bf16 matrix cores with fp32 sums; fp32
-// operands enter exactly, as three bf16 planes each of which six products are taken.
-// (The fp32 matrix instructions run at a sixteenth of the bf16 rate, and are no closer: both
+// operands enter exactly, as three bf16 planes each of which six products are taken. (The
+// fp32 matrix instructions run at a sixteenth of the bf16 rate, and are no closer: both
 // round as a chain of K additions does, 17 to 18 u rms at K = 4096.)
 //
-// Tile kernel: a workgroup of 2 waves along the w rows and WM along the x rows makes
-// 32 NI w rows x 16 WM MI x rows, wave by wave 16 NI x 16 MI. 128 bytes of every row (a
-// chunk: 64 bf16, 32 fp32) are a stage of a ring in LDS that direct-to-LDS loads fill
-// ahead of the chunk in work, one barrier a chunk. Past the operands' ends (rows, and
-// the last chunk's columns past K) a load's offset lies outside its buffer and gives
-// zeros.
+// Few rows of x: K over the waves of a workgroup, which streams its w rows from HBM. Else
+// tiles of 32 NI w rows x 64 MI x rows, with K in parts over workgroups and a second kernel
+// that joins them where there are few tiles. Past the operands' ends (rows, and the last
+// stage's columns past K) a load's offset lies outside its buffer and gives zeros.
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "moe_common.h"
@@ -192,42 +191,101 @@ struct Columns {
 
 // -------------------------------------------------------------- tiles ---
 
-// A lane's share of 32 k of its row: 16 bytes of bf16, 32 of fp32 as three bf16 planes
-// whose sum it is (moe_skinny.h).
-template <typename T>
-struct Frag {
-  static constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
-  bf16x8 plane[kPlanes];
+// A workgroup of 8 waves, two along the w rows and four along the x rows, each 16 NI w rows x
+// 16 MI x rows.
+constexpr int kWaves = 8;
 
-  // step: which 32 of the stage's k; row, key: the row in LDS and its columns' key
-  __device__ __forceinline__ void read(const uint8_t* row, int key, int step) {
-    const int g = (threadIdx.x >> 4) & 3;
-    if constexpr (sizeof(T) == 2) {
-      plane[0] = __builtin_bit_cast(
-          bf16x8, *(const u32x4*)(row + (((step * 4 + g) ^ key) << 4)));
-    } else {
-      const f32x4 a = *(const f32x4*)(row + (((2 * g) ^ key) << 4));
-      const f32x4 b = *(const f32x4*)(row + (((2 * g + 1) ^ key) << 4));
-      const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-      skinny::split8<kPlanes>(v, plane);
-    }
+// Row in LDS of row r of w tile i of the waves wn. Gated: tile after tile, gate rows in the
+// even ones and their up rows in the odd. Else row r of tile i of a pair lies at (r / 4) 8 +
+// 4 (i odd) + r % 4 of the pair's 32, so that a lane's eight sums of a pair are those of
+// eight consecutive rows.
+template <int NI, bool GATED>
+__device__ __forceinline__ int w_row(int wn, int i, int r) {
+  if (GATED) return (wn * NI + i) * 16 + r;
+  return (wn * (NI / 2) + (i >> 1)) * 32 + (r >> 2) * 8 + (i & 1) * 4 + (r & 3);
+}
+// The row of w (from the tile's first, gated: of gate or of up rows) at row r of LDS.
+template <bool GATED>
+__device__ __forceinline__ int w_at(int r) {
+  return GATED ? (r >> 5) * 16 + (r & 15) : r;
+}
+template <bool GATED>
+__device__ __forceinline__ bool w_up(int r) {
+  return GATED && (r & 16);
+}
+// Column (16 bytes) c of a row lies at column c ^ key in LDS, so that eight lanes of a read,
+// one column of eight rows (of x, and gated of w, in a row; else two times four, eight
+// apart), meet the eight columns of 128 bytes: one row, or two of BYTES = 64.
+template <int BYTES, bool PAIRS>
+__device__ __forceinline__ int key_of(int row) {
+  const int r = PAIRS ? (row & 3) | ((row >> 1) & 4) : row & 7;
+  return BYTES == 128 ? r : r >> 1;
+}
+
+// Workgroups go round the 8 XCDs: the b-th gets a tile of its XCD's share, a run of
+// consecutive tiles (shares differ by one at most).
+__device__ __forceinline__ int xcd_order(int b, int tiles) {
+  const int per = tiles >> 3, rest = tiles & 7, q = b & 7;
+  return q * per + min(q, rest) + (b >> 3);
+}
+// Tiles run down panels of kPanel columns, row by row: consecutive tiles share the rows of w
+// and x that an XCD's L2 then holds (8192^3: 1249 TFLOP/s, with panels of 4 1204, of 16 1183).
+constexpr int kPanel = 8;
+__device__ __forceinline__ void panel(int t, int m_tiles, int n_tiles, int& m, int& n) {
+  const int q = t / (kPanel * m_tiles), in = t - q * kPanel * m_tiles;
+  const int wide = min(kPanel, n_tiles - q * kPanel);
+  m = in / wide;
+  n = q * kPanel + in - m * wide;
+}
+
+// What a workgroup works on: its tile, its part of K (blockIdx.y of gridDim.y) in stages of
+// 128 bytes of every row.
+constexpr int kRowBytes = 128;
+template <int MI, int NI, bool GATED, typename T>
+struct Tile {
+  static constexpr int kRowsW = 32 * NI, kRowsX = 64 * MI;
+  static constexpr int kCols = GATED ? kRowsW / 2 : kRowsW;  // outputs of a row
+  static_assert(NI % 2 == 0, "pairs of tiles");
+  int wave, lane, wn, wm, m0, n0, first, stages;
+  int bytes;              // of K from its first stage on
+  uint32_t wstep, xstep;  // bytes from row to row
+
+  __device__ __forceinline__ Tile(const LinearProblem& p, int n_tiles)
+      : wave(uni(threadIdx.x >> 6)), lane(threadIdx.x & 63), wn(wave & 1), wm(wave >> 1) {
+    int tile_m, tile_n;
+    panel(xcd_order(blockIdx.x, gridDim.x), gridDim.x / n_tiles, n_tiles, tile_m, tile_n);
+    m0 = tile_m * kRowsX;
+    n0 = tile_n * kCols;
+    const int row = p.K * (int)sizeof(T), all = (row + kRowBytes - 1) / kRowBytes;
+    first = (int)((long)all * blockIdx.y / gridDim.y);
+    stages = (int)((long)all * (blockIdx.y + 1) / gridDim.y) - first;
+    bytes = min(row - first * kRowBytes, stages * kRowBytes);
+    wstep = (uint32_t)p.K * sizeof(T);
+    xstep = (uint32_t)p.ldx * sizeof(T);
+  }
+  // The tile's first row of w (or of the up rows) and of x, at the part's first stage, and the
+  // bytes from there to the end of a stage of the last row that is there.
+  __device__ __forceinline__ const uint8_t* w(const LinearProblem& p, bool up) const {
+    return uni_ptr((const uint8_t*)p.w + (size_t)(n0 + (up ? p.N : 0)) * wstep +
+                   (size_t)first * kRowBytes);
+  }
+  __device__ __forceinline__ const uint8_t* x(const LinearProblem& p) const {
+    return uni_ptr((const uint8_t*)p.x + (size_t)m0 * xstep + (size_t)first * kRowBytes);
+  }
+  __device__ __forceinline__ uint32_t w_size(const LinearProblem& p) const {
+    return uni((min(kCols, p.N - n0) - 1) * wstep + kRowBytes);
+  }
+  __device__ __forceinline__ uint32_t x_size(const LinearProblem& p) const {
+    return uni((min(kRowsX, p.T - m0) - 1) * xstep + kRowBytes);
   }
 };
-template <typename T>
-__device__ __forceinline__ void multiply(f32x4& acc, const Frag<T>& w, const Frag<T>& x) {
-#pragma unroll
-  for (int a = Frag<T>::kPlanes - 1; a >= 0; --a)
-#pragma unroll
-    for (int b = Frag<T>::kPlanes - 1; b >= 0; --b)
-      if (a + b <= 2) acc = mfma_bf16(w.plane[a], x.plane[b], acc);
-}
 
 // A product added in place, where it stands: the reads and loads of the loop are placed
 // among the products by hand. (As a builtin the compiler moved them together, and gave sums
 // new registers, 184 copies a step with 256 of them to a wave: 1249 TFLOP/s for 8192^3
 // instead of 1331.) It knows nothing of the matrix instruction in here: what writes the sums
 // before the first and reads them after the last goes through settle().
-__device__ __forceinline__ void mfma_in_place(f32x4& acc, const bf16x8& a, const bf16x8& b) {
+__device__ __forceinline__ void mfma_in_place(f32x4& acc, const u32x4& a, const u32x4& b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 // Orders everything else that touches the sums before or after the products, by more than
@@ -242,205 +300,247 @@ __device__ __forceinline__ void settle(f32x4 (&acc)[NI][MI]) {
   }
 }
 
-// Row in LDS of row r of w tile i of the waves wn. Gated: tile after tile, gate rows in the
-// even ones and their up rows in the odd. Else row r of tile i of a pair lies at (r / 4) 8 +
-// 4 (i odd) + r % 4 of the pair's 32, so that a lane's eight sums of a pair are those of
-// eight consecutive rows.
-template <int NI, bool GATED>
-__device__ __forceinline__ int w_row(int wn, int i, int r) {
-  if (GATED) return (wn * NI + i) * 16 + r;
-  return (wn * (NI / 2) + (i >> 1)) * 32 + (r >> 2) * 8 + (i & 1) * 4 + (r & 3);
-}
-// Column (16 bytes) c of a row lies at column c ^ key in LDS, so that eight lanes of a read,
-// one column of eight rows (of x, and gated of w, in a row; else two times four, eight
-// apart), meet the eight columns of 128 bytes: one row, or two of 64.
-template <int B, bool PAIRS>
-__device__ __forceinline__ int key_of(int row) {
-  const int r = PAIRS ? (row & 3) | ((row >> 1) & 4) : row & 7;
-  return B == 128 ? r : r >> 1;
-}
-
-// A workgroup of 2 x WM waves, each 16 NI w rows x 16 MI x rows; B bytes of every row are a
-// stage.
-template <int MI, int NI, int WM, int B>
-struct Shape {
-  static constexpr int kWaves = 2 * WM;
-  static constexpr int kRowsW = 32 * NI, kRowsX = 16 * MI * WM;
-  // a load takes kPer rows; the waves' loads take kStep, and every wave has the same number
-  // of them, so that what is in flight is known
-  static constexpr int kPer = 1024 / B, kStep = kPer * kWaves;
-  static constexpr int kLoadsW = kRowsW / kStep, kLoadsX = kRowsX / kStep;
+// bf16: direct-to-LDS loads fill a ring of stages, two steps of 32 k each. A load takes 8 rows
+// and the waves' loads 64; every wave has the same number of them, so that what is in flight
+// is known.
+template <int MI, int NI, bool GATED>
+struct Sums16 {
+  typedef Tile<MI, NI, GATED, uint16_t> Where;
+  static constexpr int kLoadsW = Where::kRowsW / 64, kLoadsX = Where::kRowsX / 64;
   static constexpr int kLoads = kLoadsW + kLoadsX;
-  static_assert(NI % 2 == 0 && kRowsW % kStep == 0 && kRowsX % kStep == 0, "whole loads");
-  static constexpr int kStage = (kRowsW + kRowsX) * B;
+  static constexpr int kStage = (Where::kRowsW + Where::kRowsX) * kRowBytes;
   static constexpr int kStages = kLds / kStage < 5 ? kLds / kStage : 5;
+  static constexpr int kLdsBytes = kStages * kStage;
+
+  static __device__ __forceinline__ void run(const LinearProblem& p, const Where& t, uint8_t* lds,
+                                             f32x4 (&acc)[NI][MI]) {
+    // This wave's loads: lane l the 16 bytes that belong at column l % 8 of row l / 8, from the
+    // rows of the tile that are there (a buffer of that size). Few registers for them: the sums
+    // and two steps' operands take nearly all that a wave has.
+    const int lane = t.lane, row = t.wave * 8 + (lane >> 3);  // of the first load of w and of x
+    const uint8_t* wbase = t.w(p, w_up<GATED>(t.wave * 8));   // (rows 64 on are alike)
+    const uint8_t* xbase = t.x(p);
+    const uint32_t wsize = t.w_size(p), xsize = t.x_size(p);
+    const int wcol = ((lane & 7) ^ key_of<128, !GATED>(row)) * 16;
+    const int xcol = ((lane & 7) ^ key_of<128, false>(row)) * 16;
+    const uint32_t woff = w_at<GATED>(row) * t.wstep + wcol, xoff = row * t.xstep + xcol;
+    const uint32_t wnext = w_at<GATED>(64) * t.wstep, xnext = 64 * t.xstep;
+    // the i-th load of stage c; past the last stage all zeros
+    auto issue = [&](int i, int c, int slot) __attribute__((always_inline)) {
+      const int left = t.bytes - c * kRowBytes;  // bytes of K from this stage on
+      const bool is_w = i < kLoadsW;
+      const int q = is_w ? i : i - kLoadsW;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((is_w ? wbase : xbase) + (size_t)c * kRowBytes), (short)0,
+          (int)(is_w ? wsize : xsize), kRsrcWord3);
+      const uint32_t o = (is_w ? wcol : xcol) < left ? (is_w ? woff : xoff) : kOOB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs,
+          (lds_ptr_t)(lds + slot * kStage +
+                      ((is_w ? 0 : Where::kRowsW) + q * 64 + t.wave * 8) * kRowBytes),
+          16, (int)(o + q * (is_w ? wnext : xnext)), 0, 0, 0);
+    };
+    // operand q of a step (h of the stage): the x tiles', then the w tiles'; lane l the k-group
+    // l / 16 of row l % 16
+    const int r = lane & 15, g = lane >> 4;
+    auto read = [&](u32x4(&wf)[NI], u32x4(&xf)[MI], int q, int slot, int h)
+        __attribute__((always_inline)) {
+      const uint8_t* at = lds + slot * kStage;
+      if (q < MI) {
+        const int x = Where::kRowsW + (t.wm * MI + q) * 16 + r;
+        xf[q] = *(const u32x4*)(at + x * kRowBytes + (((h * 4 + g) ^ key_of<128, false>(r)) << 4));
+      } else {
+        const int w = w_row<NI, GATED>(t.wn, q - MI, r);
+        wf[q - MI] = *(const u32x4*)(at + w * kRowBytes +
+                                     (((h * 4 + g) ^ key_of<128, !GATED>(w)) << 4));
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < kStages; ++c)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) issue(i, c, c);
+    int slot = 0;
+    u32x4 w0[NI], x0[MI], w1[NI], x1[MI];
+    // A step's products, with the reads of the next one's operands among the first of them
+    // and, in a stage's last step, the loads that fill its slot again. The stage's own
+    // operands are all read by then, and the next stage's loads have landed: in this wave
+    // where it waits, in all past the barrier.
+    auto step = [&](const u32x4(&wa)[NI], const u32x4(&xa)[MI], u32x4(&wb)[NI], u32x4(&xb)[MI],
+                    bool last, int c) __attribute__((always_inline)) {
+      const int here = slot;
+      if (last) {
+        wait_loads<(kStages - 2) * kLoads, 0>();
+        ring_barrier();
+        slot = slot == kStages - 1 ? 0 : slot + 1;
+      }
+      constexpr int kReads = NI + MI, kMma = NI * MI;
+      constexpr int kPer = kMma >= 2 * kReads ? 2 : 1, kGap = kMma >= 2 * kLoads ? 2 : 1;
+#pragma unroll
+      for (int n = 0; n < kMma || n / kPer < kReads || n / kGap < kLoads; ++n) {
+        if (n < kMma) mfma_in_place(acc[n / MI][n % MI], wa[n / MI], xa[n % MI]);
+        if (n % kPer == 0 && n / kPer < kReads) read(wb, xb, n / kPer, slot, last ? 0 : 1);
+        if (last && n % kGap == kGap - 1 && n / kGap < kLoads)
+          issue(n / kGap, c + kStages, here);
+      }
+    };
+    wait_loads<(kStages - 1) * kLoads>();
+    ring_barrier();
+#pragma unroll
+    for (int q = 0; q < NI + MI; ++q) read(w0, x0, q, 0, 0);
+    settle<0>(acc);
+    for (int c = 0; c < t.stages; ++c) {
+      step(w0, x0, w1, x1, false, c);
+      step(w1, x1, w0, x0, true, c);
+    }
+    settle<0>(acc);
+  }
 };
 
-// Workgroups go round the 8 XCDs: the b-th gets a tile of its XCD's share, a run of
-// consecutive tiles (shares differ by one at most).
-__device__ __forceinline__ int xcd_order(int b, int tiles) {
-  const int per = tiles >> 3, rest = tiles & 7, q = b & 7;
-  return q * per + min(q, rest) + (b >> 3);
-}
-// Tiles run down panels of kPanel columns, row by row: consecutive tiles share the rows
-// of w and x that an XCD's L2 then holds.
-constexpr int kPanel = 8;
-__device__ __forceinline__ void panel(int t, int m_tiles, int n_tiles, int& m, int& n) {
-  const int q = t / (kPanel * m_tiles), in = t - q * kPanel * m_tiles;
-  const int wide = min(kPanel, n_tiles - q * kPanel);
-  m = in / wide;
-  n = q * kPanel + in - m * wide;
+// fp32: 8 floats are three bf16 planes of 8 significant bits each, cut off one after the
+// other: exact (8 + 8 + 8 bits), and no value is rounded up to an infinity.
+__device__ __forceinline__ void cut8(const u32x4& lo, const u32x4& hi, u32x4 (&out)[3]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = __uint_as_float(i < 2 ? lo[2 * i] : hi[2 * i - 4]);
+    float b = __uint_as_float(i < 2 ? lo[2 * i + 1] : hi[2 * i - 3]);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+      out[p][i] = __builtin_amdgcn_perm(ub, ua, 0x07060302);  // the high halves
+      a -= __uint_as_float(ua & 0xffff0000u);
+      b -= __uint_as_float(ub & 0xffff0000u);
+    }
+  }
 }
 
-template <int MI, int NI, int WM, int B, bool GATED, typename T, typename OT>
-__global__ __launch_bounds__(2 * WM * 64, WM / 2) void tile_kernel(LinearProblem p,
-                                                                         int n_tiles) {
-  typedef Shape<MI, NI, WM, B> S;
-  constexpr int kWaves = S::kWaves;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[S::kStages * S::kStage];
-  const int wave = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wn = wave & 1, wm = wave >> 1;
-  const int tile = xcd_order(blockIdx.x, gridDim.x);
-  int tile_m, tile_n;
-  panel(tile, gridDim.x / n_tiles, n_tiles, tile_m, tile_n);
-  constexpr int kCols = GATED ? S::kRowsW / 2 : S::kRowsW;  // outputs of a row
-  const int m0 = tile_m * S::kRowsX, n0 = tile_n * kCols;
-
-  // This wave's loads, kPer rows each: every lane 16 bytes, which the rows' order in memory
-  // and the key of their place in LDS decide, from the rows of the tile that are there (a
-  // buffer of that size). Few registers for them: the sums and two steps' operands take
-  // nearly all of a wave's 512.
-  constexpr int kLanes = B / 16;  // of a row
-  const uint32_t wstep = (uint32_t)p.K * sizeof(T), xstep = (uint32_t)p.ldx * sizeof(T);
-  const int row = wave * S::kPer + lane / kLanes;  // of the first load of w and of x
-  // gated: 16 gate rows, 16 up rows, ...: of which the later loads' are a multiple of 32 on
-  static_assert(!GATED || S::kStep % 32 == 0, "gate and up rows");
-  const bool up = GATED && ((wave * S::kPer) & 16);
-  const uint8_t* wbase = uni_ptr((const uint8_t*)p.w + (size_t)(n0 + (up ? p.N : 0)) * wstep);
-  const uint8_t* xbase = uni_ptr((const uint8_t*)p.x + (size_t)m0 * xstep);
-  const uint32_t wsize = uni((min(kCols, p.N - n0) - 1) * wstep + B);
-  const uint32_t xsize = uni((min(S::kRowsX, p.T - m0) - 1) * xstep + B);
-  const int wcol = ((lane % kLanes) ^ key_of<B, !GATED>(row)) * 16;
-  const int xcol = ((lane % kLanes) ^ key_of<B, false>(row)) * 16;
-  const uint32_t woff = (GATED ? (row >> 5) * 16 + (row & 15) : row) * wstep + wcol;
-  const uint32_t xoff = row * xstep + xcol;
-  const uint32_t wnext = (GATED ? S::kStep / 2 : S::kStep) * wstep, xnext = S::kStep * xstep;
-  // this workgroup's part of K (blockIdx.y of gridDim.y)
-  const int all = (p.K * (int)sizeof(T) + B - 1) / B;
-  const int first = (int)((long)all * blockIdx.y / gridDim.y);
-  const int stages = (int)((long)all * (blockIdx.y + 1) / gridDim.y) - first;
-  const int bytes = min(p.K * (int)sizeof(T) - first * B, stages * B);
-  wbase += (size_t)first * B;
-  xbase += (size_t)first * B;
-  // the i-th load of stage c; past the last stage all zeros
-  auto issue = [&](int i, int c, int slot) __attribute__((always_inline)) {
-    const int left = bytes - c * B;  // bytes of K from this stage on
-    const bool is_w = i < S::kLoadsW;
-    const int q = is_w ? i : i - S::kLoadsW;
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)((is_w ? wbase : xbase) + (size_t)c * B), (short)0, (int)(is_w ? wsize : xsize),
-        kRsrcWord3);
-    const uint32_t o = (is_w ? wcol : xcol) < left ? (is_w ? woff : xoff) : kOOB;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        rs,
-        (lds_ptr_t)(lds + slot * S::kStage +
-                    ((is_w ? 0 : S::kRowsW) + q * S::kStep + wave * S::kPer) * B),
-        16, (int)(o + q * (is_w ? wnext : xnext)), 0, 0, 0);
+// A stage (32 k) is loaded into registers, cut into planes and written to one of two slots
+// of LDS, every value once for the whole workgroup; the products of planes p + q <= 2 are
+// summed. Two stages are under way in registers while one is multiplied.
+template <int MI, int NI, bool GATED>
+struct Sums32 {
+  typedef Tile<MI, NI, GATED, float> Where;
+  static constexpr int kRows = Where::kRowsW + Where::kRowsX;
+  static constexpr int kPlane = kRows * 64, kStage = 3 * kPlane, kLdsBytes = 2 * kStage;
+  static constexpr int kLoads = kRows / 128;  // of 8 floats a thread, four threads to a row
+  static_assert(kRows % 128 == 0 && kLdsBytes <= kLds, "whole loads");
+  struct Stage {
+    u32x4 v[kLoads][2];
   };
 
+  static __device__ __forceinline__ void run(const LinearProblem& p, const Where& t, uint8_t* lds,
+                                             f32x4 (&acc)[NI][MI]) {
+    const int lane = t.lane, g4 = lane & 3;
+    const uint8_t* base[kLoads];
+    uint32_t size[kLoads], off[kLoads];
+    int to[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row0 = i * 128 + t.wave * 16, row = row0 + (lane >> 2);  // 16 rows of one kind
+      const bool is_w = row0 < Where::kRowsW;
+      const int r = is_w ? w_at<GATED>(row) : row - Where::kRowsW;
+      base[i] = is_w ? t.w(p, w_up<GATED>(row0)) : t.x(p);
+      size[i] = is_w ? t.w_size(p) : t.x_size(p);
+      off[i] = r * (is_w ? t.wstep : t.xstep) + g4 * 32;
+      const int key = is_w ? key_of<64, !GATED>(row) : key_of<64, false>(row - Where::kRowsW);
+      to[i] = row * 64 + ((g4 ^ key) << 4);
+    }
+    auto load = [&](Stage& s, int c) __attribute__((always_inline)) {
+      const int left = t.bytes - c * kRowBytes;
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(base[i] + (size_t)c * kRowBytes), (short)0, (int)size[i], kRsrcWord3);
+        const uint32_t o = g4 * 32 < left ? off[i] : kOOB;  // (K a multiple of 8)
+        s.v[i][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)o, 0, 0);
+        s.v[i][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)o, 16, 0);
+      }
+    };
+    auto cut = [&](const Stage& s, int slot) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        u32x4 plane[3];
+        cut8(s.v[i][0], s.v[i][1], plane);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *(u32x4*)(lds + slot * kStage + q * kPlane + to[i]) = plane[q];
+      }
+    };
+    const int r = lane & 15, g = lane >> 4;
+    auto operand = [&](int slot, int plane, int row, int key) __attribute__((always_inline)) {
+      return __builtin_bit_cast(
+          bf16x8,
+          *(const u32x4*)(lds + slot * kStage + plane * kPlane + row * 64 + ((g ^ key) << 4)));
+    };
+    // Stage c: its slot is written in this wave, past the barrier in all; all have read the
+    // other slot by then, too, which the next stage goes to.
+    auto stage = [&](Stage& s, int c) __attribute__((always_inline)) {
+      const int slot = c & 1;
+      wait_loads<63, 0>();
+      ring_barrier();
+      bf16x8 wf[NI][3], xf[MI][3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+#pragma unroll
+        for (int j = 0; j < MI; ++j)
+          xf[j][q] = operand(slot, q, Where::kRowsW + (t.wm * MI + j) * 16 + r,
+                             key_of<64, false>(r));
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const int row = w_row<NI, GATED>(t.wn, i, r);
+          wf[i][q] = operand(slot, q, row, key_of<64, !GATED>(row));
+        }
+      }
+      cut(s, slot ^ 1);
+      load(s, c + 3);
+#pragma unroll
+      for (int a = 2; a >= 0; --a)
+#pragma unroll
+        for (int b = 2 - a; b >= 0; --b)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < MI; ++j) acc[i][j] = mfma_bf16(wf[i][a], xf[j][b], acc[i][j]);
+    };
+    Stage s0, s1;
+    load(s0, 0);
+    load(s1, 1);
+    cut(s0, 0);
+    load(s0, 2);
+    for (int c = 0; c < t.stages; c += 2) {  // (a stage more than there are: zeros)
+      stage(s1, c);
+      stage(s0, c + 1);
+    }
+  }
+};
+
+template <int MI, int NI, bool GATED, typename T, typename OT>
+__global__ __launch_bounds__(kWaves * 64, 2) void tile_kernel(LinearProblem p, int n_tiles) {
+  typedef std::conditional_t<sizeof(T) == 2, Sums16<MI, NI, GATED>, Sums32<MI, NI, GATED>> Sums;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Sums::kLdsBytes];
+  const Tile<MI, NI, GATED, T> t(p, n_tiles);
   f32x4 acc[NI][MI];
 #pragma unroll
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < MI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int r = lane & 15;
-  // operand q of a step: the x tiles', then the w tiles'
-  auto read = [&](Frag<T>(&wf)[NI], Frag<T>(&xf)[MI], int q, int slot, int step)
-      __attribute__((always_inline)) {
-    const uint8_t* at = lds + slot * S::kStage;
-    if (q < MI) {
-      xf[q].read(at + (S::kRowsW + (wm * MI + q) * 16 + r) * B, key_of<B, false>(r), step);
-    } else {
-      const int row = w_row<NI, GATED>(wn, q - MI, r);
-      wf[q - MI].read(at + row * B, key_of<B, !GATED>(row), step);
-    }
-  };
-#pragma unroll
-  for (int c = 0; c < S::kStages; ++c)
-#pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) issue(i, c, c);
-  int slot = 0;
-  if constexpr (sizeof(T) == 2) {
-    constexpr int kSteps = B / 64;  // of a stage
-    Frag<T> w0[NI], x0[MI], w1[NI], x1[MI];
-    // A step's products, with the reads of the next one's operands among the first of them
-    // and, in a stage's last step, the loads that fill its slot again. The stage's own
-    // operands are all read by then, and the next stage's loads have landed: in this wave
-    // where it waits, in all past the barrier.
-    auto step = [&](const Frag<T>(&wa)[NI], const Frag<T>(&xa)[MI], Frag<T>(&wb)[NI],
-                    Frag<T>(&xb)[MI], int h, int c) __attribute__((always_inline)) {
-      const bool last = h == kSteps - 1;
-      const int here = slot;
-      if (last) {
-        wait_loads<(S::kStages - 2) * S::kLoads, 0>();
-        ring_barrier();
-        slot = slot == S::kStages - 1 ? 0 : slot + 1;
-      }
-      constexpr int kReads = NI + MI, kMma = NI * MI;
-      constexpr int kPer = kMma >= 2 * kReads ? 2 : 1;
-      constexpr int kGap = kMma >= 2 * S::kLoads ? 2 : 1;
-#pragma unroll
-      for (int n = 0; n < kMma || n / kPer < kReads || n / kGap < S::kLoads; ++n) {
-        if (n < kMma) mfma_in_place(acc[n / MI][n % MI], wa[n / MI].plane[0], xa[n % MI].plane[0]);
-        if (n % kPer == 0 && n / kPer < kReads)
-          read(wb, xb, n / kPer, slot, last ? 0 : h + 1);
-        if (last && n % kGap == kGap - 1 && n / kGap < S::kLoads)
-          issue(n / kGap, c + S::kStages, here);
-      }
-    };
-    wait_loads<(S::kStages - 1) * S::kLoads>();
-    ring_barrier();
-#pragma unroll
-    for (int q = 0; q < NI + MI; ++q) read(w0, x0, q, 0, 0);
-    settle<0>(acc);
-    for (int c = 0; c < stages; c += 3 - kSteps) {  // (a stage more than there are: zeros)
-      step(w0, x0, w1, x1, 0, c);
-      step(w1, x1, w0, x0, kSteps - 1, kSteps == 2 ? c : c + 1);
-    }
-    settle<0>(acc);
-  } else {
-    for (int c = 0; c < stages; ++c) {
-      wait_loads<(S::kStages - 1) * S::kLoads>();
-      ring_barrier();
-      Frag<T> wf[NI], xf[MI];
-#pragma unroll
-      for (int q = 0; q < NI + MI; ++q) read(wf, xf, q, slot, 0);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < MI; ++j) multiply<T>(acc[i][j], wf[i], xf[j]);
-      wait_loads<63, 0>();
-      ring_barrier();  // all waves have read the slot
-#pragma unroll
-      for (int i = 0; i < S::kLoads; ++i) issue(i, c + S::kStages, slot);
-      slot = slot == S::kStages - 1 ? 0 : slot + 1;
-    }
-  }
+  Sums::run(p, t, lds, acc);
+
   // A wave's sums, as many of its 16-row tiles at a time as its piece of LDS holds, and back
   // along rows: whole lines of out and residual, and one copy of the epilogue's code.
   constexpr int kCell = 16 * NI * 4 + 16;  // bytes of a row, a column of banks apart
-  constexpr int kAt = S::kStages * S::kStage / kWaves / (16 * kCell);
-  constexpr int kGroup = kAt < MI ? kAt : MI;
+  constexpr int kAt = Sums::kLdsBytes / kWaves / (16 * kCell);
+  constexpr int kGroup = kAt >= MI ? MI : kAt >= 2 && MI % 2 == 0 ? 2 : 1;
   constexpr int kFours = GATED ? 2 * NI : 4 * NI;  // of a row's outputs
   constexpr int kRows = 64 / kFours;               // rows at a time, a lane to four columns
   constexpr int kTurns = (kGroup * 16 + kRows - 1) / kRows;
-  static_assert(kGroup >= 1 && MI % kGroup == 0, "LDS of a wave");
-  uint8_t* mine = lds + wave * kGroup * 16 * kCell;
+  static_assert(kAt >= 1 && MI % kGroup == 0, "LDS of a wave");
+  const int lane = t.lane;
+  uint8_t* mine = lds + t.wave * kGroup * 16 * kCell;
   const int row0 = lane / kFours, q = lane - row0 * kFours;
-  const Columns<GATED, OT> cols(p,
-                                row0 < kRows ? n0 + wn * (GATED ? 8 : 16) * NI + q * 4 : p.N);
+  const Columns<GATED, OT> cols(
+      p, row0 < kRows ? t.n0 + t.wn * (GATED ? 8 : 16) * NI + q * 4 : p.N);
   const uint8_t* cell = mine + (GATED ? (q >> 2) * 128 + (q & 3) * 16 : q * 16);
-  const int m1 = m0 + wm * MI * 16 + row0;
+  const int m1 = t.m0 + t.wm * MI * 16 + row0;
   typename Four<OT>::type raw[2][kTurns];
   auto at = [&](int j0, int a) __attribute__((always_inline)) {
     return kGroup * 16 % kRows == 0 || row0 + a * kRows < kGroup * 16 ? m1 + j0 * 16 + a * kRows
@@ -457,7 +557,7 @@ __global__ __launch_bounds__(2 * WM * 64, WM / 2) void tile_kernel(LinearProblem
     for (int j = j0; j < j0 + kGroup; ++j)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        *(f32x4*)(mine + ((j - j0) * 16 + r) * kCell +
+        *(f32x4*)(mine + ((j - j0) * 16 + (lane & 15)) * kCell +
                   w_row<NI, GATED>(0, i, (lane >> 4) * 4) * 4) = acc[i][j];
     if (whole && j0 + kGroup < MI)
       cols.fetch(p, [&](int a) { return at(j0 + kGroup, a); }, raw[(j0 / kGroup + 1) & 1]);
@@ -537,14 +637,12 @@ __global__ __launch_bounds__(NW * 64) void few_kernel(LinearProblem p) {
 
 // ------------------------------------------------------------------ plan ---
 
-template <int MI, int NI, int WM, int B, bool GATED, typename T, typename OT>
+template <int MI, int NI, bool GATED, typename T, typename OT>
 static void run_tiles(const LinearProblem& p, int parts, hipStream_t stream) {
-  typedef Shape<MI, NI, WM, B> S;
-  const int mt = (p.T + S::kRowsX - 1) / S::kRowsX;
-  const int cols = GATED ? S::kRowsW / 2 : S::kRowsW;
-  const int nt = (p.N + cols - 1) / cols;
-  tile_kernel<MI, NI, WM, B, GATED, T, OT>
-      <<<dim3(mt * nt, parts), S::kWaves * 64, 0, stream>>>(p, nt);
+  typedef Tile<MI, NI, GATED, T> Where;
+  const int mt = (p.T + Where::kRowsX - 1) / Where::kRowsX;
+  const int nt = (p.N + Where::kCols - 1) / Where::kCols;
+  tile_kernel<MI, NI, GATED, T, OT><<<dim3(mt * nt, parts), kWaves * 64, 0, stream>>>(p, nt);
   if (parts > 1) {
     const long fours = (long)p.T * ((p.N + 3) / 4);
     join_kernel<GATED, OT><<<(unsigned)((fours + 255) / 256), 256, 0, stream>>>(p, parts);
@@ -581,13 +679,20 @@ struct TileCost {
 // tiles are few: 64 x gated 2048 x 7168 in 4 15.8 (whole 27.0), 700 x 700 x 8192 in 2 21.5 (30.8);
 // the joining kernel takes 3.2 and its bytes. Few rows: w streams at 90 GB/s a CU and 7.5 TB/s
 // in all, x comes from L2 at 140: 16 x gated 2048 x 7168 11.5 (tiles 14.5), 16 x 4096 x 4096 7.7
-// (10.9), 64 x 512 x 512 3.3 (4.7), but 64 x 7168 x 2048 14.5 (10.0).
+// (10.9), 64 x 512 x 512 3.3 (4.7), but 64 x 7168 x 2048 14.5 (10.0). fp32: 2048 x 4096 x 4096 4 x 4
+// 306 (2 x 4 340, 1 x 2 434), 256 rows 2 x 4 in 4 53 (1 x 2 67), 300 x 512 x 512 1 x 2 in 4 8.5 (whole
+// 10.6), 16 x 4096 x 4096 few rows 15.6 (tiles 27).
 static const TileCost kTiles[] = {{1, 2, 3.3f, 0.21f, 0.255f}, {1, 4, 3.8f, 0.24f, 0.31f},
                                   {2, 4, 4.5f, 0.34f, 0.48f},  {2, 6, 5.0f, 0.46f, 0.68f},
                                   {2, 8, 5.5f, 0.57f, 0.86f},  {4, 8, 8.0f, 1.05f, 1.5f}};
-static const TileCost kTilesF32[] = {{1, 2, 3.3f, 0.85f, 1.0f}, {2, 4, 4.5f, 1.4f, 1.75f},
-                                     {4, 4, 5.5f, 2.2f, 2.8f}};
-static const int kFew[][3] = {{1, 1, 8}, {1, 1, 16}, {1, 2, 16}, {2, 1, 16}, {2, 2, 16}, {4, 1, 16}};
+static const TileCost kTilesF32[] = {{1, 2, 3.3f, 0.42f, 0.48f}, {2, 4, 4.5f, 0.9f, 1.25f},
+                                     {4, 4, 5.5f, 1.6f, 2.3f}};
+struct FewCost {
+  int mt, nt, r;
+  float f32;  // fp32 takes that much longer than its bytes say: fewer waves (0: not at all)
+};
+static const FewCost kFew[] = {{1, 1, 8, 1.f},  {1, 1, 16, 1.f}, {1, 2, 16, 0.f},
+                               {2, 1, 16, 1.f}, {2, 2, 16, 0.f}, {4, 1, 16, 1.8f}};
 constexpr int kCus = 256;
 
 static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
@@ -601,14 +706,15 @@ static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
       best = p;
     }
   };
-  for (const auto& f : kFew) {
-    if (T > f[0] * f[2]) continue;
-    const int cols = f[1] * f[2] / half;
+  for (const FewCost& f : kFew) {
+    if (T > f.mt * f.r || (f32 && f.f32 == 0.f)) continue;
+    const int cols = f.nt * f.r / half;
     const long tiles = ((long)N + cols - 1) / cols;
-    const float w = 1e-3f * f[1] * f[2] * K * size, x = 1e-3f * f[0] * f[2] * K * size;  // KB
+    const float w = 1e-3f * f.nt * f.r * K * size, x = 1e-3f * f.mt * f.r * K * size;  // KB
     const float all = w * std::min<long>(tiles, kCus) / (f32 ? 6000.f : 7500.f);
-    take(2.5f + (float)((tiles + kCus - 1) / kCus) * (std::max(w / 90.f, all) + x / 140.f),
-         Plan{true, f[0], f[1], f[2], 1});
+    const float round = std::max(w / 90.f, all) + x / 140.f;
+    take(2.5f + (float)((tiles + kCus - 1) / kCus) * round * (f32 ? f.f32 : 1.f),
+         Plan{true, f.mt, f.nt, f.r, 1});
   }
   const int stages = (K * size + 127) / 128;
   auto price = [&](const TileCost& c) {
@@ -640,7 +746,7 @@ static void dispatch(const LinearProblem& p, hipStream_t stream) {
   auto tiles = [&](auto mi, auto ni) {
     constexpr int MI = decltype(mi)::value, NI = decltype(ni)::value;
     if (!plan.few && plan.a == MI && plan.b == NI)
-      run_tiles<MI, NI, 4, 128, GATED, T, OT>(p, plan.parts, stream);
+      run_tiles<MI, NI, GATED, T, OT>(p, plan.parts, stream);
   };
   // NW waves with D chunks in flight each (fp32: less, for registers and LDS)
   auto few = [&](auto mt, auto nt, auto r, auto nw, auto d) {
@@ -650,10 +756,12 @@ static void dispatch(const LinearProblem& p, hipStream_t stream) {
   };
   few(Int<1>{}, Int<1>{}, Int<8>{}, Int<16>{}, Int<kF32 ? 2 : 4>{});
   few(Int<1>{}, Int<1>{}, Int<16>{}, Int<16>{}, Int<kF32 ? 1 : 4>{});
-  few(Int<1>{}, Int<2>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
-  few(Int<2>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
-  few(Int<2>{}, Int<2>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
+  few(Int<2>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<2>{});
   few(Int<4>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 4 : 8>{}, Int<kF32 ? 1 : 2>{});
+  if constexpr (!kF32) {
+    few(Int<1>{}, Int<2>{}, Int<16>{}, Int<16>{}, Int<2>{});
+    few(Int<2>{}, Int<2>{}, Int<16>{}, Int<16>{}, Int<2>{});
+  }
   tiles(Int<1>{}, Int<2>{});
   tiles(Int<2>{}, Int<4>{});
   if constexpr (kF32) {
