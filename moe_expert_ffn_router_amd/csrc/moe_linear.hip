@@ -691,7 +691,7 @@ struct FewCost {
   int mt, nt, r;
   float f32;  // fp32 takes that much longer than its bytes say: fewer waves (0: not at all)
 };
-static const FewCost kFew[] = {{1, 1, 8, 1.f},  {1, 1, 16, 1.f}, {1, 2, 16, 0.f},
+static const FewCost kFew[] = {{1, 1, 8, 1.15f}, {1, 1, 16, 1.f}, {1, 2, 16, 0.f},
                                {2, 1, 16, 1.f}, {2, 2, 16, 0.f}, {4, 1, 16, 1.8f}};
 constexpr int kCus = 256;
 
@@ -756,7 +756,7 @@ static void dispatch(const LinearProblem& p, hipStream_t stream) {
   };
   few(Int<1>{}, Int<1>{}, Int<8>{}, Int<16>{}, Int<kF32 ? 2 : 4>{});
   few(Int<1>{}, Int<1>{}, Int<16>{}, Int<16>{}, Int<kF32 ? 1 : 4>{});
-  few(Int<2>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<2>{});
+  few(Int<2>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 8 : 16>{}, Int<kF32 ? 1 : 2>{});
   few(Int<4>{}, Int<1>{}, Int<16>{}, Int<kF32 ? 4 : 8>{}, Int<kF32 ? 1 : 2>{});
   if constexpr (!kF32) {
     few(Int<1>{}, Int<2>{}, Int<16>{}, Int<16>{}, Int<2>{});
