@@ -716,7 +716,7 @@ MOE_EXPORT moe_status moe_layer_norm_backward(const void* dout, const void* s,
 static moe_status check_linear(int T, int N, int K, int dtype) {
   if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
   if (T < 0 || (long)T >= kMaxSlots || N < 1 || N >= kMaxLength) return MOE_ERR_SHAPE;
-  if (K < 8 || K % 8 != 0 || K >= 1 << 21) return MOE_ERR_SHAPE;
+  if (K < 8 || K % 8 != 0 || K >= 1 << 21 || (long)T * N >= 1L << 37) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 

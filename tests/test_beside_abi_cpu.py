@@ -199,7 +199,8 @@ def test_linear_validation():
     assert linear(dt=FP8) == UNSUP and linear(odt=FP8) == UNSUP
     assert linear(act=-1) == UNSUP and linear(act=5) == UNSUP
     for bad in (dict(T=-1), dict(T=1 << 24), dict(N=0), dict(N=1 << 24), dict(K=0), dict(K=4),
-                dict(K=60), dict(K=1 << 21, ldx=1 << 21), dict(ldx=56), dict(ldx=68),
+                dict(K=60), dict(T=1 << 20, N=1 << 17, ldo=1 << 17, ldr=1 << 17),
+                dict(K=1 << 21, ldx=1 << 21), dict(ldx=56), dict(ldx=68),
                 dict(ldx=1 << 21), dict(ldo=31), dict(ldr=31), dict(ldo=1 << 31),
                 dict(ldr=1 << 31), dict(ldx=66, dt=F32)):
         assert linear(**bad) == SHAPE, bad

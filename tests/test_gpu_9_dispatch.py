@@ -281,6 +281,24 @@ def test_large(T, k, E, local, block_m, H, dtype):
     close(dw, dots.cpu().numpy(), (H + 2) * U * mags.cpu().numpy(), "f32", "dweights")
 
 
+@pytest.mark.parametrize("H,dtype", [(1 << 20, "bf16"), ((1 << 20) - 1, "bf16"), (1 << 20, "f32")])
+def test_longest_rows(H, dtype):
+    say(f"rows of {H} {dtype}")
+    r, m = Routed(3, 2, 4, 3, 2, 5), moe()
+    x = rand(r.g, 3, H, dtype=dtype)
+    rows, at = m.dispatch(x, r.ids, r.E, r.sid, r.npad)
+    assert torch.equal(bits(rows[:r.n]).cpu(), torch.from_numpy(
+        lo.dispatch(bits(x).cpu().numpy(), r.sid_h, r.n, 2)))
+    y = f64(rows[:r.n])
+    close(m.combine(rows, at, r.w), lo.combine(y, r.at, f64(r.w)),
+          5 * U * lo.combine(np.abs(y), r.at, f64(r.w)), dtype, "out")
+    drows, dw = m.combine_backward(x, rows, at, r.w, r.sid, r.npad)
+    ref, ref_w = lo.combine_backward(f64(x), y, r.at, f64(r.w), r.n)
+    _, mag = lo.combine_backward(np.abs(f64(x)), np.abs(y), r.at, f64(r.w), r.n)
+    close(drows[:r.n], ref, U * np.abs(ref), dtype, "drows")
+    close(dw, ref_w, (H / 64 + 8) * U * mag, "f32", "dweights")   # a lane adds H / 64, then six steps
+
+
 def test_offsets_past_32_bits():
     """2^21 + 3 slots of rows of 2056 bf16: more than 2^32 elements; the last rows are checked."""
     T, k, H = (1 << 21) + 3, 1, 2056
