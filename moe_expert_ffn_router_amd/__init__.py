@@ -608,9 +608,11 @@ def _launch_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
     if dev != torch.cuda.current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        return _raw_stream(dev) if _raw_stream is not None else _stream(None)
+    if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, tensors are on cuda:{dev}")
-    return _stream(stream)
+    return stream.cuda_stream
 
 
 def _empty(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:

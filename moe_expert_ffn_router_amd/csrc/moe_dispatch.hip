@@ -6,8 +6,11 @@
 //   combine            out[t] = sum_j w[t,j] rows[at[t,j]]
 //   its gradient       drows[at[t,j]] = w[t,j] dout[t], dw[t,j] = dout[t] . rows[at[t,j]]
 //
-// Bound by HBM: each kernel reads and writes a row once. A wave takes a row (or a
-// piece of it), lanes along it, sums in a fixed order in fp32.
+// Bound by HBM: each kernel reads and writes a row once, 16 bytes to a lane; a wave takes a
+// row (or a piece of it), lanes along it, sums in a fixed order in fp32. Measured (captured
+// into a graph), 4096 tokens x top-8 x 4096 bf16, runs padded to 128: dispatch 73 us = 5.0
+// TB/s, combine 53 us = 5.7 TB/s, its gradient 131 us = 4.9 TB/s (a copy of 1 GiB: 5.1); 16
+// tokens: dispatch 2.8 us, combine 2.3.
 #include <algorithm>
 #include <type_traits>
 
@@ -161,9 +164,10 @@ __global__ __launch_bounds__(256) void tokens_kernel(const P* __restrict__ x, Li
   }
 }
 
-// The sum over a token's slots, 64 at a time: lane l holds slot l's place and weight.
-// A wave takes 64 vectors of a token's row, the last of which ends with the row (ANY: it may
-// sum some of the one before it again); slots without a place are not read.
+// The combine, and without weights the dispatch's gradient: the sum over a token's slots, 64 at
+// a time, lane l holding slot l's place and weight. A wave takes 64 vectors of a token's row,
+// the last of which ends with the row (ANY: it may sum some of the one before it again);
+// slots without a place are not read.
 constexpr int kBatch = 8;
 template <int VEC, bool ANY, bool NT, bool WEIGHTED, typename YT, typename IO>
 __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
@@ -211,7 +215,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
   if (c < H) store_vec<IO, VEC, false, ANY>(out + (size_t)t * H + col, v);
 }
 
-// One wave per slot (the first S waves): its row of the gradient and its weight's, the
+// The combine's gradient. One wave per slot (the first S waves): its row of the gradient and its weight's, the
 // dot product of the token's gradient with the row; then a wave for every 8 places:
 // zeros in those that pad a run.
 // kPiece: vectors of a lane in flight.

@@ -7,8 +7,12 @@
 //   ds = (g - mean(g) - u mean(g u)) / sqrt(var + eps)  [+ dresidual_out]
 // takes two sums over the row twice (s and g, then (s - mean)^2 and g (s - mean)); the
 // gradients of weight and bias are sums over all rows, which every worker (W waves with
-// one row after the other) keeps in registers for its own rows and writes once, for a
-// second kernel that adds the workers' in a fixed order. Bound by HBM.
+// one row after the other) keeps in registers for its own rows; a workgroup writes its sums
+// once, for a second kernel that adds the workgroups' in a fixed order. Bound by HBM, small
+// calls by their launches. Measured (captured into a graph), bf16 with residual: forward 16 x
+// 4096 2.5 us, 4096 x 4096 22.7 us = 5.9 TB/s; backward 4096 x 4096 39 us (35 = 5.2 TB/s with its
+// 16 MB of sums, and 4 the second kernel), 8192 x 7168 120 us = 4.9 TB/s, 100 x 4096 7.6 us; fp32
+// 777 x 1031 forward 3.7 us, backward 11.
 #include <algorithm>
 
 #include "../../include/moe.h"
@@ -21,10 +25,12 @@ namespace layer_norm {
 
 using namespace rows;
 
+// The forward pass's row of this thread: W > 1 waves: one row per workgroup; W = 1: a row per
+// wave, four to a workgroup. Workgroups lie in a grid of kGridX columns (a launch counts its
+// threads in 32 bits along a dimension).
 constexpr int kGridX = 1 << 20;
-// Worker of this thread: W > 1 waves make a workgroup; W = 1: four to one.
 template <int W>
-__device__ __forceinline__ int my_worker() {
+__device__ __forceinline__ int my_row() {
   const int group = blockIdx.y * kGridX + blockIdx.x;
   if constexpr (W == 1)
     return __builtin_amdgcn_readfirstlane(group * 4 + (threadIdx.x >> 6));
@@ -32,15 +38,15 @@ __device__ __forceinline__ int my_worker() {
     return group;
 }
 template <int W>
-static dim3 grid_of(int workers) {
-  const int groups = W == 1 ? (workers + 3) / 4 : workers;
+static dim3 grid_of(int T) {
+  const int groups = W == 1 ? (T + 3) / 4 : T;
   return dim3(std::min(groups, kGridX), (groups + kGridX - 1) / kGridX);
 }
 
 template <int W, int NV, int VEC, bool ANY, typename IO>
 __global__ __launch_bounds__(W == 1 ? 256 : W * 64) void forward_kernel(LayerNormProblem p) {
   __shared__ float red[2][W];
-  const int row = my_worker<W>();
+  const int row = my_row<W>();
   if (row >= p.T) return;  // whole waves, and W = 1 has no barrier
   const Span<W, NV, VEC, ANY> c(p.H, W == 1 ? threadIdx.x & 63 : threadIdx.x);
   const size_t base = (size_t)row * p.H;
