@@ -272,7 +272,8 @@ struct Tile {
     xstep = (uint32_t)p.ldx * sizeof(T);
   }
   // The tile's first row of w (or of the up rows) and of x, at the part's first stage, and the
-  // bytes from there to the end of a stage of the last row that is there.
+  // bytes from there to the end of a stage of the last row that is there (of the row itself
+  // where a stage is longer: rows that follow are not there).
   __device__ __forceinline__ const uint8_t* w(const LinearProblem& p, bool up) const {
     return uni_ptr((const uint8_t*)p.w + (size_t)(n0 + (up ? p.N : 0)) * wstep +
                    (size_t)first * kRowBytes);
@@ -281,10 +282,10 @@ struct Tile {
     return uni_ptr((const uint8_t*)p.x + (size_t)m0 * xstep + (size_t)first * kRowBytes);
   }
   __device__ __forceinline__ uint32_t w_size(const LinearProblem& p) const {
-    return uni((min(kCols, p.N - n0) - 1) * wstep + kRowBytes);
+    return uni((min(kCols, p.N - n0) - 1) * wstep + min(kRowBytes, bytes));
   }
   __device__ __forceinline__ uint32_t x_size(const LinearProblem& p) const {
-    return uni((min(kRowsX, p.T - m0) - 1) * xstep + kRowBytes);
+    return uni((min(kRowsX, p.T - m0) - 1) * xstep + min(kRowBytes, bytes));
   }
 };
 

@@ -86,6 +86,14 @@ def test_sizes(T, N, K, dtype):
         ("bf16", "f32", dtype)[q % 3])
 
 
+@pytest.mark.parametrize("K", [8, 16, 24, 32, 40, 56])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_shorter_than_a_stage(K, dtype):
+    """Several rows lie within the bytes that a stage takes of one, also behind the last."""
+    for T, N, gated in ((130, 70, False), (300, 131, True), (65, 33, True), (513, 257, False)):
+        run(T, N, K, "relu", gated, True, True, dtype)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("T,N,K", [(5, 76, 200), (40, 131, 264), (300, 260, 136), (700, 516, 72)])
