@@ -557,10 +557,9 @@ moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, int block_m,
  * product of a shared expert or a dense block; the first two with their
  * gradients. These steps are not in the pages; their formulas are stated here in
  * full. Arithmetic and sums are fp32; each output is rounded once (RNE) from the
- * fp32 value, and sums run in a fixed order: equal calls give equal bits. Vectors
- * of 16 bytes are used where rows start at multiples of 16; other lengths and
- * alignments (of an element at least, MOE_ERR_ALIGN below that) run element by
- * element.
+ * fp32 value, and sums run in a fixed order: equal calls give equal bits. Rows of
+ * any length and alignment (of an element at least, MOE_ERR_ALIGN below that) are
+ * taken; those that start at multiples of 16 bytes run fastest.
  */
 
 /*
@@ -649,8 +648,8 @@ moe_status moe_combine_backward(const void* dout, int dtype, const void* rows, i
  *                (MOE_ERR_UNSUPPORTED).
  *  weight, bias  [H] float32, either NULL: 1 and 0.
  *  Limits: 0 <= T < 2^24, 1 <= H <= MOE_NORM_MAX_H, eps finite and >= 0
- *  (MOE_ERR_UNSUPPORTED otherwise; with eps = 0 a row of equal values gives NaN).
- *  A row whose sum or sum of squares leaves the fp32 range is outside the contract.
+ *  (MOE_ERR_UNSUPPORTED otherwise). Outside the contract: a row of equal values
+ *  with eps = 0, and one whose sum or sum of squares leaves the fp32 range.
  */
 moe_status moe_layer_norm(const void* x, const void* residual, const float* weight,
                           const float* bias, float alpha, float eps, int T, int H, int dtype,
@@ -722,15 +721,17 @@ enum {
  *                more), 256-byte aligned, no initialisation needed, apart from
  *                every operand; NULL where that is 0. Calls that share one must
  *                not overlap in time (two graphs captured with it included).
+ *                A smaller T may need more: one for calls of several sizes has the
+ *                largest of their numbers.
  *  Bits are fixed for given sizes and types; a batch of another T may add a row's
  *  products in another order.
- *  Limits: 0 <= T < 2^24, 1 <= N < 2^24, T * N < 2^37, K a multiple of 8 below
- *  2^21, ldx a multiple of 8 (fp32: 4) in [K, 2^21), ldo and ldr at least N and
- *  below 2^31; x and w 16-byte aligned, bias, out and residual by their elements. Infinities and
- *  NaN in a row of x or w make the outputs that read it non-finite, and no
- *  others; with few rows fp32 values from 3.39e38 on (which round to a bf16
- *  infinity) may count as infinities, and bits of one below 2^-133 (the smallest
- *  bf16) do not count. T == 0 launches nothing.
+ *  Limits: 0 <= T < 2^24, 1 <= N < 2^24 (gated: 2^23), T * N < 2^37, K a multiple
+ *  of 8 below 2^21, ldx a multiple of 8 (fp32: 4) in [K, 2^21), ldo and ldr at
+ *  least N and below 2^31; x and w 16-byte aligned, bias, out and residual by
+ *  their elements. Infinities and NaN in a row of x or w make the outputs that
+ *  read it non-finite, and no others; with few rows fp32 values from 3.39e38 on
+ *  (which round to a bf16 infinity) may count as infinities, and bits of one below
+ *  2^-133 (the smallest bf16) do not count. T == 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
 moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias, int activation,

@@ -713,15 +713,16 @@ MOE_EXPORT moe_status moe_layer_norm_backward(const void* dout, const void* s,
       (hipStream_t)stream));
 }
 
-static moe_status check_linear(int T, int N, int K, int dtype) {
+static moe_status check_linear(int T, int N, int K, int gated, int dtype) {
   if (!bf16_or_f32(dtype)) return MOE_ERR_UNSUPPORTED;
-  if (T < 0 || (long)T >= kMaxSlots || N < 1 || N >= kMaxLength) return MOE_ERR_SHAPE;
+  if (T < 0 || (long)T >= kMaxSlots || N < 1) return MOE_ERR_SHAPE;
+  if ((long)N * (gated ? 2 : 1) >= kMaxLength) return MOE_ERR_SHAPE;
   if (K < 8 || K % 8 != 0 || K >= 1 << 21 || (long)T * N >= 1L << 37) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
 MOE_EXPORT size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype) {
-  if (check_linear(T, N, K, dtype) != MOE_OK) return 0;
+  if (check_linear(T, N, K, gated, dtype) != MOE_OK) return 0;
   return moe::linear_workspace_bytes(T, N, K, gated != 0, dtype);
 }
 
@@ -732,7 +733,7 @@ MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const
                                  moe_stream_t stream) {
   if (!bf16_or_f32(out_dtype) || activation < MOE_ACT_NONE || activation > MOE_ACT_GELU_TANH)
     return MOE_ERR_UNSUPPORTED;
-  moe_status s = check_linear(T, N, K, dtype);
+  moe_status s = check_linear(T, N, K, gated, dtype);
   if (s != MOE_OK) return s;
   const size_t b = elem_bytes(dtype), ob = elem_bytes(out_dtype);
   if (ldx < (size_t)K || ldx >= 1 << 21 || ldx % (16 / b) != 0) return MOE_ERR_SHAPE;

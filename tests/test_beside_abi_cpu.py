@@ -204,6 +204,9 @@ def test_linear_validation():
                 dict(ldx=1 << 21), dict(ldo=31), dict(ldr=31), dict(ldo=1 << 31),
                 dict(ldr=1 << 31), dict(ldx=66, dt=F32)):
         assert linear(**bad) == SHAPE, bad
+    # gated: the rows of w count
+    assert linear(gated=1, N=1 << 23, ldo=1 << 23, ldr=1 << 23) == SHAPE
+    assert linear(gated=1, N=(1 << 23) - 1, ldo=1 << 23, ldr=1 << 23, x=None) == NULL
     assert linear(ldx=68, dt=F32, x=None) == NULL
     assert linear(res=None, ldr=0, x=None) == NULL            # ldr is ignored
     for name in ("x", "w", "out"):
