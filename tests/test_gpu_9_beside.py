@@ -9,7 +9,7 @@ import torch
 import oracle
 from oracle import layer_oracle as lo
 from tests.gpu_util import moe, say
-from tests.layer_util import DT, f64, gen, rand
+from tests.layer_util import DT, U, close, f64, gen, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -120,6 +120,57 @@ def test_side_stream():
     for name, t in ref.items():
         if isinstance(t, torch.Tensor):
             assert torch.equal(got[name], t), name
+
+
+def test_two_at_once():
+    """Two blocks on two streams, each with workspaces of its own, give what they give alone; K in
+    parts (a workspace) and few rows among them."""
+    say("two blocks at once")
+    m, g = moe(), gen(5)
+    blocks = [Block(*BLOCKS[i], seed=30 + i) for i in (1, 3)]
+    xs = [rand(g, T, 4096, dtype="bf16") for T in (100, 200)]
+    ws = [rand(g, 512, 4096, dtype="bf16") for _ in xs]
+    assert all(m.linear_workspace_bytes(x.shape[0], 512, 4096, False, 1) > 0 for x in xs)
+
+    def both(i, stream):
+        return b_run(blocks[i], stream), m.linear(xs[i], ws[i], stream=stream)
+
+    def b_run(b, stream):
+        return {n: t for n, t in b.run(stream).items() if isinstance(t, torch.Tensor)}
+
+    ref = [both(i, None) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in blocks]
+    for _ in range(3):
+        # the products of both queued before either is waited for
+        got = [[m.linear(xs[i], ws[i], stream=streams[i]) for _ in range(8)] for i in (0, 1)]
+        runs = [b_run(blocks[i], streams[i]) for i in (0, 1)]
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            for out in got[i]:
+                assert torch.equal(out, ref[i][1])
+            for name, t in ref[i][0].items():
+                assert torch.equal(runs[i][name], t), name
+
+
+def test_the_same_expert_twice():
+    """A token whose ids name one expert twice has two places, whose rows count twice."""
+    say("the same expert twice")
+    m, g = moe(), gen(6)
+    T, E, H, M = 37, 4, 264, 8
+    ids = torch.randint(0, E, (T, 1), generator=g, dtype=torch.int32).cuda().repeat(1, 3)
+    ids[:, 2] = (ids[:, 2] + 1) % E
+    ids = ids.contiguous()
+    x, w = rand(g, T, H), rand(g, T, 3)
+    sid, be, n = m.align_block(ids, E, M)
+    rows, at = m.dispatch(x, ids, E, sid, n)
+    a = at.cpu()
+    assert a.unique().numel() == T * 3 and int(a.min()) >= 0
+    for j in range(3):
+        assert torch.equal(rows[a[:, j].cuda().long()], x)
+    close(m.combine(rows, at, w), f64(w).sum(1, keepdims=True) * f64(x),
+          4 * U * np.abs(f64(w)).sum(1, keepdims=True) * np.abs(f64(x)), "f32", "combine")
+    close(m.dispatch_backward(rows, at), 3 * f64(x), 3 * U * np.abs(f64(x)), "f32", "dx")
 
 
 def test_with_norm_out():
