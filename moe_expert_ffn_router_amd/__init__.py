@@ -169,6 +169,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 # The handle of a device's current stream without a Stream object around it: the
 # object costs 2.4 us of every call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device, where a tensor on one shows that the runtime is up.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
@@ -605,7 +607,7 @@ def _launch_stream(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
     """The stream a call on tensors of device ``dev`` runs on. The library
     launches on the current device, so its tensors (and a stream that is passed)
     are there."""
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if stream is None:
@@ -626,11 +628,35 @@ def _empty(like: torch.Tensor, shape, dtype, stream: Optional[torch.cuda.Stream]
         return like.new_empty(shape, dtype=dtype)
 
 
+def _like(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """_empty of the contiguous tensor ``t``'s own shape and type."""
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
+def _matrix(t: torch.Tensor, name: str) -> tuple:
+    """Check a contiguous matrix of activations on a device. Returns its dtype code, its device's
+    index and its shape."""
+    if isinstance(t, torch.Tensor):
+        code, dev, shape = _ACT.get(t.dtype), t.get_device(), t.shape
+        if code is not None and dev >= 0 and len(shape) == 2 and t.is_contiguous():
+            return code, dev, shape
+    shape = _dims(t, name, 2)
+    code = _act(t, name)
+    _need(t, name, (t.dtype,))
+    return code, t.get_device(), shape
+
+
 def _need_rows(t: torch.Tensor, name: str, dtypes, dev: Optional[int] = None, shape=None) -> int:
     """Check a matrix of contiguous rows that may lie apart (a slice of columns
     of a wider one): a device tensor of one of ``dtypes`` with stride 1 along the
     rows. Returns its row stride in elements."""
     rows, cols = _dims(t, name, 2)
+    if (t.dtype in dtypes and t.get_device() == (t.get_device() if dev is None else dev) >= 0
+            and (shape is None or (rows, cols) == shape) and t.is_contiguous()):
+        return cols
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device (cuda/hip) tensor, got {t.device}")
     if dev is not None and t.get_device() != dev:
@@ -842,10 +868,7 @@ def dispatch(x, topk_ids, E: int, sorted_ids, num_padded, out=None, slot_rows=No
     as it returned them. Returns (rows [R, H], slot_rows [T, k] int32): rows that pad an expert's
     run are zeros, those from num_padded on are not written; slot_rows is -1 for a slot whose id is
     outside [0, E)."""
-    T, H = _dims(x, "x", 2)
-    code = _act(x, "x")
-    dev = x.get_device()
-    _same(x, "x", (x.dtype,), dev, (T, H))
+    code, dev, (T, H) = _matrix(x, "x")
     k = _dims(topk_ids, "topk_ids", 2)[1]
     _same(topk_ids, "topk_ids", _I32, dev, (T, k))
     R = _rows_lists(sorted_ids, num_padded, dev)
@@ -855,7 +878,7 @@ def dispatch(x, topk_ids, E: int, sorted_ids, num_padded, out=None, slot_rows=No
     else:
         _same(out, "out", (x.dtype,), dev, (R, H))
     if slot_rows is None:
-        slot_rows = _empty(topk_ids, (T, k), torch.int32, stream)
+        slot_rows = _like(topk_ids, stream)
     else:
         _same(slot_rows, "slot_rows", _I32, dev, (T, k))
     keep = (x, topk_ids, sorted_ids, num_padded, out, slot_rows)
@@ -867,17 +890,14 @@ def dispatch(x, topk_ids, E: int, sorted_ids, num_padded, out=None, slot_rows=No
 def dispatch_backward(drows, slot_rows, out=None, stream=None, prepare: bool = False):
     """moe_dispatch_backward: dx [T, H] from the gradient drows [R, H] of the rows and the slots'
     places slot_rows [T, k]; the rows of no slot are not read."""
-    R, H = _dims(drows, "drows", 2)
-    code = _act(drows, "drows")
-    dev, like = drows.get_device(), (drows.dtype,)
-    _same(drows, "drows", like, dev, (R, H))
+    code, dev, (R, H) = _matrix(drows, "drows")
     T, k = _dims(slot_rows, "slot_rows", 2)
     _same(slot_rows, "slot_rows", _I32, dev, (T, k))
     raw = _launch_stream(dev, stream)
     if out is None:
         out = _empty(drows, (T, H), drows.dtype, stream)
     else:
-        _same(out, "out", like, dev, (T, H))
+        _same(out, "out", (drows.dtype,), dev, (T, H))
     args = (drows.data_ptr(), slot_rows.data_ptr(), T, H, k, R, code, out.data_ptr(), raw)
     return _run(lib.moe_dispatch_backward, args, (drows, slot_rows, out), prepare, out)
 
@@ -887,10 +907,7 @@ def combine(rows, slot_rows, topk_weights=None, dtype=None, out=None, stream=Non
     """moe_combine: out[t] = sum_j topk_weights[t, j] * rows[slot_rows[t, j]] (weight 1 without
     topk_weights); slots without a place add nothing. rows [R, H] bfloat16 or float32, out [T, H]
     of ``dtype`` (by default the rows')."""
-    R, H = _dims(rows, "rows", 2)
-    code_r = _act(rows, "rows")
-    dev = rows.get_device()
-    _same(rows, "rows", (rows.dtype,), dev, (R, H))
+    code_r, dev, (R, H) = _matrix(rows, "rows")
     T, k = _dims(slot_rows, "slot_rows", 2)
     _same(slot_rows, "slot_rows", _I32, dev, (T, k))
     if topk_weights is not None:
@@ -915,10 +932,8 @@ def combine_backward(dout, rows, slot_rows, topk_weights, sorted_ids, num_padded
     (drows [R, H] of the rows' type, dweights [T, k] float32); topk_weights None: weight 1. Rows of
     drows that pad a run are zeros, those from num_padded on are not written; drows may be rows
     itself."""
-    T, H = _dims(dout, "dout", 2)
-    code, code_r = _act(dout, "dout"), _act(rows, "rows")
-    dev = dout.get_device()
-    _same(dout, "dout", (dout.dtype,), dev, (T, H))
+    code, dev, (T, H) = _matrix(dout, "dout")
+    code_r = _act(rows, "rows")
     k = _dims(slot_rows, "slot_rows", 2)[1]
     _same(slot_rows, "slot_rows", _I32, dev, (T, k))
     R = _rows_lists(sorted_ids, num_padded, dev)
@@ -927,7 +942,7 @@ def combine_backward(dout, rows, slot_rows, topk_weights, sorted_ids, num_padded
         _same(topk_weights, "topk_weights", _F32, dev, (T, k))
     raw = _launch_stream(dev, stream)
     if drows is None:
-        drows = _empty(rows, (R, H), rows.dtype, stream)
+        drows = _like(rows, stream)
     else:
         _same(drows, "drows", (rows.dtype,), dev, (R, H))
     if dweights is None:
@@ -947,10 +962,8 @@ def layer_norm(x, weight=None, bias=None, residual=None, alpha: float = 1.0, eps
     ``bias`` (either None: 1 and 0); residual_out = s. x, residual [T, H] bfloat16 or float32,
     weight, bias [H] float32. Returns (out, residual_out); residual_out is None (and s not stored)
     without a residual unless a buffer is given. out or residual_out may be x or residual itself."""
-    T, H = shape = _dims(x, "x", 2)
-    code = _act(x, "x")
-    dev, like = x.get_device(), (x.dtype,)
-    _same(x, "x", like, dev, shape)
+    code, dev, shape = _matrix(x, "x")
+    (T, H), like = shape, (x.dtype,)
     if weight is not None:
         _same(weight, "weight", _F32, dev, (H,))
     if bias is not None:
@@ -961,9 +974,9 @@ def layer_norm(x, weight=None, bias=None, residual=None, alpha: float = 1.0, eps
     if residual_out is not None:
         _same(residual_out, "residual_out", like, dev, shape)
     elif residual is not None:
-        residual_out = _empty(x, shape, x.dtype, stream)
+        residual_out = _like(x, stream)
     if out is None:
-        out = _empty(x, shape, x.dtype, stream)
+        out = _like(x, stream)
     else:
         _same(out, "out", like, dev, shape)
     keep = (x, residual, weight, bias, out, residual_out)
@@ -984,10 +997,8 @@ def layer_norm_backward(dout, s, weight=None, dresidual_out=None, alpha: float =
     dweight, dbias): dx = alpha * ds; dresidual = ds, None without dresidual_out unless a buffer is
     given; dweight [H] float32, None without a weight unless a buffer is given; dbias [H] float32.
     dx or dresidual may be dout, s or dresidual_out itself."""
-    T, H = shape = _dims(dout, "dout", 2)
-    code = _act(dout, "dout")
-    dev, like = dout.get_device(), (dout.dtype,)
-    _same(dout, "dout", like, dev, shape)
+    code, dev, shape = _matrix(dout, "dout")
+    (T, H), like = shape, (dout.dtype,)
     _same(s, "s", like, dev, shape)
     if weight is not None:
         _same(weight, "weight", _F32, dev, (H,))
@@ -997,17 +1008,17 @@ def layer_norm_backward(dout, s, weight=None, dresidual_out=None, alpha: float =
     if dresidual is not None:
         _same(dresidual, "dresidual", like, dev, shape)
     elif dresidual_out is not None:
-        dresidual = _empty(dout, shape, dout.dtype, stream)
+        dresidual = _like(dout, stream)
     if dx is None:
-        dx = _empty(dout, shape, dout.dtype, stream)
+        dx = _like(dout, stream)
     else:
         _same(dx, "dx", like, dev, shape)
     if dweight is not None:
         _same(dweight, "dweight", _F32, dev, (H,))
     elif weight is not None:
-        dweight = _empty(dout, (H,), torch.float32, stream)
+        dweight = _like(weight, stream)
     if dbias is None:
-        dbias = _empty(dout, (H,), torch.float32, stream)
+        dbias = _empty(dout, (H,), torch.float32, stream) if weight is None else _like(weight, stream)
     else:
         _same(dbias, "dbias", _F32, dev, (H,))
     need = layer_norm_backward_workspace_bytes(T, H)

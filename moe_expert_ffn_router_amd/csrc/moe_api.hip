@@ -723,7 +723,7 @@ static moe_status check_linear(int T, int N, int K, int gated, int dtype) {
 
 MOE_EXPORT size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype) {
   if (check_linear(T, N, K, gated, dtype) != MOE_OK) return 0;
-  return moe::linear_workspace_bytes(T, N, K, gated != 0, dtype);
+  return moe::linear_workspace_bytes(moe::linear_plan(T, N, K, gated != 0, dtype), T, N, gated != 0);
 }
 
 MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias,
@@ -740,7 +740,8 @@ MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const
   if (ldo < (size_t)N || ldo > INT_MAX || (residual && (ldr < (size_t)N || ldr > INT_MAX)))
     return MOE_ERR_SHAPE;
   if (T == 0) return MOE_OK;
-  const size_t used = moe::linear_workspace_bytes(T, N, K, gated != 0, dtype);
+  const moe::LinearPlan plan = moe::linear_plan(T, N, K, gated != 0, dtype);
+  const size_t used = moe::linear_workspace_bytes(plan, T, N, gated != 0);
   if (!x || !w || !out || (used && !workspace)) return MOE_ERR_NULL;
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 4) || !aligned(residual, ob) ||
       !aligned(out, ob) || (used && !aligned(workspace, 256)))
@@ -764,5 +765,5 @@ MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const
   return hip_status(moe::launch_linear(
       moe::LinearProblem{x, ldx, w, bias, activation, gated != 0, residual, ldr, T, N, K, dtype,
                          out_dtype, workspace, out, ldo, by_four},
-      (hipStream_t)stream));
+      plan, (hipStream_t)stream));
 }

@@ -249,7 +249,14 @@ struct LayerNormBackwardProblem {
 size_t layer_norm_backward_workspace_bytes(int T, int H);
 hipError_t launch_layer_norm_backward(const LayerNormBackwardProblem& p, hipStream_t stream);
 
-// Matrix product with bias, activation and residual (moe_linear.hip).
+// Matrix product with bias, activation and residual (moe_linear.hip). Which kernel a call runs:
+// the few-rows kernel with a x b tiles of r rows, or the tile kernel with a x b and K in `parts`.
+struct LinearPlan {
+  bool few;
+  int a, b, r, parts;
+};
+LinearPlan linear_plan(int T, int N, int K, bool gated, int dtype);
+size_t linear_workspace_bytes(const LinearPlan& plan, int T, int N, bool gated);
 struct LinearProblem {
   const void* x;
   size_t ldx;
@@ -264,7 +271,6 @@ struct LinearProblem {
   size_t ldo;
   bool by_four;  // four columns of out and residual from a multiple of four on are aligned
 };
-size_t linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
-hipError_t launch_linear(const LinearProblem& p, hipStream_t stream);
+hipError_t launch_linear(const LinearProblem& p, const LinearPlan& plan, hipStream_t stream);
 
 }  // namespace moe

@@ -672,13 +672,6 @@ struct Int {
   static constexpr int value = V;
 };
 
-// Which kernel a call runs: the few-rows kernel with mt x nt tiles of r rows, or the tile
-// kernel with mi x ni and K in `parts`.
-struct Plan {
-  bool few;
-  int a, b, r;  // few: mt, nt, r; tiles: mi, ni
-  int parts;
-};
 struct TileCost {
   int mi, ni;
   float fixed, alone, full;  // us: of a tile beside its stages; of a stage, one tile and all CUs
@@ -706,12 +699,12 @@ static const FewCost kFew[] = {{1, 1, 8, 1.15f}, {1, 1, 16, 1.f}, {1, 2, 16, 0.f
                                {2, 1, 16, 1.f}, {2, 2, 16, 0.f}, {4, 1, 16, 1.8f}};
 constexpr int kCus = 256;
 
-static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
+static LinearPlan plan_of(int T, int N, int K, bool gated, int dtype) {
   const bool f32 = dtype == MOE_DTYPE_F32;
   const int size = f32 ? 4 : 2, half = gated ? 2 : 1;
-  Plan best{};
+  LinearPlan best{};
   float least = 3.0e38f;
-  auto take = [&](float t, const Plan& p) {
+  auto take = [&](float t, const LinearPlan& p) {
     if (t < least) {
       least = t;
       best = p;
@@ -725,7 +718,7 @@ static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
     const float all = w * std::min<long>(tiles, kCus) / (f32 ? 6000.f : 7500.f);
     const float round = std::max(w / 90.f, all) + x / 140.f;
     take(2.5f + (float)((tiles + kCus - 1) / kCus) * round * (f32 ? f.f32 : 1.f),
-         Plan{true, f.mt, f.nt, f.r, 1});
+         LinearPlan{true, f.mt, f.nt, f.r, 1});
   }
   const int stages = (K * size + 127) / 128;
   auto price = [&](const TileCost& c) {
@@ -738,7 +731,7 @@ static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
       float t = 2.5f + whole * (c.fixed - 2.5f + n * c.full);
       if (part > 0) t += c.fixed - 2.5f + n * (c.alone + (c.full - c.alone) * part);
       if (parts > 1) t += 3.2f + 2e-6f * parts * T * ((float)N * half);  // 8 bytes at 4 TB/s
-      take(t, Plan{false, c.mi, c.ni, 0, parts});
+      take(t, LinearPlan{false, c.mi, c.ni, 0, parts});
       if (groups > 2 * kCus) break;  // more parts: more rounds
     }
   };
@@ -751,9 +744,8 @@ static Plan plan_of(int T, int N, int K, bool gated, int dtype) {
 }
 
 template <bool GATED, typename T, typename OT>
-static void dispatch(const LinearProblem& p, hipStream_t stream) {
+static void dispatch(const LinearProblem& p, const LinearPlan& plan, hipStream_t stream) {
   constexpr bool kF32 = sizeof(T) == 4;
-  const Plan plan = plan_of(p.T, p.N, p.K, GATED, kF32 ? MOE_DTYPE_F32 : MOE_DTYPE_BF16);
   auto tiles = [&](auto mi, auto ni) {
     constexpr int MI = decltype(mi)::value, NI = decltype(ni)::value;
     if (!plan.few && plan.a == MI && plan.b == NI)
@@ -787,25 +779,29 @@ static void dispatch(const LinearProblem& p, hipStream_t stream) {
 
 }  // namespace linear
 
-size_t linear_workspace_bytes(int T, int N, int K, int gated, int dtype) {
-  const linear::Plan plan = linear::plan_of(T, N, K, gated, dtype);
+LinearPlan linear_plan(int T, int N, int K, bool gated, int dtype) {
+  return linear::plan_of(T, N, K, gated, dtype);
+}
+
+size_t linear_workspace_bytes(const LinearPlan& plan, int T, int N, bool gated) {
   if (plan.few || plan.parts == 1) return 0;
   const size_t n = (size_t)(N + 3) / 4 * 4 * (gated ? 2 : 1);
   return (plan.parts * T * n * sizeof(float) + 255) / 256 * 256;
 }
 
-hipError_t launch_linear(const LinearProblem& p, hipStream_t stream) {
+hipError_t launch_linear(const LinearProblem& p, const LinearPlan& plan, hipStream_t stream) {
   using namespace linear;
   const bool b = p.dtype == MOE_DTYPE_BF16, ob = p.out_dtype == MOE_DTYPE_BF16;
   if (p.gated) {
-    if (b) ob ? dispatch<true, uint16_t, uint16_t>(p, stream)
-              : dispatch<true, uint16_t, float>(p, stream);
-    else ob ? dispatch<true, float, uint16_t>(p, stream) : dispatch<true, float, float>(p, stream);
+    if (b) ob ? dispatch<true, uint16_t, uint16_t>(p, plan, stream)
+              : dispatch<true, uint16_t, float>(p, plan, stream);
+    else ob ? dispatch<true, float, uint16_t>(p, plan, stream)
+            : dispatch<true, float, float>(p, plan, stream);
   } else {
-    if (b) ob ? dispatch<false, uint16_t, uint16_t>(p, stream)
-              : dispatch<false, uint16_t, float>(p, stream);
-    else ob ? dispatch<false, float, uint16_t>(p, stream)
-            : dispatch<false, float, float>(p, stream);
+    if (b) ob ? dispatch<false, uint16_t, uint16_t>(p, plan, stream)
+              : dispatch<false, uint16_t, float>(p, plan, stream);
+    else ob ? dispatch<false, float, uint16_t>(p, plan, stream)
+            : dispatch<false, float, float>(p, plan, stream);
   }
   return hipGetLastError();
 }
