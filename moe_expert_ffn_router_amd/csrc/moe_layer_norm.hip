@@ -114,10 +114,11 @@ __device__ __forceinline__ void row_sums(float& a, float& b, f32x2* slot) {
 
 // A worker of W waves takes the rows w, w + workers, ... . W > 1: it is a workgroup; W = 1:
 // 16 of them are one. At the end a workgroup's sums for the weight and the bias (16 workers'
-// added up in LDS, in order) go to partial[workgroup] ([2, H]). The slots of the two sums over
-// a row are each written again only past the other's barrier, when all have read them. (Two
-// workers of 8 waves to a workgroup, for half the partials, hold each other up at the
-// barriers: 41.4 us instead of 38.8 for 4096 x 4096 bf16.)
+// side by side in LDS, added up in order) go to partial[workgroup] ([2, H]), or are the
+// gradients where it is the only one. The slots of the two sums over a row are each written
+// again only past the other's barrier, when all have read them. (Two workers of 8 waves to a
+// workgroup, for half the partials, hold each other up at the barriers: 41.4 us instead of
+// 38.8 for 4096 x 4096 bf16.)
 template <int W>
 constexpr int group_waves() {
   return W == 1 ? 16 : W;
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(group_waves<W>() * 64) void backward_kernel(
     LayerNormBackwardProblem p) {
   constexpr int kWorkers = group_waves<W>() / W, kLength = W * 64 * NV * VEC;
   __shared__ f32x2 red[2][W];
-  __shared__ float sums[2][kWorkers > 1 ? kLength : 1];
+  __shared__ __attribute__((aligned(16))) float sums[2][kWorkers][kWorkers > 1 ? kLength : 1];
   const int mine = kWorkers == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Span<W, NV, VEC, ANY> c(p.H, threadIdx.x - mine * 64);
   Vec<float, VEC> w[NV];
@@ -192,29 +193,36 @@ __global__ __launch_bounds__(group_waves<W>() * 64) void backward_kernel(
     }
   }
   if (!p.dweight && !p.dbias) return;
-  float* to = p.partial + (size_t)blockIdx.x * 2 * p.H;
+  float* to_w = p.partial + (size_t)blockIdx.x * 2 * p.H;
+  float* to_b = to_w + p.H;
+  if (gridDim.x == 1) {
+    to_w = p.dweight;
+    to_b = p.dbias;
+  }
   if constexpr (kWorkers > 1) {
-    for (int t = 0; t < kWorkers; ++t) {
-      __syncthreads();
-      if (t != mine) continue;
+    // a lane's vectors where it has them among the 64 lanes', what is another's as zeros
+    const int me = (threadIdx.x - mine * 64) * VEC;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-          if (!c.has(i, q)) continue;
-          const int at = c.at[i] + q;
-          sums[0][at] = t ? sums[0][at] + dw[i][q] : dw[i][q];
-          sums[1][at] = t ? sums[1][at] + db[i][q] : db[i][q];
-        }
+    for (int i = 0; i < NV; ++i) {
+      store_vec<float, VEC>(&sums[0][mine][me + i * 64 * VEC], dw[i]);
+      store_vec<float, VEC>(&sums[1][mine][me + i * 64 * VEC], db[i]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x)
-      to[i] = i < p.H ? sums[0][i] : sums[1][i - p.H];
+    const int last = (p.H - 1) / VEC * VEC;  // the vector that ends with the row is kept here
+    for (int i = threadIdx.x; i < 2 * p.H; i += blockDim.x) {
+      const int half = i >= p.H, col = i - half * p.H;
+      const int at = ANY && col >= last ? col - (p.H - VEC) + last : col;
+      float v = 0.f;
+#pragma unroll
+      for (int t = 0; t < kWorkers; ++t) v += sums[half][t][at];
+      float* to = half ? to_b : to_w;
+      if (to) to[col] = v;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      c.store(i, to, dw[i]);
-      c.store(i, to + p.H, db[i]);
+      if (to_w) c.store(i, to_w, dw[i]);
+      if (to_b) c.store(i, to_b, db[i]);
     }
   }
 }
@@ -244,12 +252,15 @@ __global__ __launch_bounds__(1024) void finish_kernel(const float* __restrict__ 
   }
 }
 
-// Calls f(W, NV) as compile-time constants for rows of H elements.
+// Calls f(W, NV) as compile-time constants for rows of H elements. The longest rows of the
+// backward pass (BACK) take 8 waves: 16 leave a wave 128 registers, from which some of a
+// row spills (4096 x 16384 bf16 202 us instead of 149, 2048 x 16384 fp32 180 instead
+// of 169).
 template <int V>
 struct Int {
   static constexpr int value = V;
 };
-template <int VEC, typename F>
+template <int VEC, bool BACK, typename F>
 static void by_row_length(int H, F f) {
   const int vecs = (H + VEC - 1) / VEC;
   if (VEC == 1 || vecs <= 64) {
@@ -259,7 +270,10 @@ static void by_row_length(int H, F f) {
     else if (vecs <= 256) f(Int<4>{}, Int<1>{});
     else if (vecs <= 512) f(Int<8>{}, Int<1>{});
     else if (vecs <= 1024) f(Int<8>{}, Int<2>{});
-    else if (VEC == 8 || vecs <= 2048) f(Int<16>{}, Int<2>{});
+    else if constexpr (BACK) {
+      if (VEC == 8 || vecs <= 2048) f(Int<8>{}, Int<4>{});
+      else if constexpr (VEC == 4) f(Int<8>{}, Int<8>{});
+    } else if (VEC == 8 || vecs <= 2048) f(Int<16>{}, Int<2>{});
     else if constexpr (VEC == 4) f(Int<16>{}, Int<4>{});
   }
 }
@@ -288,7 +302,9 @@ static void by_type(int H, int dtype, std::initializer_list<const void*> ptrs, F
 // More of them keep more rows in flight, fewer have fewer sums to write and add up (2 H floats
 // each): an eighth of the rows, at least 256 and at most what these measured (us, bf16): 8192
 // x 2048 256 36.9, 512 28.1, 768 27.4; 4096 x 4096 256 40.1, 512 38.8, 768 45.7; 1000 x 4096 256
-// 15.9, 512 19.6; 8192 x 7168 256 121, 512 129. Rows of one wave: 8192 x 1024 24.5 with 256.
+// 15.9, 512 19.6; 8192 x 7168 256 121, 512 129. Rows of one wave: a wave for each as far as 256
+// workgroups go, one workgroup alone up to 16 rows (with 64, four to a wave, 64 x 512 took 8.7
+// instead of 5.8 with a second kernel).
 static int partials_of(int T, int H, int dtype) {
   const int vec = dtype == MOE_DTYPE_BF16 ? 8 : 4, vecs = (H + vec - 1) / vec;
   if (H < vec || vecs <= 128) return std::min((T + 15) / 16, 256);
@@ -309,7 +325,7 @@ hipError_t launch_layer_norm(const LayerNormProblem& p, hipStream_t stream) {
   by_type(p.H, p.dtype, {p.x, p.residual, p.weight, p.bias, p.residual_out, p.out},
           [&](auto v, auto any, auto io) {
             constexpr int VEC = decltype(v)::value;
-            by_row_length<VEC>(p.H, [&](auto w, auto nv) {
+            by_row_length<VEC, false>(p.H, [&](auto w, auto nv) {
               constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
               forward_kernel<W, NV, VEC, decltype(any)::value != 0, decltype(io)>
                   <<<grid_of<W>(p.T), W == 1 ? 256 : W * 64, 0, stream>>>(p);
@@ -322,10 +338,13 @@ hipError_t launch_layer_norm_backward(const LayerNormBackwardProblem& p, hipStre
   using namespace layer_norm;
   const int partials = partials_of(p.T, p.H, p.dtype);
   if (p.T > 0) {
-    by_type(p.H, p.dtype, {p.dout, p.s, p.weight, p.dresidual_out, p.dx, p.dresidual},
+    const bool alone = partials == 1;
+    by_type(p.H, p.dtype,
+            {p.dout, p.s, p.weight, p.dresidual_out, p.dx, p.dresidual,
+             alone ? p.dweight : nullptr, alone ? p.dbias : nullptr},
             [&](auto v, auto any, auto io) {
               constexpr int VEC = decltype(v)::value;
-              by_row_length<VEC>(p.H, [&](auto w, auto nv) {
+              by_row_length<VEC, true>(p.H, [&](auto w, auto nv) {
                 constexpr int W = decltype(w)::value, NV = decltype(nv)::value;
                 backward_kernel<W, NV, VEC, decltype(any)::value != 0, decltype(io)>
                     <<<partials, group_waves<W>() * 64, 0, stream>>>(p);
@@ -334,7 +353,7 @@ hipError_t launch_layer_norm_backward(const LayerNormBackwardProblem& p, hipStre
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (p.dweight || p.dbias)
+  if (partials != 1 && (p.dweight || p.dbias))
     finish_kernel<<<dim3((p.H + 31) / 32, 2), 1024, 0, stream>>>(p.partial, partials, p.H,
                                                                 p.dweight, p.dbias);
   return hipGetLastError();

@@ -21,7 +21,8 @@ SHAPES = [(1, 8, "bf16"), (3, 512, "bf16"), (2, 520, "bf16"), (9, 1024, "bf16"),
           (1, 16383, "bf16"), (7, 256, "f32"), (2, 1028, "f32"), (2, 4100, "f32"), (2, 8192, "f32"),
           (1, 8196, "f32"), (2, 16384, "f32"), (3, 777, "f32"), (1, 3, "f32"), (2, 16381, "f32"),
           (300, 64, "bf16"), (65, 4096, "bf16"), (515, 200, "f32"), (1030, 72, "bf16"),
-          (777, 1031, "f32"), (2100, 136, "bf16")]
+          (777, 1031, "f32"), (2100, 136, "bf16"), (40, 12288, "bf16"), (270, 9001, "bf16"),
+          (33, 9001, "f32")]
 
 
 def forward_error(s, e_s, w, b, eps):
@@ -133,6 +134,35 @@ def test_backward(T, H, dtype):
     got = moe().layer_norm_backward(dout, s, eps=1e-2)
     assert got[1] is None and got[2] is None
     check_backward(dout, s, None, None, 1.0, 1e-2, got, dtype)
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 40, 257])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sums_over_rows(T, dtype):
+    """One workgroup or several, rows of one wave or of more, and gradients of weight and bias off
+    the 16-byte grid, each with and without the other."""
+    say(f"layer_norm_backward: sums T={T} {dtype}")
+    m = moe()
+    for H in (5, 9, 64, 257, 509, 512, 1000, 1023, 1032, 2056, 4099, 9000):
+        g = gen(T + H)
+        s, dout, w = rand(g, T, H, dtype=dtype, std=2.0), rand(g, T, H, dtype=dtype), rand(g, H)
+        ref = m.layer_norm_backward(dout, s, w, eps=EPS)
+        check_backward(dout, s, w, None, 1.0, EPS, ref, dtype)
+        off = torch.full((2, H + 2), 12345.0, device="cuda")
+        m.layer_norm_backward(dout, s, w, eps=EPS, dweight=off[0, 1:H + 1], dbias=off[1, 1:H + 1])
+        assert torch.equal(off[0, 1:H + 1], ref[2]) and torch.equal(off[1, 1:H + 1], ref[3])
+        assert bool((off[:, [0, H + 1]] == 12345.0).all())
+        ws = torch.empty(m.layer_norm_backward_workspace_bytes(T, H), dtype=torch.uint8,
+                         device="cuda")
+        for only in (0, 1):
+            one = torch.full((H,), 12345.0, device="cuda")
+            dx = torch.empty_like(dout)
+            to = [one.data_ptr() if i == only else None for i in (0, 1)]
+            status = m.lib.moe_layer_norm_backward(
+                dout.data_ptr(), s.data_ptr(), w.data_ptr(), None, 1.0, EPS, T, H,
+                {"bf16": 1, "f32": 0}[dtype], dx.data_ptr(), None, *to, ws.data_ptr(), ws.numel(),
+                torch.cuda.current_stream().cuda_stream)
+            assert status == 0 and torch.equal(one, ref[2 + only]) and torch.equal(dx, ref[0])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
