@@ -759,11 +759,8 @@ MOE_EXPORT moe_status moe_linear(const void* x, size_t ldx, const void* w, const
   if (used && (meets(ws.p, ws.n, {vecs[0], vecs[1]}) || rows_meet(x, ldx * b, K * b, T, ws) ||
                (residual && rows_meet(residual, ldrb, N * ob, T, ws))))
     return MOE_ERR_UNSUPPORTED;
-  const size_t four = 4 * ob;
-  const bool by_four = N % 4 == 0 && ldo % 4 == 0 && aligned(out, four) &&
-                       (!residual || (ldr % 4 == 0 && aligned(residual, four)));
   return hip_status(moe::launch_linear(
       moe::LinearProblem{x, ldx, w, bias, activation, gated != 0, residual, ldr, T, N, K, dtype,
-                         out_dtype, workspace, out, ldo, by_four},
+                         out_dtype, workspace, out, ldo},
       plan, (hipStream_t)stream));
 }

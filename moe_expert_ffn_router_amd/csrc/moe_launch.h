@@ -269,7 +269,6 @@ struct LinearProblem {
   void* workspace;
   void* out;
   size_t ldo;
-  bool by_four;  // four columns of out and residual from a multiple of four on are aligned
 };
 hipError_t launch_linear(const LinearProblem& p, const LinearPlan& plan, hipStream_t stream);
 

@@ -99,14 +99,17 @@ __device__ __forceinline__ void activate(int act, f32x4 (&v)[N]) {
     });
 }
 
-// Four consecutive values of out or residual as they are in memory.
+// Four consecutive values of out or residual as they are in memory, where they need not start
+// at a multiple of more than their type.
 template <typename OT>
 struct Four {
   typedef u32x2 type;
+  typedef type any __attribute__((aligned(2)));
 };
 template <>
 struct Four<float> {
   typedef f32x4 type;
+  typedef type any __attribute__((aligned(4)));
 };
 __device__ __forceinline__ f32x4 value(const u32x2& r) {
   return f32x4{__uint_as_float(r[0] << 16), __uint_as_float(r[0] & 0xffff0000u),
@@ -114,9 +117,9 @@ __device__ __forceinline__ f32x4 value(const u32x2& r) {
 }
 __device__ __forceinline__ f32x4 value(const f32x4& r) { return r; }
 __device__ __forceinline__ void store_four(uint16_t* p, f32x4 v) {
-  *(u32x2*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  *(Four<uint16_t>::any*)p = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
-__device__ __forceinline__ void store_four(float* p, f32x4 v) { *(f32x4*)p = v; }
+__device__ __forceinline__ void store_four(float* p, f32x4 v) { *(Four<float>::any*)p = v; }
 __device__ __forceinline__ float load_one(const uint16_t* p) { return bf16_bits_to_f32(*p); }
 __device__ __forceinline__ float load_one(const float* p) { return *p; }
 __device__ __forceinline__ void store_one(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, v); }
@@ -126,9 +129,11 @@ __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 template <bool GATED, typename OT>
 struct Columns {
   int n;
+  bool whole;  // N cuts none of the fours of the wave, nor is it less than four
   f32x4 bias, up_bias;
 
-  __device__ __forceinline__ Columns(const LinearProblem& p, int n) : n(n), bias{}, up_bias{} {
+  __device__ __forceinline__ Columns(const LinearProblem& p, int n)
+      : n(n), whole(p.N >= 4 && __ballot(n < p.N && n + 4 > p.N) == 0), bias{}, up_bias{} {
     if (!p.bias || n >= p.N) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -151,16 +156,16 @@ struct Columns {
     }
   }
   // What residual holds of rows m(i), ahead of their sums: loads that nothing waits for yet
-  // (those past the ends from inside, never used). Only where p.by_four.
+  // (those past the ends from inside, never used). Only where the fours are whole.
   template <int R, typename F>
   __device__ __forceinline__ void fetch(const LinearProblem& p, F m,
                                         typename Four<OT>::type (&raw)[R]) const {
-    if (!p.residual || !p.by_four) return;
+    if (!p.residual || !whole) return;
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      raw[i] = *(const typename Four<OT>::type*)((const OT*)p.residual +
-                                                 (size_t)min(m(i), p.T - 1) * p.ldr +
-                                                 min(n, p.N - 4));
+      raw[i] = *(const typename Four<OT>::any*)((const OT*)p.residual +
+                                                (size_t)min(m(i), p.T - 1) * p.ldr +
+                                                min(n, p.N - 4));
   }
   // Rows m(i) of them from their sums (and, gated, those of the up rows) and what fetch has
   // brought. m(i) >= T: none.
@@ -175,7 +180,7 @@ struct Columns {
 #pragma unroll
       for (int i = 0; i < R; ++i) v[i] *= up[i] + up_bias;
     }
-    if (p.by_four) {
+    if (whole) {
       if (p.residual) {
 #pragma unroll
         for (int i = 0; i < R; ++i) v[i] += value(raw[i]);
