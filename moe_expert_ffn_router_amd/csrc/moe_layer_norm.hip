@@ -11,8 +11,8 @@
 // once, for a second kernel that adds the workgroups' in a fixed order. Bound by HBM, small
 // calls by their launches. Measured (captured into a graph), bf16 with residual: forward 16 x
 // 4096 2.5 us, 4096 x 4096 22.7 us = 5.9 TB/s; backward 4096 x 4096 39 us (35 = 5.2 TB/s with its
-// 16 MB of sums, and 4 the second kernel), 8192 x 7168 120 us = 4.9 TB/s, 100 x 4096 7.6 us; fp32
-// 777 x 1031 forward 3.7 us, backward 11.
+// 16 MB of sums, and 4 the second kernel), 8192 x 7168 120 us = 4.9 TB/s, 4096 x 16384 149, 8192 x
+// 1024 18, 100 x 4096 7.6, 16 x 512 3.6; fp32 777 x 1031 forward 3.7 us, backward 11.
 #include <algorithm>
 
 #include "../../include/moe.h"
