@@ -1044,12 +1044,16 @@ def linear(x, w, bias=None, activation: int = ACT_NONE, gated: bool = False, res
     and w bfloat16 or float32 (the same), bias float32, activation ACT_*; residual and out of
     ``dtype`` (by default the residual's, else x's). x, residual and out may be column slices of
     wider matrices; out may be residual itself."""
-    T, K = _dims(x, "x", 2)
-    n = _dims(w, "w", 2)[0]
-    code = _act(x, "x")
-    dev = x.get_device()
-    ldx = _need_rows(x, "x", (x.dtype,))
-    _same(w, "w", (x.dtype,), dev, (n, K))
+    if isinstance(x, torch.Tensor) and x.is_contiguous():
+        code, dev, (T, K) = _matrix(x, "x")
+        ldx = K
+    else:
+        T, K = _dims(x, "x", 2)
+        code, dev = _act(x, "x"), x.get_device()
+        ldx = _need_rows(x, "x", (x.dtype,))
+    wcode, wdev, (n, wk) = _matrix(w, "w")
+    if wcode != code or wdev != dev or wk != K:
+        _same(w, "w", (x.dtype,), dev, (n, K))
     if gated and n % 2:
         raise ValueError(f"w has shape {tuple(w.shape)}, expected [2 N, K={K}]")
     N = n // 2 if gated else n
