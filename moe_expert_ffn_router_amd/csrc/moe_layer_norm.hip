@@ -12,7 +12,7 @@
 // calls by their launches. Measured (captured into a graph), bf16 with residual: forward 16 x
 // 4096 2.5 us, 4096 x 4096 22.7 us = 5.9 TB/s; backward 4096 x 4096 39 us (35 = 5.2 TB/s with its
 // 16 MB of sums, and 4 the second kernel), 8192 x 7168 120 us = 4.9 TB/s, 4096 x 16384 149, 8192 x
-// 1024 18, 100 x 4096 7.6, 16 x 512 3.6; fp32 777 x 1031 forward 3.7 us, backward 11.
+// 1024 18, 100 x 4096 7.6, 16 x 512 3.6; fp32 777 x 1031 forward 3.1 us, backward 11.
 #include <algorithm>
 
 #include "../../include/moe.h"
@@ -252,10 +252,11 @@ __global__ __launch_bounds__(1024) void finish_kernel(const float* __restrict__ 
   }
 }
 
-// Calls f(W, NV) as compile-time constants for rows of H elements. The longest rows of the
-// backward pass (BACK) take 8 waves: 16 leave a wave 128 registers, from which some of a
-// row spills (4096 x 16384 bf16 202 us instead of 149, 2048 x 16384 fp32 180 instead
-// of 169).
+// Calls f(W, NV) as compile-time constants for rows of H elements: up to 8 waves with a vector a
+// lane, as few as hold the row (of 4 and 8 alone 4096 x 2560 bf16 took 17.1 us forward and
+// 28.5 backward instead of 16.4 and 26.2). The longest rows of the backward pass (BACK) take 8
+// waves: 16 leave a wave 128 registers, from which some of a row spills (4096 x 16384 bf16 202
+// us instead of 149, 2048 x 16384 fp32 180 instead of 169).
 template <int V>
 struct Int {
   static constexpr int value = V;
@@ -267,7 +268,11 @@ static void by_row_length(int H, F f) {
     f(Int<1>{}, Int<1>{});
   } else if constexpr (VEC > 1) {
     if (vecs <= 128) f(Int<1>{}, Int<2>{});
+    else if (vecs <= 192) f(Int<3>{}, Int<1>{});
     else if (vecs <= 256) f(Int<4>{}, Int<1>{});
+    else if (vecs <= 320) f(Int<5>{}, Int<1>{});
+    else if (vecs <= 384) f(Int<6>{}, Int<1>{});
+    else if (vecs <= 448) f(Int<7>{}, Int<1>{});
     else if (vecs <= 512) f(Int<8>{}, Int<1>{});
     else if (vecs <= 1024) f(Int<8>{}, Int<2>{});
     else if constexpr (BACK) {
@@ -300,16 +305,17 @@ static void by_type(int H, int dtype, std::initializer_list<const void*> ptrs, F
 
 // Workgroups of the backward pass for rows of H elements.
 // More of them keep more rows in flight, fewer have fewer sums to write and add up (2 H floats
-// each): an eighth of the rows, at least 256 and at most what these measured (us, bf16): 8192
-// x 2048 256 36.9, 512 28.1, 768 27.4; 4096 x 4096 256 40.1, 512 38.8, 768 45.7; 1000 x 4096 256
-// 15.9, 512 19.6; 8192 x 7168 256 121, 512 129. Rows of one wave: a wave for each as far as 256
-// workgroups go, one workgroup alone up to 16 rows (with 64, four to a wave, 64 x 512 took 8.7
-// instead of 5.8 with a second kernel).
+// each): a quarter of the rows (an eighth: 2385 x 1704 17.9 us instead of 16.5, 5446 x 1168 22.1
+// instead of 20.2), at least 256 and at most what these measured (us, bf16): 8192 x 2048 256
+// 36.9, 512 28.1, 768 27.4; 4096 x 4096 256 40.1, 512 38.8, 768 45.7; 1000 x 4096 256 15.9, 512
+// 19.6; 8192 x 7168 256 121, 512 129. Rows of one wave: a wave for each as far as 256 workgroups
+// go, one workgroup alone up to 16 rows (with 64, four to a wave, 64 x 512 took 8.7 instead of
+// 5.8 with a second kernel).
 static int partials_of(int T, int H, int dtype) {
   const int vec = dtype == MOE_DTYPE_BF16 ? 8 : 4, vecs = (H + vec - 1) / vec;
   if (H < vec || vecs <= 128) return std::min((T + 15) / 16, 256);
   const int most = vecs <= 256 ? 768 : vecs <= 512 ? 512 : 256;
-  return std::min(T, std::min(std::max(T / 8, 256), most));
+  return std::min(T, std::min(std::max(T / 4, 256), most));
 }
 
 }  // namespace layer_norm

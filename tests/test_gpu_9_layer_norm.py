@@ -22,7 +22,8 @@ SHAPES = [(1, 8, "bf16"), (3, 512, "bf16"), (2, 520, "bf16"), (9, 1024, "bf16"),
           (1, 8196, "f32"), (2, 16384, "f32"), (3, 777, "f32"), (1, 3, "f32"), (2, 16381, "f32"),
           (300, 64, "bf16"), (65, 4096, "bf16"), (515, 200, "f32"), (1030, 72, "bf16"),
           (777, 1031, "f32"), (2100, 136, "bf16"), (40, 12288, "bf16"), (270, 9001, "bf16"),
-          (33, 9001, "f32")]
+          (33, 9001, "f32"), (600, 1500, "bf16"), (1100, 2500, "bf16"), (70, 3000, "bf16"),
+          (40, 3500, "bf16"), (50, 750, "f32"), (45, 1249, "f32"), (30, 1533, "f32"), (20, 1790, "f32")]
 
 
 def forward_error(s, e_s, w, b, eps):
