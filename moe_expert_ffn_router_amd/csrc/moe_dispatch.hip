@@ -203,7 +203,8 @@ __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
       }
       Vec<YT, VEC> r[kBatch];
 #pragma unroll
-      for (int q = 0; q < kBatch; ++q) r[q] = load_vec<YT, VEC, NT, ANY>(y + (size_t)row[q] * H + col);
+      for (int q = 0; q < kBatch; ++q)
+        r[q] = load_vec<YT, VEC, NT, ANY>(y + (size_t)row[q] * H + col);
 #pragma unroll
       for (int q = 0; q < kBatch; ++q) {
         keep_vec<YT, VEC>(r[q], keep[q]);
@@ -215,10 +216,9 @@ __global__ __launch_bounds__(256) void combine_kernel(const YT* __restrict__ y,
   if (c < H) store_vec<IO, VEC, false, ANY>(out + (size_t)t * H + col, v);
 }
 
-// The combine's gradient. One wave per slot (the first S waves): its row of the gradient and its weight's, the
-// dot product of the token's gradient with the row; then a wave for every 8 places:
-// zeros in those that pad a run.
-// kPiece: vectors of a lane in flight.
+// The combine's gradient. One wave per slot (the first S waves): its row of the gradient and its
+// weight's, the dot product of the token's gradient with the row; then a wave for every 8
+// places: zeros in those that pad a run. kPiece: vectors of a lane in flight.
 template <int VEC, bool ANY, int kPiece, bool NT, typename YT, typename IO>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBackwardProblem p) {
   const int w = my_wave(), lane = threadIdx.x & 63, S = p.T * p.k;
@@ -377,9 +377,11 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
 
 hipError_t launch_combine(const CombineProblem& p, hipStream_t stream) {
   using namespace dispatch;
-  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.rows, p.out}), [&](auto v, auto any, auto y, auto io) {
-    run_combine<decltype(v)::value, decltype(any)::value != 0, decltype(y), decltype(io)>(p, stream);
-  });
+  by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.rows, p.out}),
+          [&](auto v, auto any, auto y, auto io) {
+            run_combine<decltype(v)::value, decltype(any)::value != 0, decltype(y), decltype(io)>(
+                p, stream);
+          });
   return hipGetLastError();
 }
 
@@ -387,8 +389,8 @@ hipError_t launch_combine_backward(const CombineBackwardProblem& p, hipStream_t 
   using namespace dispatch;
   by_type(p.rows_dtype, p.dtype, p.H, aligned16({p.dout, p.rows, p.drows}),
           [&](auto v, auto any, auto y, auto io) {
-            run_combine_backward<decltype(v)::value, decltype(any)::value != 0, decltype(y), decltype(io)>(
-                p, stream);
+            run_combine_backward<decltype(v)::value, decltype(any)::value != 0, decltype(y),
+                                 decltype(io)>(p, stream);
           });
   return hipGetLastError();
 }
