@@ -151,7 +151,9 @@ __global__ __launch_bounds__(256) void tokens_kernel(const P* __restrict__ x, Li
     }
     return;
   }
-  for (int c = lane; c < words.count; c += 64 * kCopy) {
+  // The lanes go on together, those past the row's end too: each brings a slot's place.
+  for (int c0 = 0; c0 < words.count; c0 += 64 * kCopy) {
+    const int c = c0 + lane;
     typename W::Word v[kCopy];
     load_piece(words.at(x, w), c, words, v);
     for (int j0 = 0; j0 < k; j0 += 64) {

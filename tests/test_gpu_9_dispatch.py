@@ -317,3 +317,40 @@ def test_offsets_past_32_bits():
     assert torch.equal(out[-4:].float(), rows[at[-4:, 0].long()].float() * 0.5)
     drows, dw = m.combine_backward(out, rows, at, w, sid, npad, drows=rows)
     assert torch.equal(drows[at[-4:, 0].long()].float(), out[-4:].float() * 0.5)
+
+
+# T, k, H, dtype: rows of 64 MB and more whose last words are fewer than a wave's lanes, and than a
+# token's slots: 513 and 1025 words of 16 bytes (on and off their grid; together on both sides of
+# 128 MB), rows of fewer words than slots, rows below 16 bytes (words of an element)
+TAILS = [(1100, 8, 4104, "bf16"), (2200, 8, 4104, "bf16"), (1100, 8, 4100, "bf16"),
+         (2200, 8, 4100, "bf16"), (1100, 8, 2052, "f32"), (2200, 8, 2049, "f32"),
+         (560, 8, 8200, "bf16"), (140, 66, 4104, "bf16"), (270, 66, 4098, "bf16"),
+         (1700, 66, 320, "bf16"), (3400, 66, 319, "bf16"), (180000, 8, 24, "bf16"),
+         (360000, 8, 23, "bf16"), (1050000, 8, 4, "bf16"), (700000, 8, 3, "f32")]
+
+
+@pytest.mark.parametrize("T,k,H,dtype", TAILS)
+def test_large_tails(T, k, H, dtype):
+    """Every word of every place, bit for bit, and none behind the last run."""
+    say(f"dispatch T={T} k={k} H={H} {dtype}")
+    m, g, E = moe(), torch.Generator("cuda").manual_seed(T + H), 80
+    ids = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)
+    ids[::3, k // 2:] = E                                    # another shard's
+    sid, _, npad = m.align_block(ids, E, 16)
+    n, S = int(npad), T * k
+    x = torch.randint(-2 ** 31, 2 ** 31 - 1, (T, H), generator=g, device="cuda").int()
+    x = (x >> 16).short().view(torch.bfloat16) if dtype == "bf16" else x.view(torch.float32)
+    out, ok = sentinel((sid.numel(), H), dtype)
+    rows, at = m.dispatch(x, ids, E, sid, npad, out=out)
+    torch.cuda.synchronize()
+    ok()
+    slot = sid[:n].long()
+    live = slot < S
+    ref = torch.full((S,), -1, dtype=torch.int32, device="cuda")
+    ref[slot[live]] = torch.arange(n, device="cuda", dtype=torch.int32)[live]
+    assert torch.equal(at.view(-1), ref)
+    want = bits(x)[slot.clamp(max=S - 1) // k]
+    want[~live] = 0
+    lost = int((bits(rows[:n]) != want).any(1).sum())
+    assert lost == 0, f"{lost} of {n} rows are not their token's"
+    assert bool((rows[n:] == 12345.0).all()), "rows behind the last run were written"
