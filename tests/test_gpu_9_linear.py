@@ -280,3 +280,56 @@ def test_offsets_past_32_bits():
     out = m.linear(x, w)
     check(x[-70:], w, None, "none", False, None, out[-70:], "bf16")
     assert bool((out[:-70] == 0).all())
+
+
+# fp32 tiles of all three sizes (the last two: 1024 x 4096 and 2048 x 4096 w rows are 256 of them)
+@pytest.mark.parametrize("T,N", [(300, 520), (1024, 4096), (2048, 4096)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_fp32_of_one_sign(T, N, gated):
+    """Positive operands and eight products a sum: nothing averages out, and fp32 has nearly all
+    bits of the sum. Of a product 2^-23 = 2 u may be left out; the first planes' products have 16
+    bits, so that eight of them between 1 and 4 add up exactly, and go with the rest (all other
+    pairs of planes, below 2^-6 of them, whose own steps count for 0.1 u) into one step of the
+    sum, 2 u whichever way it is rounded: 4.1 u of the sum. Planes cut off after 8 bits each leave
+    7.8 u out for operands of 1 + 2^-7 - 2^-23. The few-rows kernel takes the same planes in the
+    same order: the two differ by no more than 0.1 u in the mean (planes cut off: 0.6)."""
+    say(f"linear: fp32 of one sign T={T} N={N} gated={gated}")
+    m, g, K = moe(), gen(13), 8
+    n = N // 2 if gated else N
+
+    def run_(x, w):
+        if not gated:
+            return m.linear(x, w)
+        b = torch.cat([torch.zeros(n), torch.ones(n)]).cuda()     # gate times one
+        return m.linear(x, torch.cat([w[:n], torch.zeros_like(w[:n])]), b, gated=True)
+
+    worst = torch.full((1, K), 1 + 2.0 ** -7 - 2.0 ** -23, device="cuda")
+    some = [1 + torch.rand((r, K), generator=g).cuda() for r in (T, N)]
+    for x, w in ((worst.repeat(T, 1), worst.repeat(N, 1)), some):
+        ref = f64(x) @ f64(w[:n]).T
+        off = np.abs(f64(run_(x, w)) - ref).max() / U / ref.min()
+        say(f"    {off:.2f} u")
+        assert np.all(np.abs(f64(run_(x, w)) - ref) <= 4.1 * U * ref)
+    x, w = some
+    d = f64(run_(x, w)[:16]) - f64(run_(x[:16].contiguous(), w))
+    mean = float((d / (f64(x[:16]) @ f64(w[:n]).T)).mean()) / U
+    say(f"    mean difference from the few-rows kernel {mean:.3f} u")
+    assert abs(mean) <= 0.1
+
+
+@pytest.mark.parametrize("T,N", [(300, 520), (1024, 4096), (2048, 4096)])
+def test_fp32_ends_of_the_range(T, N):
+    """The largest fp32 values (which round to a bf16 infinity) stay what they are in tiles, and of
+    the smallest what is not below 2^-133."""
+    say(f"linear: ends of the fp32 range T={T} N={N}")
+    m, g, K = moe(), gen(14), 264
+    pick = torch.randint(0, K, (N,), generator=g)
+    w = torch.zeros((N, K), device="cuda")
+    w[torch.arange(N), pick] = 0.5
+    last = torch.randint(0x7f7f0000, 0x7f800000, (T, K), generator=g).int().cuda().view(torch.float32)
+    last[0, :2] = torch.tensor([3.4028234663852886e38, -3.4028234663852886e38])
+    last[1::2] *= -1
+    # (one such value a row: the others' products with 0 are zeros)
+    assert torch.equal(m.linear(last, w), last[:, pick.cuda()] * 0.5)
+    small = torch.randint(-(1 << 24) + 1, 1 << 24, (T, K), generator=g).float().cuda() * 2.0 ** -133
+    assert torch.equal(m.linear(small, 2 * w), small[:, pick.cuda()])
