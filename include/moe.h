@@ -725,13 +725,14 @@ enum {
  *                largest of their numbers.
  *  Bits are fixed for given sizes and types; a batch of another T may add a row's
  *  products in another order.
- *  Limits: 0 <= T < 2^24, 1 <= N < 2^24 (gated: 2^23), T * N < 2^37, K a multiple
- *  of 8 below 2^21, ldx a multiple of 8 (fp32: 4) in [K, 2^21), ldo and ldr at
- *  least N and below 2^31; x and w 16-byte aligned, bias, out and residual by
- *  their elements. Infinities and NaN in a row of x or w make the outputs that
- *  read it non-finite, and no others; with few rows fp32 values from 3.39e38 on
- *  (which round to a bf16 infinity) may count as infinities, and bits of one below
- *  2^-133 (the smallest bf16) do not count. T == 0 launches nothing.
+ *  Limits: 0 <= T < 2^24, 1 <= N < 2^24 (gated: 2^23), T * N < 2^37 (gated fp32
+ *  also ceil(T / 256) * ceil(N / 64) < 2^23), K a multiple of 8 below 2^21, ldx a
+ *  multiple of 8 (fp32: 4) in [K, 2^21), ldo and ldr at least N and below 2^31; x
+ *  and w 16-byte aligned, bias, out and residual by their elements. Infinities
+ *  and NaN in a row of x or w make the outputs that read it non-finite, and no
+ *  others; with few rows fp32 values from 3.39e38 on (which round to a bf16
+ *  infinity) may count as infinities, and bits of one below 2^-133 (the smallest
+ *  bf16) do not count. T == 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
 moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias, int activation,

@@ -718,6 +718,10 @@ static moe_status check_linear(int T, int N, int K, int gated, int dtype) {
   if (T < 0 || (long)T >= kMaxSlots || N < 1) return MOE_ERR_SHAPE;
   if ((long)N * (gated ? 2 : 1) >= kMaxLength) return MOE_ERR_SHAPE;
   if (K < 8 || K % 8 != 0 || K >= 1 << 21 || (long)T * N >= 1L << 37) return MOE_ERR_SHAPE;
+  // A launch counts its threads in 32 bits, and of the largest tiles gated fp32 ones hold the
+  // fewest outputs, 256 x 64 to 512 threads. (All others' 2^37 are 2^22 of them and their edges.)
+  if (gated && dtype == MOE_DTYPE_F32 && ((long)T + 255) / 256 * (((long)N + 63) / 64) >= 1 << 23)
+    return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 

@@ -274,3 +274,15 @@ def test_wrong_types_and_ranks_are_refused():
         m.dispatch([[0.0]], None, 4, None, None)
     with pytest.raises(TypeError, match="dtype"):
         m.layer_norm_backward(x.double(), x)
+
+
+def test_linear_gated_fp32_grid():
+    """Products whose tiles would be 2^23 workgroups of 512 threads, 2^32 in one dimension."""
+    big = dict(gated=1, odt=BF16, res=None, x=None)
+    for T, N in ((16384, (1 << 23) - 1), ((1 << 24) - 1, 8129), (16129, (1 << 23) - 1)):
+        call = dict(T=T, N=N, ldo=N, **big)
+        assert linear(dt=F32, **call) == SHAPE, (T, N)
+        assert linear(dt=BF16, **call) == NULL and linear(dt=F32, **{**call, "gated": 0}) == NULL
+        assert lib.moe_linear_workspace_bytes(T, N, 64, 1, F32) == 0
+    for T, N in ((16128, (1 << 23) - 1), ((1 << 24) - 1, 8128)):
+        assert linear(dt=F32, T=T, N=N, ldo=N, **big) == NULL, (T, N)
