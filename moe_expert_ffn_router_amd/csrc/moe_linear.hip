@@ -63,16 +63,25 @@ __device__ __forceinline__ float exp_of(float v) {
 __device__ __forceinline__ float logistic(float v) {
   return __builtin_amdgcn_rcpf(1.0f + exp_of(-v));
 }
-// v times the normal distribution at v. Its upper tail by Abramowitz and Stegun's 7.1.26,
-// erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2) with t = 1 / (1 + 0.3275911 x), x >= 0, off by
-// 1.5e-7 at most (2.5 u, half of that in the result): a tenth of the library function's code.
+// v times the normal distribution at v. Its tail at x = |v| / sqrt 2 is erfc(x) / 2 = t P(1 - t)
+// exp(-x^2), t = 1 / (1 + 0.49 x), with P of degree 8 fitted to what that leaves of erfc
+// for the least relative error, 2.3e-8 (0.4 u) for x to 9.4, where exp(-x^2) ends. In 1 - t, so
+// that its terms do not cancel near 0: the tail is off by (20 + v^2) u of itself at most, 7 of
+// them t's steps, and for |v| < 1 the result by 3.1 u of v at most, 0.6 u rms. (A polynomial of
+// degree 5 in t that holds to an absolute 1.5e-7: 5.5 u and 1.2 u, and 0.2 % of the tail at 4;
+// 4096 x 7168 x 4096 with gelu 208.7 us instead of 210.3.)
 __device__ __forceinline__ float gelu(float v) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(1.0f + 0.3275911f * x);
-  const float p =
-      t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f +
-                                                    t * (-1.453152027f + t * 1.061405429f))));
-  const float tail = 0.5f * p * exp_of(-x * x);
+  const float t = __builtin_amdgcn_rcpf(1.0f + 0.34648232278141387f * fabsf(v));
+  const float s = 1.0f - t;
+  float p = 0.084097139533734436f + s * -0.028645332902669907f;
+  p = -0.053465139120817184f + s * p;
+  p = -0.020093560218811035f + s * p;
+  p = -0.069017730653285980f + s * p;
+  p = 0.097168847918510437f + s * p;
+  p = 0.279573887586593628f + s * p;
+  p = -0.651405036449432373f + s * p;
+  p = 0.5f + s * p;
+  const float tail = t * p * __builtin_amdgcn_exp2f(v * (v * -0.72134752044448170f));
   return v * (v < 0.f ? tail : 1.0f - tail);
 }
 // The activation of all of a lane's values in one branch, not one a value: what is executed

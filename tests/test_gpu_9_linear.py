@@ -1,5 +1,7 @@
 """GPU parity of the matrix product with its epilogue against the fp64 oracle: every output within
 half a step of its type plus the fp32 arithmetic's own error."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -333,3 +335,28 @@ def test_fp32_ends_of_the_range(T, N):
     assert torch.equal(m.linear(last, w), last[:, pick.cuda()] * 0.5)
     small = torch.randint(-(1 << 24) + 1, 1 << 24, (T, K), generator=g).float().cuda() * 2.0 ** -133
     assert torch.equal(m.linear(small, 2 * w), small[:, pick.cuda()])
+
+
+@pytest.mark.parametrize("T", [1, 100])
+def test_gelu_of_one_value(T):
+    """GELU of exact products in fp32, also where it is the small difference of large terms. Its
+    tail, erfc(|v| / sqrt 2) / 2, is off by (20 + v^2) u of itself at most: the reciprocal and its
+    operand 3 u, which count 2.3 times; 1 - t 1 u; the polynomial's steps 7 u and fit 0.4; the
+    exponential 2 u, its argument v^2 u; two products 2 u. Below zero the result is v times that
+    (1 u more), above v times one less it (2 u)."""
+    say(f"linear: gelu T={T}")
+    m, g = moe(), gen(15)
+    v = torch.cat([12.5 * (2 * torch.rand(3000, generator=g) - 1),
+                   2 * torch.rand(3000, generator=g) - 1,
+                   10.0 ** (-30 * torch.rand(500, generator=g)),
+                   -10.0 ** (-30 * torch.rand(500, generator=g))]).cuda()
+    x, w = torch.zeros((T, 8), device="cuda"), torch.zeros((v.numel(), 8), device="cuda")
+    x[:, 0], w[:, 0] = 1, v
+    assert torch.equal(m.linear(x, w)[T // 2], v)
+    out, h = f64(m.linear(x, w, activation=m.ACT_GELU)), f64(v)
+    tail = 0.5 * np.vectorize(math.erfc)(np.abs(h) / math.sqrt(2))
+    ref = np.where(h < 0, h * tail, h * (1 - tail))
+    tol = np.abs(h) * (tail * (20 + h * h) + np.where(h < 0, tail, 2)) * U
+    worst = float((np.abs(out - ref) / tol).max())
+    say(f"    largest error {worst:.3f} of its bound")
+    assert worst <= 1
