@@ -308,8 +308,9 @@ struct Tile {
 // new registers, 184 copies a step with 256 of them to a wave: 1249 TFLOP/s for 8192^3
 // instead of 1331.) It knows nothing of the matrix instruction in here: what writes the sums
 // before the first and reads them after the last goes through settle(), and the operands are
-// registers that LDS reads fill (a vector instruction that wrote one would have to be two
-// states ahead; the compiled loops have none).
+// registers that LDS reads fill. A vector instruction that wrote one would have to be two states
+// ahead: the compiled loops have none, which tests/test_compiled_linear_cpu.py checks in the
+// library as built.
 __device__ __forceinline__ void mfma_in_place(f32x4& acc, const u32x4& a, const u32x4& b) {
   asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
