@@ -360,3 +360,37 @@ def test_gelu_of_one_value(T):
     worst = float((np.abs(out - ref) / tol).max())
     say(f"    largest error {worst:.3f} of its bound")
     assert worst <= 1
+
+
+# few rows of every size; every tile, whole K and K in parts; K past a chunk and a stage by 8 or more
+EXACT = [(1, 4100, 4104), (7, 300, 8), (9, 2048, 1000), (16, 2050, 7176), (29, 1001, 2056),
+         (64, 512, 520), (64, 2048, 7176), (70, 70, 8184), (300, 520, 4104), (700, 700, 8200),
+         (512, 4096, 1032), (1024, 4096, 1000), (3000, 1500, 2008), (2048, 4096, 1096),
+         (4096, 4099, 328)]
+
+
+@pytest.mark.parametrize("T,N,K", EXACT)
+@pytest.mark.parametrize("gated", [False, True])
+def test_bf16_whole_numbers(T, N, K, gated):
+    """Whole numbers to 8 in bf16: every sum stays below 64 K < 2^24 and is exact in fp32 in any
+    order, so that one k too few or too many shows. Gated: gate or up sums of K products, the
+    other one's of a single one, 2^22 at most together."""
+    say(f"linear: whole numbers T={T} N={N} K={K} gated={gated}")
+    m, g = moe(), torch.Generator("cuda").manual_seed(T + N + K)
+
+    def whole(rows):
+        return torch.randint(-8, 9, (rows, K), generator=g, device="cuda").bfloat16()
+
+    x, w = whole(T), whole(N)
+    ref = x.double() @ w.double().T
+    if not gated:
+        assert torch.equal(m.linear(x, w, dtype=torch.float32).double(), ref)
+        return
+    pick = torch.randint(0, K, (N,), generator=g, device="cuda")
+    one = torch.zeros_like(w)
+    one[torch.arange(N, device="cuda"), pick] = 1
+    ref *= x[:, pick].double()
+    assert float(ref.abs().max()) < 2 ** 24
+    for pair in ((w, one), (one, w)):
+        got = m.linear(x, torch.cat(pair), gated=True, dtype=torch.float32)
+        assert torch.equal(got.double(), ref)
