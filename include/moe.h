@@ -559,7 +559,8 @@ moe_status moe_ffn_intermediates(int T, int E, int H, int I, int k, int block_m,
  * full. Arithmetic and sums are fp32; each output is rounded once (RNE) from the
  * fp32 value, and sums run in a fixed order: equal calls give equal bits. Rows of
  * any length and alignment (of an element at least, MOE_ERR_ALIGN below that) are
- * taken; those that start at multiples of 16 bytes run fastest.
+ * taken, but for those of moe_linear's x and w; rows that start at multiples of 16
+ * bytes run fastest.
  */
 
 /*
@@ -729,10 +730,10 @@ enum {
  *  also ceil(T / 256) * ceil(N / 64) < 2^23), K a multiple of 8 below 2^21, ldx a
  *  multiple of 8 (fp32: 4) in [K, 2^21), ldo and ldr at least N and below 2^31; x
  *  and w 16-byte aligned, bias, out and residual by their elements. Infinities
- *  and NaN in a row of x or w make the outputs that read it non-finite, and no
- *  others; with few rows fp32 values from 3.39e38 on (which round to a bf16
- *  infinity) may count as infinities, and bits of one below 2^-133 (the smallest
- *  bf16) do not count. T == 0 launches nothing.
+ *  and NaN in a row of x or w make the sums that read it non-finite (infinite or
+ *  NaN), and no others; with few rows fp32 values from 3.39e38 on (which round to
+ *  a bf16 infinity) may count as infinities, and bits of one below 2^-133 (the
+ *  smallest bf16) do not count. T == 0 launches nothing.
  */
 size_t moe_linear_workspace_bytes(int T, int N, int K, int gated, int dtype);
 moe_status moe_linear(const void* x, size_t ldx, const void* w, const float* bias, int activation,

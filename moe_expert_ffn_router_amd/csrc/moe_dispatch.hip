@@ -40,7 +40,7 @@ static dim3 grid_of(long waves, int pieces = 1) {
 // Rows that together pass this are read and written around the caches: they leave nothing
 // there that a later kernel would find (the cache before HBM holds 256 MB). 268 MB of rows:
 // dispatch 72.7 us instead of 78.9, combine 52.0 instead of 56.9, its gradient 130 instead of
-// 140.
+// 140. The host knows T, k and H but not the ids: slots of another shard count as rows too.
 constexpr size_t kStreamBytes = (size_t)128 << 20;
 
 // How the rows of a call are copied: in words (U) of 16 bytes; where rows do not start at
@@ -301,7 +301,9 @@ template <int VEC, bool ANY, typename YT, typename IO>
 static void run_combine_backward(const CombineBackwardProblem& p, hipStream_t stream) {
   const dim3 grid = grid_of((long)p.T * p.k + (p.R + 7) / 8);
   // Eight vectors of a lane in flight for rows of more than four a lane: 32768 rows of 4096
-  // bf16 129.7 us instead of 135.4 with two; 2250 rows of 2048 bf16 8.9 instead of 8.4.
+  // bf16 129.7 us instead of 135.4 with two; 2250 rows of 2048 bf16 8.9 instead of 8.4. Shorter
+  // rows also where they pass kStreamBytes: 131072 of 1024 bf16 115.9 us instead of 146.8 with
+  // eight around the caches (65536 of 2048, the longest with two, 118.9 and 116.4).
   constexpr bool kStream = VEC > 1 && !ANY;
   const bool nt = kStream && (size_t)p.T * p.k * p.H * sizeof(YT) > kStreamBytes;
   if (p.H <= 256 * VEC)
@@ -344,9 +346,9 @@ hipError_t launch_dispatch(const DispatchProblem& p, hipStream_t stream) {
   using namespace dispatch;
   const int bytes = p.dtype == MOE_DTYPE_BF16 ? 2 : 4;
   const Lists l{p.topk_ids, p.sorted_ids, p.num_padded, p.slot_rows, p.T * p.k, p.E, p.R};
-  // Token by token from kTokenBytes on: the second launch costs 3 us. 65 MB of rows 20.7
-  // us instead of 21.4, 59 MB 17.7 instead of 18.4; 268 MB 78.9 instead of 90.8; 15 MB 10.5
-  // instead of 7.1.
+  // Token by token from kTokenBytes on (all slots counted, as above): the second launch costs
+  // 3 us. 65 MB of rows 20.7 us instead of 21.4, 59 MB 17.7 instead of 18.4; 268 MB 78.9
+  // instead of 90.8; 15 MB 10.5 instead of 7.1.
   constexpr size_t kTokenBytes = (size_t)64 << 20;
   const size_t all = (size_t)l.S * p.H * bytes;
   // P: what the kernels count rows' addresses in

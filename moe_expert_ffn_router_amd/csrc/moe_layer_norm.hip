@@ -255,8 +255,10 @@ __global__ __launch_bounds__(1024) void finish_kernel(const float* __restrict__ 
 // Calls f(W, NV) as compile-time constants for rows of H elements: up to 8 waves with a vector a
 // lane, as few as hold the row (of 4 and 8 alone 4096 x 2560 bf16 took 17.1 us forward and
 // 28.5 backward instead of 16.4 and 26.2). The longest rows of the backward pass (BACK) take 8
-// waves: 16 leave a wave 128 registers, from which some of a row spills (4096 x 16384 bf16 202
-// us instead of 149, 2048 x 16384 fp32 180 instead of 169).
+// waves: 16 leave a wave 128 registers, from which more of a row spills (4096 x 16384 bf16 202
+// us instead of 149, 2048 x 16384 fp32 180 instead of 169). fp32 rows past 8192 spill with 8
+// too, 26 registers of a lane, off the 16-byte grid 131 (2048 x 16383 195 us), bf16 ones there
+// 4 (4096 x 16383 185), and rows of 65 to 128 vectors off it 1.
 template <int V>
 struct Int {
   static constexpr int value = V;

@@ -1,8 +1,9 @@
 // Matrix product with its epilogue: out = residual + act(x w^T + bias), or gated
 // residual + act(x wg^T + bg) (x wu^T + bu), on the bf16 matrix cores with fp32 sums; fp32
-// operands enter exactly, as three bf16 planes each of which six products are taken. (The
-// fp32 matrix instructions run at a sixteenth of the bf16 rate, and are no closer: both
-// round as a chain of K additions does, 17 to 18 u rms at K = 4096.)
+// operands enter exactly, as three bf16 planes each, of whose nine products six are taken (the
+// other three are 2^-24 of the whole). (The fp32 matrix instructions run at a sixteenth of the
+// bf16 rate, and are no closer: both round as a chain of K additions does, 17 to 18 u rms at
+// K = 4096.)
 //
 // Few rows of x: K over the waves of a workgroup, which streams its w rows from HBM. Else
 // tiles of 32 NI w rows x 64 MI x rows, with K in parts over workgroups and a second kernel
@@ -11,10 +12,10 @@
 //
 // Measured (captured into a graph), bf16: 16 rows x gated 2048 x 7168 11.4 us = 5.2 TB/s of
 // weights, 1 x 4096 x 4096 7.1 us; 509 x 4100 x 4096 with gelu 29 us = 586 TFLOP/s (132 tiles of 256
-// CUs); 4096 x 7168 x 4096 187 us = 1286 TFLOP/s, with bias and residual 200 us; 8192^3 1397-1430
+// CUs); 4096 x 7168 x 4096 187 us = 1286 TFLOP/s, with bias and residual 200-208 us; 8192^3 1397-1430
 // TFLOP/s (the vendor library's plain product 1478-1550), where the chip's power and the LDS
 // (256 KB through it for 2048 cycles of products a stage) are the bounds. fp32: 16 x 4096 x
-// 4096 16 us = 4.1 TB/s, 2048 x 4096 x 4096 294-306 us = 225-234 TFLOP/s of the 420 that six
+// 4096 16 us = 4.1 TB/s, 2048 x 4096 x 4096 296-307 us = 224-232 TFLOP/s of the 420 that six
 // products leave.
 #include <algorithm>
 #include <type_traits>
@@ -722,7 +723,9 @@ struct TileCost {
 // in all, x comes from L2 at 140: 16 x gated 2048 x 7168 11.5 (tiles 14.5), 16 x 4096 x 4096 7.7
 // (10.9), 64 x 512 x 512 3.3 (4.7), but 64 x 7168 x 2048 14.5 (10.0). fp32: 2048 x 4096 x 4096 4 x 4
 // 306 (2 x 4 340, 1 x 2 434), 256 rows 2 x 4 in 4 53 (1 x 2 67), 300 x 512 x 512 1 x 2 in 4 8.5 (whole
-// 10.6), 16 x 4096 x 4096 few rows 15.6 (tiles 27).
+// 10.6), 16 x 4096 x 4096 few rows 15.6 (tiles 27). A CU counts as holding one tile at a time,
+// and tiles past 256 as a round more, as measured for the large ones; the small ones' LDS
+// leaves room for more (fp32 1 x 2: three, bf16 1 x 2: two), whose rounds were not measured.
 static const TileCost kTiles[] = {{1, 2, 3.3f, 0.21f, 0.255f}, {1, 4, 3.8f, 0.24f, 0.31f},
                                   {2, 4, 4.5f, 0.34f, 0.48f},  {2, 6, 5.0f, 0.46f, 0.68f},
                                   {2, 8, 5.5f, 0.57f, 0.86f},  {4, 8, 8.0f, 1.05f, 1.5f}};
